@@ -543,6 +543,149 @@ int zero1_step_dynamic_noalloc(const zero1_plan_t *plan, int32_t shard_begin, in
  * first). */
 int zero1_checksum(const void *data, int64_t nbytes, uint64_t *out, zero1_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a training block next to the optimizer step (no counterpart in
+ * the pages, which count a layer's activations, "CS336 Lecture 7: Parallelism
+ * 1", but hold no kernel): block norms with gate and residual scale, 8-bit
+ * activation checkpoints, and the weight gradient taken from a checkpoint and
+ * written where the step reads it, into a replica's flat gradient buffer.
+ *
+ * Conventions beyond those at the top of this file:
+ *  - A matrix is a pointer to its first element and `ld`, the elements from
+ *    one row to the next; columns are contiguous.  Outputs need ld >= columns;
+ *    inputs may have any ld >= 0 (0: the same row again).  With one row ld is
+ *    not used.  Rows of 16-byte aligned bases and strides, with columns a
+ *    multiple of 8, take the 128-bit path; anything else runs per element.
+ *  - dtype codes: ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32.  Arithmetic, statistics
+ *    and sums are fp32 (fused multiply-adds allowed here, unlike the optimizer
+ *    step); each output is rounded once, when it is stored.
+ *  - rows may be 0: forward calls do nothing, gradients that are sums over
+ *    rows get +0 (or stay, when accumulated into).
+ *  - Results do not depend on timing: no floating-point atomics, fixed
+ *    summation orders.
+ * ------------------------------------------------------------------------- */
+
+/* An 8-bit checkpoint of a [rows, cols] activation: e4m3 codes and one
+ * power-of-two scale for each row and 128 columns.  With E = exps[(j / 128) *
+ * ld_exps + t], the value of element (t, j) is codes[t * ld_codes + j] * 2^(E -
+ * 127), which bf16 and fp32 hold exactly.  E - 127 is the least exponent in
+ * [-119, 119] with max|x| <= 448 * 2^(E - 127) over the row's 128 columns (the
+ * last block may be shorter); magnitudes above 448 * 2^119 saturate there.  A
+ * block that held an Inf or a NaN has E = 255 and zero codes and stands for
+ * NaN, so an overflow in a saved activation reaches the gradients and through
+ * them the step's overflow flag.
+ *  codes:    device, 16-byte aligned; ld_codes >= cols rounded up to 128, a
+ *            multiple of 16; columns from cols up to that multiple of 128 are
+ *            written as 0;
+ *  exps:     device, 16-byte aligned; ld_exps >= rows rounded up to 128, a
+ *            multiple of 16.  Bytes from `rows` on need no particular value,
+ *            and packing writes none of them. */
+typedef struct zero1_checkpoint8 {
+    uint8_t *codes;
+    uint8_t *exps;
+    int64_t ld_codes, ld_exps;
+    int64_t rows, cols;
+} zero1_checkpoint8_t;
+
+/* Pack x (dtype, [ckpt->rows, ckpt->cols]) into *ckpt / unpack *ckpt into out.
+ * Codes are round to nearest even.  Element-wise, so the result is unique.
+ * Any buffer may be pinned host memory. */
+int zero1_checkpoint_pack(const void *x, int64_t ld_x, int32_t dtype, const zero1_checkpoint8_t *ckpt,
+                          zero1_stream_t stream);
+int zero1_checkpoint_unpack(const zero1_checkpoint8_t *ckpt, void *out, int64_t ld_out, int32_t dtype,
+                            zero1_stream_t stream);
+
+/* Block norms with gate and residual scale.  For a block's output y and the
+ * residual stream x, row by row (D = cols, a = residual_scale):
+ *   yh = y * rstd_post,  rstd_post = 1 / sqrt(mean(y^2) + eps)    [yh = y without the norm after the block]
+ *   u  = w_post * yh
+ *   r  = x + a * g * u          (the new residual stream)
+ *   rh = r * rstd_pre,   rstd_pre = 1 / sqrt(mean(r^2) + eps)
+ *   h  = w_pre * rh             (the next block's input)          [absent without the norm before it]
+ * g is 1, or the gate, or its logistic sigmoid; the gate is one value per
+ * channel [D], one per token [rows] or a [rows, D] matrix.  r enters its norm
+ * unrounded.  1 <= cols <= ZERO1_BLOCK_NORM_MAX_COLS (ERANGE above). */
+#define ZERO1_BLOCK_NORM_MAX_COLS 16384
+#define ZERO1_GATE_NONE 0
+#define ZERO1_GATE_CHANNEL 1
+#define ZERO1_GATE_TOKEN 2
+#define ZERO1_GATE_FULL 3
+#define ZERO1_GATE_LINEAR 0
+#define ZERO1_GATE_SIGMOID 1
+typedef struct zero1_block_norm {
+    int64_t rows, cols;
+    float eps;            /* finite, > 0 */
+    float residual_scale; /* a, finite */
+    int32_t act_dtype;    /* y, h, dh, dy */
+    int32_t res_dtype;    /* x, r, dr, dx; fp32 whenever act_dtype is */
+    int32_t param_dtype;  /* w_post, w_pre */
+    int32_t gate_dtype;   /* gate; also dgate of a [rows, D] gate */
+    int32_t grad_dtype;   /* dw_post, dw_pre, dgate of a channel or token gate */
+    int32_t gate_kind;    /* ZERO1_GATE_NONE .. ZERO1_GATE_FULL */
+    int32_t gate_act;     /* ZERO1_GATE_LINEAR or ZERO1_GATE_SIGMOID */
+    int32_t accumulate;   /* backward: add to dw_post, dw_pre and a channel dgate instead of overwriting */
+} zero1_block_norm_t;
+
+/* Forward.  w_post NULL: no norm after the block (rstd_post NULL).  w_pre
+ * NULL: no norm before the next one (h, rstd_pre, r8 NULL).  y8 and r8, when
+ * not NULL, get checkpoints of yh and rh - what the backward pass reads in
+ * place of y and r, half the bytes - in the same pass over the data.  r may
+ * be x (same pointer, type and stride); other buffers must not overlap. */
+typedef struct zero1_block_norm_forward {
+    const void *y, *x, *w_post, *w_pre, *gate;
+    void *r, *h;
+    float *rstd_post, *rstd_pre; /* [rows] */
+    const zero1_checkpoint8_t *y8, *r8;
+    int64_t ld_y, ld_x, ld_gate, ld_r, ld_h; /* ld_gate: [rows, D] gates; elements between tokens for a token gate */
+} zero1_block_norm_forward_t;
+int zero1_block_norm_forward(const zero1_block_norm_t *cfg, const zero1_block_norm_forward_t *io,
+                             zero1_stream_t stream);
+
+/* Backward, from the gradients dh of h and dr of r (dr NULL: none):
+ *   d  = dr + rstd_pre * (w_pre dh - rh * mean(w_pre dh rh)),   dx = d
+ *   dw_pre  = sum over rows of dh * rh
+ *   dgate   = sum of a * d * u over what the gate was broadcast over, times
+ *             s (1 - s) for a sigmoid gate
+ *   dw_post = sum over rows of a g d yh
+ *   dy = rstd_post * (w_post a g d - yh * mean(w_post a g d yh))
+ * The saved activations come either as y (act_dtype) and r (res_dtype) or as
+ * the checkpoints y8 and r8 of the forward call, each on its own.  Without the
+ * norm after the block y (or y8, then a checkpoint of y itself) is needed for
+ * dgate only.  dw_post, dw_pre and dgate may be views into a replica's flat
+ * gradient buffer at any element offset; any of them may be NULL when it is
+ * not wanted.  dx may be dr and dy may be dh (same pointer, type and stride).
+ * workspace: device, 16-byte aligned, zero1_block_norm_workspace bytes
+ * (scratch). */
+typedef struct zero1_block_norm_backward {
+    const void *dh, *dr, *y, *r, *w_post, *w_pre, *gate;
+    const float *rstd_post, *rstd_pre;
+    const zero1_checkpoint8_t *y8, *r8;
+    void *dy, *dx, *dw_post, *dw_pre, *dgate;
+    int64_t ld_dh, ld_dr, ld_y, ld_r, ld_gate, ld_dy, ld_dx, ld_dgate;
+} zero1_block_norm_backward_t;
+int zero1_block_norm_workspace(const zero1_block_norm_t *cfg, int64_t *bytes);
+int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const zero1_block_norm_backward_t *io, void *workspace,
+                              int64_t workspace_bytes, zero1_stream_t stream);
+
+/* The weight gradient of a projection p = X W^T from the 8-bit checkpoint of
+ * its input:
+ *   dw[n, k] (+)= col_scale[k] * sum_t dy[t, n] * x8[t, k]
+ * dy: device bf16 [x8->rows, n]; x8: the checkpoint, [rows, k = x8->cols];
+ * col_scale: device, k values of scale_dtype, or NULL (1) - with the
+ * checkpoint of rh and col_scale = w_pre this is the gradient for X = h, which
+ * then need not be kept; dw: device [n, k] of out_dtype, for instance a view
+ * into a replica's flat gradient buffer at any element offset; accumulate != 0
+ * adds to it (rounded once).  The checkpoint's values are exact in bf16; the
+ * products are summed in fp32 on the tensor cores.  Device memory only.
+ * workspace: device, 128-byte aligned, zero1_weight_grad_workspace bytes for
+ * the same rows, n, k, dy and ld_dy (fp32 partial sums where the rows are
+ * split over blocks; an aligned copy of dy when its rows are not on 16-byte
+ * boundaries). */
+int zero1_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy, int64_t *bytes);
+int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const zero1_checkpoint8_t *x8, const void *col_scale,
+                      int32_t scale_dtype, void *dw, int64_t ld_dw, int32_t out_dtype, int32_t accumulate,
+                      void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
+
 /* Text of a status code. */
 const char *zero1_strerror(int code);
 

@@ -50,3 +50,15 @@ from ._lib import (  # noqa: F401
     debug_last_launch,
 )
 from .host_stream import HostStreamedStep  # noqa: E402,F401
+from .block import (  # noqa: E402,F401
+    BlockNorm,
+    Checkpoint8,
+    new_checkpoint,
+    zero1_block_norm_backward,
+    zero1_block_norm_forward,
+    zero1_block_norm_workspace,
+    zero1_checkpoint_pack,
+    zero1_checkpoint_unpack,
+    zero1_weight_grad,
+    zero1_weight_grad_workspace,
+)

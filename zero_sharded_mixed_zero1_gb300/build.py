@@ -25,7 +25,7 @@ def _nvcc() -> str:
 
 def _sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-            if f.endswith((".cu", ".cpp", ".h"))] + [os.path.join(INCLUDE, "zero1.h")]
+            if f.endswith((".cu", ".cuh", ".cpp", ".h"))] + [os.path.join(INCLUDE, "zero1.h")]
 
 
 def is_stale() -> bool:

@@ -1,0 +1,228 @@
+// zero1_block.cuh - helpers shared by the training-block operators: typed
+// 8-element loads and stores, the 8-bit checkpoint code, and the host-side
+// checks of matrices and checkpoints (library-internal).
+#pragma once
+
+#include "zero1_checks.h"
+#include "zero1_device.cuh"
+
+namespace {
+
+constexpr int kQBlock = 128;  // columns that share a checkpoint scale
+constexpr int kMinE = 8;      // biased exponents of the scales: 127 - 119 .. 127 + 119
+constexpr int kMaxE = 246;
+constexpr int kNanE = 255;
+
+// ------------------------------------------------------- typed elements ----
+
+__device__ __forceinline__ float ld1(const uint16_t *p) { return bf_one(*p); }
+__device__ __forceinline__ float ld1(const float *p) { return *p; }
+__device__ __forceinline__ void st1(uint16_t *p, float x) { *p = to_bf16(x); }
+__device__ __forceinline__ void st1(float *p, float x) { *p = x; }
+
+// Eight consecutive elements as they lie in memory: one 16-byte access for
+// bf16, two for fp32.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    uint4 q;
+    __device__ __forceinline__ void load(const uint16_t *p) { q = ld_stream_u4(p); }
+    __device__ __forceinline__ void get(float f[8]) const { unpack8(q, f); }
+    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldcs(reinterpret_cast<const float4 *>(p));
+        b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float f[8]) const
+    {
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+};
+
+__device__ __forceinline__ void store8(uint16_t *p, const float f[8])
+{
+    __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                    pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+}
+__device__ __forceinline__ void store8(float *p, const float f[8])
+{
+    st_stream(p, f[0], f[1], f[2], f[3]);
+    st_stream(p + 4, f[4], f[5], f[6], f[7]);
+}
+
+// One value of a small vector (weights, gates) whose type is only known at
+// run time; the branch is the same for the whole grid.
+__device__ __forceinline__ float ld_param(const void *p, int f32, int64_t i)
+{
+    return f32 ? __ldg(static_cast<const float *>(p) + i) : bf_one(__ldg(static_cast<const uint16_t *>(p) + i));
+}
+
+// -------------------------------------------------- 8-bit checkpoint code --
+
+// Largest magnitude seen, as the bits of |x|: integer order is the order of
+// the magnitudes, with Inf and NaN above every finite value.
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Biased scale exponent of a block from its largest magnitude 1.m * 2^(b-127):
+// 448 = 1.75 * 2^8, so b - 8, one more if the mantissa is above 1.75.
+__device__ __forceinline__ int scale_exp(uint32_t amax)
+{
+    const int e = (int)(amax >> 23) - 8 + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return amax >= 0x7f800000u ? kNanE : min(max(e, kMinE), kMaxE);
+}
+
+// 2^(127 - E), the factor that brings a block's values to the codes' range
+// (0 for a block that stands for NaN, whose codes are 0).
+__device__ __forceinline__ float scale_inv(int E) { return E == kNanE ? 0.f : __uint_as_float((uint32_t)(254 - E) << 23); }
+
+// 2^(E - 127), the factor from codes to values (NaN for 255).
+__device__ __forceinline__ float scale_of(int E)
+{
+    return __uint_as_float(E == kNanE ? 0x7fc00000u : (uint32_t)E << 23);
+}
+
+// Two values to two e4m3 codes, round to nearest even, saturating.
+__device__ __forceinline__ uint32_t code2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four codes of a scaled block; `ok` false for a block that stands for NaN.
+__device__ __forceinline__ uint32_t code4(float a, float b, float c, float d, float inv, bool ok)
+{
+    const uint32_t q = code2(__fmul_rn(a, inv), __fmul_rn(b, inv)) |
+                       (code2(__fmul_rn(c, inv), __fmul_rn(d, inv)) << 16);
+    return ok ? q : 0u;
+}
+
+// Two codes to two values (an fp16 holds every e4m3 value exactly).
+__device__ __forceinline__ float2 value2(uint16_t q)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(q));
+    float2 f;
+    asm("{ .reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h; }"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(h));
+    return f;
+}
+
+__device__ __forceinline__ void values8(uint2 q, float scale, float f[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? q.x : q.y;
+        const float2 v = value2((uint16_t)(k & 1 ? w >> 16 : w & 0xffffu));
+        f[2 * k] = __fmul_rn(v.x, scale);
+        f[2 * k + 1] = __fmul_rn(v.y, scale);
+    }
+}
+
+__device__ __forceinline__ uint32_t max16(uint32_t a)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+__device__ __forceinline__ uint32_t max32(uint32_t a) { return __reduce_max_sync(0xffffffffu, a); }
+
+struct Ckpt {
+    uint8_t *codes, *exps;
+    int64_t ld_codes, ld_exps;
+};
+
+// ------------------------------------------------------------ host checks --
+
+int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int esize(int dtype) { return dtype == ZERO1_DTYPE_F32 ? 4 : 2; }
+
+int check_dtype(int32_t d, const char *call, const char *what)
+{
+    if (d != ZERO1_DTYPE_BF16 && d != ZERO1_DTYPE_F32)
+        return z1_fail(ZERO1_EINVAL, "%s: unknown %s %d", call, what, d);
+    return ZERO1_OK;
+}
+
+// A matrix of a call: `rows` rows of `width` bytes, `pitch` bytes apart.
+struct Mat {
+    const void *p;
+    int64_t rows, width, pitch;
+    const char *what;
+};
+
+Mat mat(const void *p, int64_t rows, int64_t cols, int64_t ld, int es, const char *what)
+{
+    return Mat{p, rows, cols * es, (rows > 1 ? ld : cols) * es, what};
+}
+
+// Whether two matrices share a byte.  Of equal pitch they may be interleaved
+// (column ranges of one wider matrix).
+bool mats_overlap(const Mat &a, const Mat &b)
+{
+    if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const Extent ea{a.p, (a.rows - 1) * a.pitch + a.width, ""}, eb{b.p, (b.rows - 1) * b.pitch + b.width, ""};
+    if (!overlap(ea, eb)) return false;
+    if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch && a.pitch > 0) {
+        const int64_t p = a.pitch;
+        int64_t d = ((intptr_t)b.p - (intptr_t)a.p) % p;
+        if (d < 0) d += p;
+        return !(d >= a.width && d + b.width <= p);
+    }
+    return true;
+}
+
+// A matrix argument: present, aligned to its elements, a stride that fits.
+int check_mat(const Mat &m, int es, bool out, const char *call)
+{
+    if (m.rows == 0) return ZERO1_OK;
+    if (!m.p) return z1_fail(ZERO1_EINVAL, "%s: %s is NULL", call, m.what);
+    if (m.pitch < 0 || (out && m.pitch < m.width))
+        return z1_fail(ZERO1_EINVAL, "%s: %s: row stride of %lld elements", call, m.what, (long long)(m.pitch / es));
+    if (m.rows > 1 && m.pitch > INT64_MAX / m.rows)
+        return z1_fail(ZERO1_ERANGE, "%s: %s: size overflows", call, m.what);
+    return check_natural(m.p, es, m.what);
+}
+
+int check_ckpt(const zero1_checkpoint8_t *c, const char *call, const char *what)
+{
+    if (!c) return z1_fail(ZERO1_EINVAL, "%s: %s is NULL", call, what);
+    if (c->rows < 0 || c->cols < 1)
+        return z1_fail(ZERO1_EINVAL, "%s: %s: %lld rows, %lld columns", call, what, (long long)c->rows,
+                       (long long)c->cols);
+    if (c->rows > (INT64_C(1) << 40) || c->cols > (INT64_C(1) << 40))
+        return z1_fail(ZERO1_ERANGE, "%s: %s: size not supported", call, what);
+    if (c->rows == 0) return ZERO1_OK;
+    if (!c->codes || !c->exps) return z1_fail(ZERO1_EINVAL, "%s: %s: NULL codes or exps", call, what);
+    if (((uintptr_t)c->codes | (uintptr_t)c->exps | (uintptr_t)c->ld_codes | (uintptr_t)c->ld_exps) & 15)
+        return z1_fail(ZERO1_EALIGN, "%s: %s: codes, exps and their strides must be multiples of 16 bytes", call, what);
+    if (c->ld_codes < round_up(c->cols, kQBlock) || c->ld_exps < round_up(c->rows, kQBlock))
+        return z1_fail(ZERO1_EINVAL, "%s: %s: strides %lld, %lld are too short", call, what, (long long)c->ld_codes,
+                       (long long)c->ld_exps);
+    if (c->ld_codes > INT64_MAX / c->rows || c->ld_exps > INT64_MAX / (round_up(c->cols, kQBlock) / kQBlock))
+        return z1_fail(ZERO1_ERANGE, "%s: %s: size overflows", call, what);
+    return ZERO1_OK;
+}
+
+Mat codes_mat(const zero1_checkpoint8_t *c, const char *what)
+{
+    return c ? Mat{c->codes, c->rows, round_up(c->cols, kQBlock), c->ld_codes, what} : Mat{nullptr, 0, 0, 0, what};
+}
+Mat exps_mat(const zero1_checkpoint8_t *c, const char *what)
+{
+    return c ? Mat{c->exps, round_up(c->cols, kQBlock) / kQBlock, c->rows, c->ld_exps, what}
+             : Mat{nullptr, 0, 0, 0, what};
+}
+
+// Rows that the 128-bit path can address.
+bool vec_ok(const Mat &m) { return !m.p || ((((uintptr_t)m.p) | (uintptr_t)m.pitch) & 15) == 0; }
+
+}  // namespace
