@@ -562,3 +562,8 @@ def test_pinned_host_checkpoint(cuda_device):
     codes, exps = ref.pack(x.double())
     assert torch.equal(k.codes, codes) and torch.equal(out.double().cpu(), ref.values(codes, exps, 1000))
     assert np.array_equal(k.exps[:, :33].numpy(), exps.t().numpy())
+
+
+def test_no_wait_ran_out(cuda_device):
+    """The staged kernel's bounded waits all completed in the tests above."""
+    assert z.zero1_device_status() == 0

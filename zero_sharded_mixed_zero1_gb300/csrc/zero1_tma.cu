@@ -2,6 +2,7 @@
 // Memory Accelerator (bulk copies counted on mbarriers), kept to reproduce
 // the design comparison with the direct loads of zero1_fused.cu.
 
+#include "zero1_async.cuh"
 #include "zero1_device.cuh"
 #include "zero1_checks.h"
 
@@ -22,65 +23,8 @@ namespace {
 // gains nothing from the extra pass through shared memory), so the fused step
 // does not use it; it is kept so the comparison can be reproduced.
 
-__device__ uint32_t g_zero1_status;  // bit 0: a bounded wait ran out
-
-constexpr uint64_t kWaitNs = 1000000000ull;  // 1 s
 constexpr int kTmaConsumers = 256;           // 8 consumer warps
 constexpr int kTmaThreads = kTmaConsumers + 32;
-
-__device__ __forceinline__ uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ void mbar_init(uint64_t *b, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint64_t *b, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t *b)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(smem_u32(b)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-__device__ __forceinline__ uint64_t global_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Wait for the phase of the given parity; false (and the status bit set)
-// if it has not completed within limit_ns of %globaltimer, or within
-// kWaitPolls polls should the timer not advance.
-constexpr uint64_t kWaitPolls = 1ull << 24;
-
-__device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, uint64_t limit_ns = kWaitNs)
-{
-    if (mbar_try(b, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (uint64_t polls = 1; !mbar_try(b, parity); ++polls) {
-        if (global_ns() - t0 > limit_ns || polls >= kWaitPolls) {
-            atomicOr(&g_zero1_status, 1u);
-            return false;
-        }
-    }
-    return true;
-}
 
 // Self-test of the bounded wait: a barrier that expects two arrivals gets
 // one, so its phase never completes; the wait must give up after limit_ns,
@@ -94,15 +38,6 @@ __global__ void k_wait_selftest(uint64_t limit_ns, uint32_t *gave_up)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     mbar_arrive(&bar);
     *gave_up = mbar_wait(&bar, 0, limit_ns) ? 0u : 1u;
-}
-
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
 }
 
 // Tile of T elements (E = T / 256 per consumer thread); S stages in the ring.
@@ -314,11 +249,10 @@ extern "C" int zero1_step_tma(const zero1_plan_t *plan, int32_t shard_begin, int
 extern "C" int zero1_device_status(uint32_t *status, int32_t clear)
 {
     if (!status) return z1_fail(ZERO1_EINVAL, "device status: out is NULL");
-    cudaError_t e = cudaMemcpyFromSymbol(status, g_zero1_status, sizeof(uint32_t));
-    if (e == cudaSuccess && clear) {
-        const uint32_t zero = 0;
-        e = cudaMemcpyToSymbol(g_zero1_status, &zero, sizeof(uint32_t));
-    }
+    uint32_t other = 0;
+    cudaError_t e = async_status(status, clear);
+    if (e == cudaSuccess) e = (cudaError_t)z1_weight_grad_status(&other, clear);
+    *status |= other;
     if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "device status: %s", cudaGetErrorString(e));
     return ZERO1_OK;
 }

@@ -1,63 +1,546 @@
 // zero1_weight_grad.cu - the weight gradient of a projection, taken straight
-// from the 8-bit checkpoint of its input.
+// from the 8-bit checkpoint of its input, on the tensor cores.
 
+#include <cuda.h>
+
+#include "zero1_async.cuh"
 #include "zero1_block.cuh"
 
 namespace {
 
-constexpr int kTile = 64, kDeep = 16;
+// dw[n, k] = c[k] * sum_t dy[t, n] * x8[t, k].
+//
+// The contraction runs over the rows t of both operands, so both are "M/N
+// major": TMA brings dy as it lies in memory into swizzled shared memory,
+// which is the layout the MMA reads for its B operand.  x8 becomes the A
+// operand: a code is 8 bits of a bf16 (sign, exponent, mantissa) 120 binades
+// too low, so shifting it into place and multiplying by 2^(e + 120) gives the
+// exact value; eight warps do that for 16-bit pairs of rows and write A into
+// tensor memory, where it needs no second pass through shared memory.  A
+// checkpoint block is 128 columns, which is one CTA's share of the tile, so
+// each row has one scale per CTA.
+//
+// Two CTAs share a 256 (k) x 256 (n) tile: each holds 128 rows of A and of
+// the accumulator in its tensor memory and loads half of B, 24 KB per 64 rows
+// of the contraction where a CTA alone would load 40.  Products are exact in
+// fp32; sums are fp32 in the accumulator.
+//
+// Roles (16 warps): warp 0 loads, warp 1 of the leading CTA issues the MMAs,
+// warps 4-11 convert (two sets of four take alternate stages), warps 12-15
+// store the result.
 
-// dw[n, k] = c[k] * sum_t dy[t, n] * x8[t, k]: 64 x 64 outputs per block,
-// 4 x 4 per thread, 16 rows of dy and x at a time in shared memory.
-template <class TO>
-__global__ void __launch_bounds__(256)
-k_weight_grad(const uint16_t *__restrict__ dy, int64_t ld_dy, int64_t T, int64_t N, int64_t K, const Ckpt x8,
-              const void *scale, int scale_f32, TO *__restrict__ dw, int64_t ld_dw, int accumulate)
+constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
+constexpr int kDeep = 64;                  // rows of the contraction per stage
+constexpr int kStages = 8;
+constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;
+constexpr int kStageBytes = kBBytes + kXBytes;
+constexpr int kWgThreads = 512;
+constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
+
+struct WgBars {
+    uint64_t full[kStages], afull[kStages], empty[kStages], dfull, dempty;
+    uint32_t tmem;
+};
+constexpr int kWgSmem = 1024 + kStages * kStageBytes + kStages * kDeep + (int)sizeof(WgBars);
+static_assert(kWgSmem <= 227 * 1024, "shared memory of a block");
+static_assert(kTmemA + kStages * kTmemAStage <= kTmemCols, "tensor memory");
+
+struct Wg {
+    int64_t T, N, K;
+    int tiles_k, tiles_n, splits, kblocks, per_split;  // kblocks: stages of the whole contraction
+    const uint8_t *exps;
+    int64_t ld_exps;
+    const void *scale;
+    int scale_f32;
+    void *dw;
+    int64_t ld_dw;
+    int out_f32, accumulate, pairs;  // pairs: two outputs of a row per store
+    float *part;                     // splits > 1: [splits][N][ld_part]
+    int64_t ld_part;
+};
+
+// ------------------------------------------------------------- tcgen05 -----
+
+__device__ __forceinline__ void tc_alloc(uint32_t *slot)
 {
-    __shared__ float a[kDeep][kTile], b[kDeep][kTile];
-    const int64_t n0 = (int64_t)blockIdx.x * kTile, k0 = (int64_t)blockIdx.y * kTile;
-    const int tn = threadIdx.x / 16 * 4, tk = threadIdx.x % 16 * 4;
-    float acc[4][4] = {};
-    for (int64_t t0 = 0; t0 < T; t0 += kDeep) {
-        for (int q = threadIdx.x; q < kDeep * kTile; q += 256) {
-            const int t = q / kTile, c = q % kTile;
-            const bool in = t0 + t < T;
-            a[t][c] = in && n0 + c < N ? bf_one(dy[(t0 + t) * ld_dy + n0 + c]) : 0.f;
-            float v = 0.f;
-            if (in && k0 + c < K) {
-                const float2 f = value2(x8.codes[(t0 + t) * x8.ld_codes + k0 + c]);
-                v = f.x * scale_of(x8.exps[(k0 + c) / kQBlock * x8.ld_exps + t0 + t]);
-            }
-            b[t][c] = v;
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tc_free(uint32_t base)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemCols));
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// D (both CTAs' tensor memory) (+)= A (tensor memory) * B (shared memory).
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+
+// Arrive on this barrier of both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// 16 lanes x 128 bits, four times: r[2j], r[2j + 1] are lanes l / 4 and 8 + l / 4,
+// column 4 j + l % 4.
+__device__ __forceinline__ void tc_store(uint32_t addr, const uint32_t r[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 accumulator columns of this thread's lane.
+__device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t r[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Descriptor of a B tile: 128-byte swizzle, 64 columns x kDeep rows per TMA
+// box (kDeep * 128 bytes from one 64-column group to the next), 8 rows per
+// 1024-byte group.
+__device__ __forceinline__ uint64_t b_desc(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)((kDeep * 128) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// Instruction descriptor: fp32 accumulator, bf16 operands, B along N in
+// memory, M = 256 (both CTAs), N = 256.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kTileN / 8) << 17) |
+                            ((uint32_t)(kTileK / 16) << 24);
+
+// ------------------------------------------------------------- clusters ----
+
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the leading CTA's copy of a barrier.
+__device__ __forceinline__ void arrive_leader(uint64_t *bar)
+{
+    asm volatile(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a]; }" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+// A bounded wait of a whole warp on a barrier that either CTA may arrive on.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+{
+    bool ok = mbar_wait_cluster(bar, parity);
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// ----------------------------------------------------------- conversion ----
+
+__device__ __forceinline__ void ldmatrix_t(uint32_t addr, uint32_t r[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// bf16 factors of one row's scale E = e + 127: 2^(e + 120) up to e = 7, the
+// rest of the binades in a second factor; rows past the end are 0.
+__device__ __forceinline__ uint32_t factor1(int E, bool in)
+{
+    return !in ? 0u : E == kNanE ? 0x7fc0u : (uint32_t)(min(E, 134) + 120) << 7;
+}
+__device__ __forceinline__ uint32_t factor2(int E) { return (uint32_t)(127 + (E == kNanE ? 0 : max(E - 134, 0))) << 7; }
+
+// ----------------------------------------------------------------- kernel --
+
+struct Item {
+    int n0, k0, kb0, kb1, split;
+};
+
+// Tiles run in bands of eight along k, so that the pairs of CTAs at work at
+// one time share few columns of both operands (they meet in L2).
+__device__ __forceinline__ Item item_of(const Wg &a, int i)
+{
+    const int tiles = a.tiles_k * a.tiles_n;
+    const int split = i / tiles, t = i % tiles;
+    constexpr int kBand = 8;
+    const int per = kBand * a.tiles_n, band = t / per, in = t % per;
+    const int width = min(kBand, a.tiles_k - band * kBand);
+    Item o;
+    o.k0 = (band * kBand + in % width) * kTileK;
+    o.n0 = in / width * kTileN;
+    o.split = split;
+    o.kb0 = split * a.per_split;
+    o.kb1 = min(o.kb0 + a.per_split, a.kblocks);
+    return o;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
+k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const Wg a)
+{
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t *s_exps = smem + kStages * kStageBytes;
+    WgBars &bar = *reinterpret_cast<WgBars *>(s_exps + kStages * kDeep);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.afull[s], 8);   // four converting warps of each CTA
+            mbar_init(&bar.empty[s], 1);
         }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < kDeep; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[t][tn + i], b[t][tk + j], acc[i][j]);
-        __syncthreads();
+        mbar_init(&bar.dfull, 1);
+        mbar_init(&bar.dempty, 8);  // four storing warps of each CTA
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t n = n0 + tn + i, k = k0 + tk + j;
-            if (n >= N || k >= K) continue;
-            TO *o = dw + n * ld_dw + k;
-            float v = acc[i][j];
-            if (scale) v *= ld_param(scale, scale_f32, k);
-            st1(o, accumulate ? ld1(o) + v : v);
+    if (warp == 2) tc_alloc(&bar.tmem);
+    tc_before();
+    __syncthreads();
+    cluster_sync();
+    tc_after();
+    const uint32_t tmem = bar.tmem;
+    const int items = a.tiles_k * a.tiles_n * a.splits;
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int i = first; i < items && ok; i += step) {
+                const Item w = item_of(a, i);
+                const int64_t block = min((int64_t)(w.k0 / kQBlock) + rank, (a.K - 1) / kQBlock);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (it >= kStages && !(ok = mbar_wait_cluster(&bar.empty[s], (it / kStages - 1) & 1))) break;
+                    unsigned char *b = smem + s * kStageBytes;
+                    mbar_expect_tx(&bar.full[s], kStageBytes + kDeep);
+                    const int n = w.n0 + (int)rank * (kTileN / 2);
+                    tma_2d(b, &map_dy, n, kb * kDeep, &bar.full[s]);
+                    tma_2d(b + kBBytes / 2, &map_dy, n + 64, kb * kDeep, &bar.full[s]);
+                    tma_2d(b + kBBytes, &map_x, w.k0 + (int)rank * kQBlock, kb * kDeep, &bar.full[s]);
+                    bulk_load(s_exps + s * kDeep, a.exps + block * a.ld_exps + (int64_t)kb * kDeep, kDeep, &bar.full[s]);
+                }
+            }
+            // the last copies must land before the block may exit
+            for (uint32_t q = it > kStages ? it - kStages : 0; q < it; ++q)
+                mbar_wait(&bar.full[q % kStages], (q / kStages) & 1);
         }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            uint32_t it = 0, tile = 0;
+            bool ok = true;
+            for (int i = first; i < items && ok; i += step, ++tile) {
+                const Item w = item_of(a, i);
+                if (tile > 0 && !(ok = mbar_wait_cluster(&bar.dempty, (tile - 1) & 1))) break;
+                tc_after();
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (it / kStages) & 1;
+                    if (!(ok = mbar_wait_cluster(&bar.full[s], ph) && mbar_wait_cluster(&bar.afull[s], ph))) break;
+                    tc_after();
+                    const uint32_t b = smem_u32(smem + s * kStageBytes);
+#pragma unroll
+                    for (int j = 0; j < kDeep / 16; ++j)
+                        tc_mma(tmem, tmem + kTmemA + s * kTmemAStage + 8 * j, b_desc(b + j * 2048), kIdesc,
+                               kb > w.kb0 || j > 0);
+                    tc_commit(&bar.empty[s]);
+                }
+                if (ok) tc_commit(&bar.dfull);
+            }
+            // the MMAs must have finished with both CTAs' memory before the exit
+            if (it > 0) mbar_wait_cluster(&bar.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1);
+        }
+    } else if (warp >= 4 && warp < 12) {
+        const int set = (warp - 4) / 4, q = warp % 4;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = first; i < items && ok; i += step) {
+            const Item w = item_of(a, i);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                if ((int)(it & 1) != set) continue;
+                const int s = it % kStages;
+                if (!(ok = warp_wait(&bar.full[s], (it / kStages) & 1))) break;
+                tc_after();
+                // scales of this thread's row pairs 8 j + 2 (lane % 4)
+                uint32_t f1[8], f2[8];
+                bool big = false;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int t = 8 * j + 2 * (lane & 3);
+                    const uint32_t e = *reinterpret_cast<const uint16_t *>(s_exps + s * kDeep + t);
+                    const int e0 = e & 255, e1 = e >> 8;
+                    const int64_t row = (int64_t)kb * kDeep + t;
+                    f1[j] = factor1(e0, row < a.T) | factor1(e1, row + 1 < a.T) << 16;
+                    f2[j] = factor2(e0) | factor2(e1) << 16;
+                    big |= f2[j] != 0x3f803f80u;
+                }
+                big = __any_sync(0xffffffffu, big);
+                const uint32_t x = smem_u32(smem + s * kStageBytes + kBBytes);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {       // 16 columns
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // 32 rows
+                        const int row = 32 * h + lane, chunk = 2 * q + g;
+                        uint32_t m[4], r[8];
+                        ldmatrix_t(x + row * 128 + ((chunk ^ (row & 7)) << 4), m);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = m[j] << 8, hi = m[j];
+                            r[2 * j] = mul_bf16x2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u), f1[4 * h + j]);
+                            r[2 * j + 1] = mul_bf16x2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u), f1[4 * h + j]);
+                        }
+                        if (big) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) r[j] = mul_bf16x2(r[j], f2[4 * h + j / 2]);
+                        }
+                        tc_store(tmem + ((uint32_t)(32 * q + 16 * g) << 16) + kTmemA + s * kTmemAStage + 16 * h, r);
+                    }
+                }
+                tc_store_wait();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&bar.afull[s]);
+            }
+        }
+    } else if (warp >= 12) {
+        const int q = warp % 4;
+        uint32_t tile = 0;
+        for (int i = first; i < items; i += step, ++tile) {
+            const Item w = item_of(a, i);
+            if (!warp_wait(&bar.dfull, tile & 1)) break;
+            tc_after();
+            // lane l of a group of 16 holds column 2 l (l < 8) or 2 (l - 8) + 1;
+            // neighbours trade halves so that each stores two columns of one row
+            const int64_t k = w.k0 + (int64_t)rank * kQBlock + 32 * q + (lane & 16) + 2 * (lane & 7);
+            float s0 = 1.f, s1 = 1.f;
+            if (a.scale && a.splits == 1) {
+                if (k < a.K) s0 = ld_param(a.scale, a.scale_f32, k);
+                if (k + 1 < a.K) s1 = ld_param(a.scale, a.scale_f32, k + 1);
+            }
+            for (int c = 0; c < kTileN; c += 32) {
+                uint32_t v[32];
+                tc_load32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
+                if (c + 32 == kTileN) {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_leader(&bar.dempty);
+                }
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const bool up = lane & 8;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
+                    const float x0 = __uint_as_float(up ? got : v[j]) * s0;
+                    const float x1 = __uint_as_float(up ? v[j + 1] : got) * s1;
+                    const int64_t n = w.n0 + c + j + (up ? 1 : 0);
+                    if (n >= a.N || k >= a.K) continue;
+                    const bool two = k + 1 < a.K;
+                    if (a.splits > 1) {  // ld_part is even and covers the pair
+                        float *o = a.part + ((int64_t)w.split * a.N + n) * a.ld_part + k;
+                        *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
+                    } else if (a.out_f32) {
+                        float *o = static_cast<float *>(a.dw) + n * a.ld_dw + k;
+                        if (a.pairs && two && !a.accumulate) {
+                            *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
+                        } else {
+                            o[0] = a.accumulate ? o[0] + x0 : x0;
+                            if (two) o[1] = a.accumulate ? o[1] + x1 : x1;
+                        }
+                    } else {
+                        uint16_t *o = static_cast<uint16_t *>(a.dw) + n * a.ld_dw + k;
+                        if (a.pairs && two && !a.accumulate) {
+                            *reinterpret_cast<uint32_t *>(o) = pack_bf16x2(x0, x1);
+                        } else {
+                            o[0] = to_bf16(a.accumulate ? bf_one(o[0]) + x0 : x0);
+                            if (two) o[1] = to_bf16(a.accumulate ? bf_one(o[1]) + x1 : x1);
+                        }
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 2) {
+        tc_after();
+        tc_free(tmem);
+    }
+}
+
+// Joins the splits in order and finishes the gradient; also writes the
+// gradient of no rows at all (splits = 0).
+__global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
+{
+    wait_prior_grid();
+    const int64_t n = blockIdx.y + (int64_t)blockIdx.z * 65535;
+    const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+    if (n >= a.N || k >= a.K) return;
+    float x0 = 0.f, x1 = 0.f;
+    const float *p = a.part + n * a.ld_part + k;
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 v = *reinterpret_cast<const float2 *>(p + (int64_t)s * a.N * a.ld_part);
+        x0 += v.x;
+        x1 += v.y;
+    }
+    const float x[2] = {x0, x1};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (k + j >= a.K) break;
+        const float v = a.scale ? x[j] * ld_param(a.scale, a.scale_f32, k + j) : x[j];
+        if (a.out_f32) {
+            float *o = static_cast<float *>(a.dw) + n * a.ld_dw + k + j;
+            *o = a.accumulate ? *o + v : v;
+        } else {
+            uint16_t *o = static_cast<uint16_t *>(a.dw) + n * a.ld_dw + k + j;
+            *o = to_bf16(a.accumulate ? bf_one(*o) + v : v);
+        }
+    }
+}
+
+// Copies dy to rows that start on 16-byte boundaries.
+__global__ void __launch_bounds__(256)
+k_align_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t T, int64_t N, uint16_t *__restrict__ dst, int64_t ld_dst)
+{
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
+        for (int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x; c < ld_dst; c += gridDim.y * 256)
+            dst[t * ld_dst + c] = c < N ? src[t * ld + c] : (uint16_t)0;
+}
+
+// --------------------------------------------------------------- launch ----
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A [rows, cols] matrix in boxes of box_x columns and kDeep rows, 128-byte swizzled.
+int make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *p, int64_t rows, int64_t cols, int64_t ld,
+             int box_x, const char *what)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)kDeep}, one[2] = {1, 1};
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return z1_fail(ZERO1_ECUDA, "weight gradient: the driver has no tensor maps");
+    const CUresult r = fn(m, type, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return z1_fail(ZERO1_ECUDA, "weight gradient: tensor map of %s: error %d", what, (int)r);
+    return ZERO1_OK;
+}
+
+bool rows_aligned(const void *dy, int64_t ld, int64_t rows)
+{
+    return (((uintptr_t)dy) & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld > 0));
+}
+
+// How a call is cut up: its tiles, the splits of the rows, and where the
+// partial sums and the aligned copy lie in the workspace.
+struct Plan {
+    int tiles_k, tiles_n, splits, kblocks, per_split, clusters;
+    int64_t ld_part, ld_copy, copy_at, bytes;
+};
+
+int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p)
+{
+    const char *call = "weight gradient";
+    const int64_t tk = (K + kTileK - 1) / kTileK, tn = (N + kTileN - 1) / kTileN, kb = (T + kDeep - 1) / kDeep;
+    if (T > INT32_MAX - kDeep || N > INT32_MAX - kTileN || K > INT32_MAX - kTileK || tk * tn > (1 << 24))
+        return z1_fail(ZERO1_ERANGE, "%s: %lld rows, %lld x %lld outputs: size not supported", call, (long long)T,
+                       (long long)N, (long long)K);
+    const int sms = sm_count();
+    if (sms == 0) return z1_fail(ZERO1_ECUDA, "%s: no CUDA device", call);
+    p->clusters = sms / 2;
+    const int64_t tiles = tk * tn;
+    int64_t splits = tiles < p->clusters ? p->clusters / tiles : 1;
+    if (splits > kb / 4) splits = kb / 4;  // at least four stages each
+    if (splits < 1) splits = 1;
+    p->per_split = (int)((kb + splits - 1) / splits);
+    p->splits = p->per_split ? (int)((kb + p->per_split - 1) / p->per_split) : 0;
+    p->tiles_k = (int)tk;
+    p->tiles_n = (int)tn;
+    p->kblocks = (int)kb;
+    p->ld_part = round_up(K, 8);
+    p->copy_at = p->splits > 1 ? round_up((int64_t)p->splits * N * p->ld_part * 4, 128) : 0;
+    p->ld_copy = round_up(N, 8);
+    p->bytes = p->copy_at + (rows_aligned(dy, ld, T) ? 0 : round_up(T * p->ld_copy * 2, 128));
+    return ZERO1_OK;
 }
 
 }  // namespace
+
+int z1_weight_grad_status(uint32_t *status, int32_t clear) { return (int)async_status(status, clear); }
 
 extern "C" int zero1_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy,
                                            int64_t *bytes)
 {
     if (!bytes) return z1_fail(ZERO1_EINVAL, "weight gradient workspace: bytes is NULL");
-    *bytes = 0;
-    return ZERO1_OK;
+    if (rows < 0 || n < 1 || k < 1)
+        return z1_fail(ZERO1_EINVAL, "weight gradient workspace: %lld rows, %lld x %lld outputs", (long long)rows,
+                       (long long)n, (long long)k);
+    Plan p;
+    const int rc = plan_of(rows, n, k, dy, ld_dy, &p);
+    if (rc == ZERO1_OK) *bytes = p.bytes;
+    return rc;
 }
 
 extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const zero1_checkpoint8_t *x8,
@@ -73,22 +556,75 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
         return rc;
     const int64_t T = x8->rows, K = x8->cols;
     const int eo = esize(out_dtype), es = esize(scale_dtype);
-    const Mat a = mat(dy, T, n, ld_dy, 2, "dy"), o = mat(dw, n, K, ld_dw, eo, "dw");
-    if ((rc = check_mat(a, 2, false, call)) || (rc = check_mat(o, eo, true, call)) ||
+    const Mat my = mat(dy, T, n, ld_dy, 2, "dy"), mo = mat(dw, n, K, ld_dw, eo, "dw");
+    if ((rc = check_mat(my, 2, false, call)) || (rc = check_mat(mo, eo, true, call)) ||
         (col_scale && (rc = check_natural(col_scale, es, "col_scale"))))
         return rc;
-    const Mat in[] = {a, codes_mat(x8, "the codes of x8"), exps_mat(x8, "the exps of x8"),
-                      mat(col_scale, 1, K, 0, es, "col_scale")};
+    Plan p;
+    if ((rc = plan_of(T, n, K, dy, ld_dy, &p)) != ZERO1_OK) return rc;
+    if (p.bytes > 0) {
+        if (!workspace || workspace_bytes < p.bytes)
+            return z1_fail(ZERO1_EINVAL, "%s: workspace of %lld bytes, needs %lld", call,
+                           (long long)(workspace ? workspace_bytes : 0), (long long)p.bytes);
+        if ((uintptr_t)workspace & 127) return z1_fail(ZERO1_EALIGN, "%s: the workspace is not 128-byte aligned", call);
+    }
+    const Mat in[] = {my, codes_mat(x8, "the codes of x8"), exps_mat(x8, "the exps of x8"),
+                      mat(col_scale, 1, K, 0, es, "col_scale"), Mat{workspace, 1, p.bytes, p.bytes, "the workspace"}};
     for (const Mat &m : in)
-        if (mats_overlap(o, m)) return z1_fail(ZERO1_EINVAL, "%s: dw and %s overlap", call, m.what);
-    const Ckpt c{x8->codes, x8->exps, x8->ld_codes, x8->ld_exps};
+        if (mats_overlap(mo, m)) return z1_fail(ZERO1_EINVAL, "%s: dw and %s overlap", call, m.what);
+    for (int q = 0; q < 4; ++q)
+        if (mats_overlap(in[4], in[q])) return z1_fail(ZERO1_EINVAL, "%s: the workspace and %s overlap", call, in[q].what);
+    if (T > 0 && (in_host_memory(dy) || in_host_memory(x8->codes) || in_host_memory(x8->exps)))
+        return z1_fail(ZERO1_EINVAL, "%s: dy and x8 must be device memory", call);
+
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid((unsigned)((n + kTile - 1) / kTile), (unsigned)((K + kTile - 1) / kTile));
-    if (out_dtype == ZERO1_DTYPE_F32)
-        k_weight_grad<float><<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(dy), ld_dy, T, n, K, c, col_scale,
-                                                   scale_dtype, static_cast<float *>(dw), ld_dw, accumulate);
-    else
-        k_weight_grad<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(dy), ld_dy, T, n, K, c, col_scale,
-                                                      scale_dtype, static_cast<uint16_t *>(dw), ld_dw, accumulate);
-    return launch_status("weight gradient launch");
+    Wg a{};
+    a.T = T; a.N = n; a.K = K;
+    a.tiles_k = p.tiles_k; a.tiles_n = p.tiles_n; a.splits = p.splits; a.kblocks = p.kblocks; a.per_split = p.per_split;
+    a.scale = col_scale;
+    a.scale_f32 = scale_dtype == ZERO1_DTYPE_F32;
+    a.dw = dw; a.ld_dw = n > 1 ? ld_dw : K;
+    a.out_f32 = out_dtype == ZERO1_DTYPE_F32;
+    a.accumulate = accumulate != 0;
+    a.pairs = ((uintptr_t)dw & (2 * eo - 1)) == 0 && a.ld_dw % 2 == 0;
+    a.part = static_cast<float *>(workspace);
+    a.ld_part = p.ld_part;
+    if (T > 0) {
+        a.exps = x8->exps;
+        a.ld_exps = x8->ld_exps;
+        const void *src = dy;
+        int64_t ld = T > 1 ? ld_dy : round_up(n, 8);
+        if (!rows_aligned(dy, ld_dy, T)) {
+            uint16_t *copy = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + p.copy_at);
+            const dim3 grid((unsigned)(T < 4096 ? T : 4096), (unsigned)(p.ld_copy < 256 * 65535 ? (p.ld_copy + 255) / 256 : 65535));
+            k_align_rows<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(dy), T > 1 ? ld_dy : 0, T, n, copy, p.ld_copy);
+            if ((rc = launch_status("weight gradient: aligned copy")) != ZERO1_OK) return rc;
+            src = copy;
+            ld = p.ld_copy;
+        }
+        CUtensorMap mdy, mx;
+        if ((rc = make_map(&mdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, src, T, n, ld, 64, "dy")) ||
+            (rc = make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
+                           "the codes")))
+            return rc;
+        cudaError_t e = cudaFuncSetAttribute(k_weight_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
+        if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
+        const int64_t items = (int64_t)p.tiles_k * p.tiles_n * p.splits;
+        const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
+        k_weight_grad<<<grid, kWgThreads, kWgSmem, st>>>(mdy, mx, a);
+        z1_note_launch(reinterpret_cast<const void *>(k_weight_grad), grid, 1, kWgThreads, 0);
+        if ((rc = launch_status("weight gradient launch")) != ZERO1_OK || p.splits == 1) return rc;
+    }
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)((K + 511) / 512), (unsigned)(n < 65535 ? n : 65535), (unsigned)((n + 65534) / 65535));
+    lc.blockDim = dim3(256);
+    lc.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, k_weight_grad_join, a);
+    if (e != cudaSuccess) return pdl_fail(e, "weight gradient: joining the splits");
+    return ZERO1_OK;
 }
