@@ -56,10 +56,15 @@ __device__ __forceinline__ uint64_t global_ns()
 // kWaitPolls polls should the timer not advance.
 constexpr uint64_t kWaitPolls = 1ull << 24;
 
+// The timer is only read after kWaitFree polls: a read takes about as long as
+// a whole stage of a pipeline that is waited on.
+constexpr int kWaitFree = 64;
+
 template <class Try>
 __device__ __forceinline__ bool bounded_wait(Try &&done, uint64_t limit_ns)
 {
-    if (done()) return true;
+    for (int k = 0; k < kWaitFree; ++k)
+        if (done()) return true;
     const uint64_t t0 = global_ns();
     for (uint64_t polls = 1; !done(); ++polls) {
         if (global_ns() - t0 > limit_ns || polls >= kWaitPolls) {
@@ -75,16 +80,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *b, uint32_t parity, uint64_t
     return bounded_wait([&] { return mbar_try(b, parity); }, limit_ns);
 }
 
-// The same for a barrier that another CTA of the cluster may arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *b, uint32_t parity)
+// The same, letting the hardware suspend the thread for up to kSuspendNs per
+// poll: for warps that wait long beside others that compute.
+constexpr uint32_t kSuspendNs = 20000;
+
+__device__ __forceinline__ bool mbar_wait_long(uint64_t *b, uint32_t parity)
 {
     return bounded_wait(
         [&] {
             uint32_t ok;
             asm volatile(
-                "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
                 : "=r"(ok)
-                : "r"(smem_u32(b)), "r"(parity)
+                : "r"(smem_u32(b)), "r"(parity), "r"(kSuspendNs)
                 : "memory");
             return ok != 0;
         },

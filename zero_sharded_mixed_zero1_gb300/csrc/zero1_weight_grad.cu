@@ -25,23 +25,29 @@ namespace {
 // of the contraction where a CTA alone would load 40.  Products are exact in
 // fp32; sums are fp32 in the accumulator.
 //
-// Roles (16 warps): warp 0 loads, warp 1 of the leading CTA issues the MMAs,
-// warps 4-11 convert (two sets of four take alternate stages), warps 12-15
-// store the result.
+// Roles (28 warps): warp 0 loads dy and warp 3 the codes, warp 1 of the
+// leading CTA issues the MMAs, warps 4-19 convert (four sets of four take
+// stages in turn), warps 20-27 store the result (each 32 lanes and half of the
+// columns of the accumulator).  bf16 results leave tensor memory at once, half
+// into registers and half into shared memory, so that the next tile's MMAs do
+// not wait for the stores to memory.
 
 constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
 constexpr int kDeep = 64;                  // rows of the contraction per stage
-constexpr int kStages = 8;
-constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;
-constexpr int kStageBytes = kBBytes + kXBytes;
-constexpr int kWgThreads = 512;
+constexpr int kStages = 8;                 // of B in shared and A in tensor memory
+constexpr int kCodeStages = 8;             // of codes and scales in shared memory
+constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;  // of a CTA, per stage
+constexpr int kSets = 4;                   // of four converting warps
+constexpr int kWgThreads = 32 * (4 + 4 * kSets + 8);
 constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
 
 struct WgBars {
-    uint64_t full[kStages], afull[kStages], empty[kStages], dfull, dempty;
+    uint64_t bfull[kStages], afull[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
 };
-constexpr int kWgSmem = 1024 + kStages * kStageBytes + kStages * kDeep + (int)sizeof(WgBars);
+constexpr int kStash = 32;  // packed pairs of results that a storing thread keeps in shared memory
+constexpr int kStashBytes = 8 * 32 * kStash * 4;
+constexpr int kWgSmem = 1024 + kStages * kBBytes + kCodeStages * (kXBytes + kDeep) + kStashBytes + (int)sizeof(WgBars);
 static_assert(kWgSmem <= 227 * 1024, "shared memory of a block");
 static_assert(kTmemA + kStages * kTmemAStage <= kTmemCols, "tensor memory");
 
@@ -117,6 +123,17 @@ __device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t r[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tc_load16(uint32_t addr, uint32_t r[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // Descriptor of a B tile: 128-byte swizzle, 64 columns x kDeep rows per TMA
 // box (kDeep * 128 bytes from one 64-column group to the next), 8 rows per
 // 1024-byte group.
@@ -148,16 +165,41 @@ __device__ __forceinline__ void cluster_sync()
 __device__ __forceinline__ void arrive_leader(uint64_t *bar)
 {
     asm volatile(
-        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a]; }" ::"r"(
+        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; mbarrier.arrive.shared::cluster.b64 _, [a]; }" ::"r"(
             smem_u32(bar))
         : "memory");
 }
 
-// A bounded wait of a whole warp on a barrier that either CTA may arrive on.
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
+}
+
+// A bounded wait of a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
-    bool ok = mbar_wait_cluster(bar, parity);
-    return __all_sync(0xffffffffu, ok);
+    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity));
+}
+
+// The leading CTA's copy of a barrier, as a cluster address.
+__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+    return a;
+}
+
+// A box into this CTA's shared memory, counted on the leading CTA's barrier.
+__device__ __forceinline__ void tma_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
@@ -218,23 +260,135 @@ __device__ __forceinline__ Item item_of(const Wg &a, int i)
     return o;
 }
 
+// ------------------------------------------------------------- epilogue ----
+//
+// A warp stores 32 lanes (columns k) x 128 accumulator columns (rows n).  Lane
+// l of a group of 16 holds column 2 l (l < 8) or 2 (l - 8) + 1; lanes l and
+// l + 8 trade so that each has both columns of every other row, and a store
+// instruction writes 64 consecutive bytes (bf16) of two rows.
+
+__device__ __forceinline__ int own_column(int lane) { return (lane & 16) + 2 * (lane & 7) + ((lane >> 3) & 1); }
+
+// The accumulator has been read: the next tile may overwrite it.
+__device__ __forceinline__ void release_acc(uint64_t *dempty)
+{
+    tc_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_leader(dempty);
+}
+
+__device__ __forceinline__ void store_bf16(const Wg &a, uint32_t acc, int64_t k0, int64_t n0, uint32_t *stash, uint64_t *dempty)
+{
+    const int lane = threadIdx.x & 31;
+    float scale = 1.f;
+    if (a.scale && k0 + own_column(lane) < a.K) scale = ld_param(a.scale, a.scale_f32, k0 + own_column(lane));
+    const bool up = lane & 8;
+    const int64_t k = k0 + (lane & 16) + 2 * (lane & 7);
+    if (a.accumulate) {  // rounded once, after the addition
+        for (int c = 0; c < kTileN / 2; c += 32) {
+            uint32_t v[32];
+            tc_load32(acc + c, v);
+            if (c + 32 == kTileN / 2) release_acc(dempty);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const int64_t n = n0 + c + j, kk = k0 + own_column(lane);
+                if (n >= a.N || kk >= a.K) continue;
+                uint16_t *o = static_cast<uint16_t *>(a.dw) + n * a.ld_dw + kk;
+                *o = to_bf16(fmaf(__uint_as_float(v[j]), scale, bf_one(*o)));
+            }
+        }
+        return;
+    }
+    uint32_t p[kTileN / 4 - kStash];
+#pragma unroll
+    for (int c = 0; c < kTileN / 2; c += 16) {
+        uint32_t v[16];
+        tc_load16(acc + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const uint32_t x = pack_bf16x2(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale);
+            if ((c + j) / 2 < kStash) stash[(c + j) / 2 * 32] = x;
+            else p[(c + j) / 2 - kStash] = x;
+        }
+    }
+    release_acc(dempty);
+    uint16_t *o = static_cast<uint16_t *>(a.dw) + (n0 + (up ? 1 : 0)) * a.ld_dw + k;
+    const bool two = k + 1 < a.K;
+#pragma unroll
+    for (int j = 0; j < kTileN / 2; j += 2, o += 2 * a.ld_dw) {
+        const uint32_t mine = j / 2 < kStash ? stash[j / 2 * 32] : p[j / 2 - kStash], other = __shfl_xor_sync(0xffffffffu, mine, 8);
+        const uint32_t x = up ? __byte_perm(mine, other, 0x3276) : __byte_perm(mine, other, 0x5410);
+        if (n0 + j + (up ? 1 : 0) >= a.N || k >= a.K) continue;
+        if (a.pairs && two) {
+            *reinterpret_cast<uint32_t *>(o) = x;
+        } else {
+            o[0] = (uint16_t)x;
+            if (two) o[1] = (uint16_t)(x >> 16);
+        }
+    }
+}
+
+// fp32 gradients and the partial sums of a split.
+__device__ __forceinline__ void store_f32(const Wg &a, uint32_t acc, int64_t k0, int64_t n0, int split, uint64_t *dempty)
+{
+    const int lane = threadIdx.x & 31;
+    const bool part = a.splits > 1, up = lane & 8;
+    const bool accumulate = a.accumulate && !part;
+    float scale = 1.f;
+    if (!part && a.scale && k0 + own_column(lane) < a.K) scale = ld_param(a.scale, a.scale_f32, k0 + own_column(lane));
+    const int64_t k = k0 + (lane & 16) + 2 * (lane & 7);
+    const int64_t ld = part ? a.ld_part : a.ld_dw;
+    float *base = part ? a.part + (int64_t)split * a.N * a.ld_part : static_cast<float *>(a.dw);
+    // ld_part is even and its padding belongs to the row
+    const bool two = k + 1 < a.K || part, pairs = (a.pairs || part) && two;
+    for (int c = 0; c < kTileN / 2; c += 32) {
+        uint32_t v[32];
+        tc_load32(acc + c, v);
+        if (c + 32 == kTileN / 2) release_acc(dempty);
+        float *o = base + (n0 + c + (up ? 1 : 0)) * ld + k;
+#pragma unroll
+        for (int j = 0; j < 32; j += 2, o += 2 * ld) {
+            const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
+            float x0 = up ? got : v0, x1 = up ? v1 : got;
+            if (n0 + c + j + (up ? 1 : 0) >= a.N || k >= a.K) continue;
+            if (accumulate) {
+                x0 += o[0];
+                if (two) x1 += o[1];
+            }
+            if (pairs) {
+                *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
+            } else {
+                o[0] = x0;
+                if (two) o[1] = x1;
+            }
+        }
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
 k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const Wg a)
 {
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint8_t *s_exps = smem + kStages * kStageBytes;
-    WgBars &bar = *reinterpret_cast<WgBars *>(s_exps + kStages * kDeep);
+    unsigned char *s_codes = smem + kStages * kBBytes;
+    uint8_t *s_exps = s_codes + kCodeStages * kXBytes;
+    uint32_t *s_stash = reinterpret_cast<uint32_t *>(s_exps + kCodeStages * kDeep);
+    WgBars &bar = *reinterpret_cast<WgBars *>(s_stash + kStashBytes / 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.bfull[s], 1);
             mbar_init(&bar.afull[s], 8);   // four converting warps of each CTA
             mbar_init(&bar.empty[s], 1);
         }
+        for (int s = 0; s < kCodeStages; ++s) {
+            mbar_init(&bar.cfull[s], 1);
+            mbar_init(&bar.cempty[s], 4);  // four converting warps
+        }
         mbar_init(&bar.dfull, 1);
-        mbar_init(&bar.dempty, 8);  // four storing warps of each CTA
+        mbar_init(&bar.dempty, 16);  // eight storing warps of each CTA
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tc_alloc(&bar.tmem);
@@ -246,160 +400,157 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     const int items = a.tiles_k * a.tiles_n * a.splits;
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
+    // The loading and issuing warps run whole, so that addresses and descriptors
+    // stay in uniform registers, and elect one lane for each instruction.
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            for (int i = first; i < items && ok; i += step) {
-                const Item w = item_of(a, i);
-                const int64_t block = min((int64_t)(w.k0 / kQBlock) + rank, (a.K - 1) / kQBlock);
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (it >= kStages && !(ok = mbar_wait_cluster(&bar.empty[s], (it / kStages - 1) & 1))) break;
-                    unsigned char *b = smem + s * kStageBytes;
-                    mbar_expect_tx(&bar.full[s], kStageBytes + kDeep);
-                    const int n = w.n0 + (int)rank * (kTileN / 2);
-                    tma_2d(b, &map_dy, n, kb * kDeep, &bar.full[s]);
-                    tma_2d(b + kBBytes / 2, &map_dy, n + 64, kb * kDeep, &bar.full[s]);
-                    tma_2d(b + kBBytes, &map_x, w.k0 + (int)rank * kQBlock, kb * kDeep, &bar.full[s]);
-                    bulk_load(s_exps + s * kDeep, a.exps + block * a.ld_exps + (int64_t)kb * kDeep, kDeep, &bar.full[s]);
-                }
-            }
-            // the last copies must land before the block may exit
-            for (uint32_t q = it > kStages ? it - kStages : 0; q < it; ++q)
-                mbar_wait(&bar.full[q % kStages], (q / kStages) & 1);
-        }
-    } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            uint32_t it = 0, tile = 0;
-            bool ok = true;
-            for (int i = first; i < items && ok; i += step, ++tile) {
-                const Item w = item_of(a, i);
-                if (tile > 0 && !(ok = mbar_wait_cluster(&bar.dempty, (tile - 1) & 1))) break;
-                tc_after();
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int s = it % kStages;
-                    const uint32_t ph = (it / kStages) & 1;
-                    if (!(ok = mbar_wait_cluster(&bar.full[s], ph) && mbar_wait_cluster(&bar.afull[s], ph))) break;
-                    tc_after();
-                    const uint32_t b = smem_u32(smem + s * kStageBytes);
-#pragma unroll
-                    for (int j = 0; j < kDeep / 16; ++j)
-                        tc_mma(tmem, tmem + kTmemA + s * kTmemAStage + 8 * j, b_desc(b + j * 2048), kIdesc,
-                               kb > w.kb0 || j > 0);
-                    tc_commit(&bar.empty[s]);
-                }
-                if (ok) tc_commit(&bar.dfull);
-            }
-            // the MMAs must have finished with both CTAs' memory before the exit
-            if (it > 0) mbar_wait_cluster(&bar.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1);
-        }
-    } else if (warp >= 4 && warp < 12) {
-        const int set = (warp - 4) / 4, q = warp % 4;
         uint32_t it = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
             const Item w = item_of(a, i);
+            const int n = w.n0 + (int)rank * (kTileN / 2);
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                if ((int)(it & 1) != set) continue;
                 const int s = it % kStages;
-                if (!(ok = warp_wait(&bar.full[s], (it / kStages) & 1))) break;
-                tc_after();
-                // scales of this thread's row pairs 8 j + 2 (lane % 4)
-                uint32_t f1[8], f2[8];
-                bool big = false;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = 8 * j + 2 * (lane & 3);
-                    const uint32_t e = *reinterpret_cast<const uint16_t *>(s_exps + s * kDeep + t);
-                    const int e0 = e & 255, e1 = e >> 8;
-                    const int64_t row = (int64_t)kb * kDeep + t;
-                    f1[j] = factor1(e0, row < a.T) | factor1(e1, row + 1 < a.T) << 16;
-                    f2[j] = factor2(e0) | factor2(e1) << 16;
-                    big |= f2[j] != 0x3f803f80u;
+                if (it >= kStages && !(ok = warp_wait(&bar.empty[s], (it / kStages - 1) & 1))) break;
+                unsigned char *b = smem + s * kBBytes;
+                if (elect_one()) {
+                    // both CTAs' halves count on the leading CTA's barrier
+                    const uint32_t full = leader_addr(&bar.bfull[s]);
+                    if (rank == 0) mbar_expect_tx(&bar.bfull[s], 2 * kBBytes);
+                    tma_2d_pair(b, &map_dy, n, kb * kDeep, full);
+                    tma_2d_pair(b + kBBytes / 2, &map_dy, n + 64, kb * kDeep, full);
                 }
-                big = __any_sync(0xffffffffu, big);
-                const uint32_t x = smem_u32(smem + s * kStageBytes + kBBytes);
+                __syncwarp();
+            }
+        }
+        // the last copies must land before the pair may exit
+        if (rank == 0)
+            for (uint32_t q = it > kStages ? it - kStages : 0; q < it; ++q)
+                warp_wait(&bar.bfull[q % kStages], (q / kStages) & 1);
+    } else if (warp == 3) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = first; i < items && ok; i += step) {
+            const Item w = item_of(a, i);
+            const int64_t block = min((int64_t)(w.k0 / kQBlock) + rank, (a.K - 1) / kQBlock);
+            const uint8_t *exps = a.exps + block * a.ld_exps;
+            const int k = w.k0 + (int)rank * kQBlock;
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const int s = it % kCodeStages;
+                if (it >= kCodeStages && !(ok = warp_wait(&bar.cempty[s], (it / kCodeStages - 1) & 1))) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&bar.cfull[s], kXBytes + kDeep);
+                    tma_2d(s_codes + s * kXBytes, &map_x, k, kb * kDeep, &bar.cfull[s]);
+                    bulk_load(s_exps + s * kDeep, exps + (int64_t)kb * kDeep, kDeep, &bar.cfull[s]);
+                }
+                __syncwarp();
+            }
+        }
+        for (uint32_t q = it > kCodeStages ? it - kCodeStages : 0; q < it; ++q)
+            warp_wait(&bar.cfull[q % kCodeStages], (q / kCodeStages) & 1);
+    } else if (warp == 1) {
+        if (rank == 0) {
+            uint32_t it = 0, tile = 0;
+            bool ok = true;
+            const uint64_t b0 = b_desc(smem_u32(smem));
+            for (int i = first; i < items && ok; i += step, ++tile) {
+                const Item w = item_of(a, i);
+                if (tile > 0 && !(ok = warp_wait(&bar.dempty, (tile - 1) & 1))) break;
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (it / kStages) & 1;
+                    if (!(ok = warp_wait(&bar.bfull[s], ph) && warp_wait(&bar.afull[s], ph))) break;
+                    tc_after();
+                    if (elect_one()) {
+                        const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
+                        const uint32_t ta = tmem + kTmemA + s * kTmemAStage;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {       // 16 columns
+                        for (int j = 0; j < kDeep / 16; ++j)
+                            tc_mma(tmem, ta + 8 * j, b + j * (2048 >> 4), kIdesc, kb > w.kb0 || j > 0);
+                        tc_commit(&bar.empty[s]);
+                        if (kb + 1 == w.kb1) tc_commit(&bar.dfull);
+                    }
+                    __syncwarp();
+                }
+            }
+            // the MMAs must have finished with both CTAs' memory before the exit
+            if (it > 0) warp_wait(&bar.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1);
+        }
+    } else if (warp >= 4 && warp < 4 + 4 * kSets) {
+        const uint32_t set = (warp - 4) / 4, q = warp % 4;
+        uint32_t it0 = 0;  // stages before this item
+        bool ok = true;
+        // this thread's share of a stage: ldmatrix rows `lane` and 32 + lane, columns 32 q .. 32 q + 31
+        const uint32_t x_row = smem_u32(s_codes) + lane * 128, x_swz = lane & 7;
+        const uint32_t a_addr = tmem + ((32 * q) << 16) + kTmemA;
+        for (int i = first; i < items && ok; i += step) {
+            const Item w = item_of(a, i);
+            const uint32_t n = w.kb1 - w.kb0;
+            for (uint32_t j = (set - it0) % kSets; j < n; j += kSets) {
+                const uint32_t it = it0 + j, s = it % kStages, c = it % kCodeStages;
+                if (!(ok = warp_wait(&bar.cfull[c], (it / kCodeStages) & 1))) break;
+                // Scales of rows 2 lane and 2 lane + 1 as a bf16 pair, passed to
+                // the lanes that convert those rows.  Almost always every scale
+                // of the stage is at most 2^7 and every row is there: then one
+                // factor 2^(e + 120) does.
+                const uint32_t e = reinterpret_cast<const uint16_t *>(s_exps + c * kDeep)[lane];
+                const int left = (int)(a.T - (int64_t)(w.kb0 + j) * kDeep) - 2 * lane;  // rows from this lane's on
+                uint32_t mine = (__byte_perm(e, 0, 0x4140) + 0x00780078u) << 7, more = 0x3f803f80u;
+                const bool plain = __all_sync(0xffffffffu, (e & 255) <= 134 && (e >> 8) <= 134 && left >= 2);
+                if (!plain) {
+                    mine = factor1(e & 255, left >= 1) | factor1(e >> 8, left >= 2) << 16;
+                    more = factor2(e & 255) | factor2(e >> 8) << 16;
+                }
+                if (it >= kStages && !(ok = warp_wait(&bar.empty[s], (it / kStages - 1) & 1))) break;
+                tc_after();
+                const uint32_t x = x_row + c * kXBytes, at = a_addr + s * kTmemAStage;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {   // 32 rows
-                        const int row = 32 * h + lane, chunk = 2 * q + g;
+                for (int h = 0; h < 2; ++h) {  // 32 rows
+                    uint32_t f[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) f[p] = __shfl_sync(0xffffffffu, mine, 16 * h + 4 * p + (lane & 3));
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {  // 16 columns
                         uint32_t m[4], r[8];
-                        ldmatrix_t(x + row * 128 + ((chunk ^ (row & 7)) << 4), m);
+                        ldmatrix_t(x + h * 4096 + (((2 * q + g) ^ x_swz) << 4), m);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = m[j] << 8, hi = m[j];
-                            r[2 * j] = mul_bf16x2((lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u), f1[4 * h + j]);
-                            r[2 * j + 1] = mul_bf16x2((hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u), f1[4 * h + j]);
+                        for (int p = 0; p < 4; ++p) {
+                            // even and odd columns of the pair, sign and magnitude put in place
+                            const uint32_t lo = (m[p] & 0x007f007fu) * 16u, hi = (m[p] >> 4) & 0x07f007f0u;
+                            r[2 * p] = mul_bf16x2((m[p] & 0x00800080u) * 256u + lo, f[p]);
+                            r[2 * p + 1] = mul_bf16x2(hi | (m[p] & 0x80008000u), f[p]);
                         }
-                        if (big) {
+                        if (!plain) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) r[j] = mul_bf16x2(r[j], f2[4 * h + j / 2]);
+                            for (int p = 0; p < 4; ++p) {
+                                const uint32_t f2 = __shfl_sync(0xffffffffu, more, 16 * h + 4 * p + (lane & 3));
+                                r[2 * p] = mul_bf16x2(r[2 * p], f2);
+                                r[2 * p + 1] = mul_bf16x2(r[2 * p + 1], f2);
+                            }
                         }
-                        tc_store(tmem + ((uint32_t)(32 * q + 16 * g) << 16) + kTmemA + s * kTmemAStage + 16 * h, r);
+                        tc_store(at + ((16 * g) << 16) + 16 * h, r);
                     }
                 }
                 tc_store_wait();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader(&bar.afull[s]);
+                if (lane == 0) {
+                    mbar_arrive(&bar.cempty[c]);
+                    arrive_leader(&bar.afull[s]);
+                }
             }
+            it0 += n;
         }
-    } else if (warp >= 12) {
-        const int q = warp % 4;
+    } else if (warp >= 4 + 4 * kSets) {
+        const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
         uint32_t tile = 0;
         for (int i = first; i < items; i += step, ++tile) {
             const Item w = item_of(a, i);
             if (!warp_wait(&bar.dfull, tile & 1)) break;
             tc_after();
-            // lane l of a group of 16 holds column 2 l (l < 8) or 2 (l - 8) + 1;
-            // neighbours trade halves so that each stores two columns of one row
-            const int64_t k = w.k0 + (int64_t)rank * kQBlock + 32 * q + (lane & 16) + 2 * (lane & 7);
-            float s0 = 1.f, s1 = 1.f;
-            if (a.scale && a.splits == 1) {
-                if (k < a.K) s0 = ld_param(a.scale, a.scale_f32, k);
-                if (k + 1 < a.K) s1 = ld_param(a.scale, a.scale_f32, k + 1);
-            }
-            for (int c = 0; c < kTileN; c += 32) {
-                uint32_t v[32];
-                tc_load32(tmem + ((uint32_t)(32 * q) << 16) + c, v);
-                if (c + 32 == kTileN) {
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_leader(&bar.dempty);
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const bool up = lane & 8;
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + 1], 8);
-                    const float x0 = __uint_as_float(up ? got : v[j]) * s0;
-                    const float x1 = __uint_as_float(up ? v[j + 1] : got) * s1;
-                    const int64_t n = w.n0 + c + j + (up ? 1 : 0);
-                    if (n >= a.N || k >= a.K) continue;
-                    const bool two = k + 1 < a.K;
-                    if (a.splits > 1) {  // ld_part is even and covers the pair
-                        float *o = a.part + ((int64_t)w.split * a.N + n) * a.ld_part + k;
-                        *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
-                    } else if (a.out_f32) {
-                        float *o = static_cast<float *>(a.dw) + n * a.ld_dw + k;
-                        if (a.pairs && two && !a.accumulate) {
-                            *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
-                        } else {
-                            o[0] = a.accumulate ? o[0] + x0 : x0;
-                            if (two) o[1] = a.accumulate ? o[1] + x1 : x1;
-                        }
-                    } else {
-                        uint16_t *o = static_cast<uint16_t *>(a.dw) + n * a.ld_dw + k;
-                        if (a.pairs && two && !a.accumulate) {
-                            *reinterpret_cast<uint32_t *>(o) = pack_bf16x2(x0, x1);
-                        } else {
-                            o[0] = to_bf16(a.accumulate ? bf_one(o[0]) + x0 : x0);
-                            if (two) o[1] = to_bf16(a.accumulate ? bf_one(o[1]) + x1 : x1);
-                        }
-                    }
-                }
-            }
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * (kTileN / 2);
+            const int64_t k0 = w.k0 + (int64_t)rank * kQBlock + 32 * q, n0 = w.n0 + half * (kTileN / 2);
+            if (a.splits == 1 && !a.out_f32) store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
+            else store_f32(a, acc, k0, n0, w.split, &bar.dempty);
         }
     }
     __syncwarp();
