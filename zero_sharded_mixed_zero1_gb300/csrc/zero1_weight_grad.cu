@@ -53,7 +53,8 @@ static_assert(kTmemA + kStages * kTmemAStage <= kTmemCols, "tensor memory");
 
 struct Wg {
     int64_t T, N, K;
-    int tiles_k, tiles_n, splits, kblocks, per_split;  // kblocks: stages of the whole contraction
+    int tiles_k, tiles_n, kblocks;      // kblocks: stages of the whole contraction
+    int whole, splits, per_split;       // tiles done whole; the others in this many parts of per_split stages
     const uint8_t *exps;
     int64_t ld_exps;
     const void *scale;
@@ -61,8 +62,7 @@ struct Wg {
     void *dw;
     int64_t ld_dw;
     int out_f32, accumulate, pairs;  // pairs: two outputs of a row per store
-    float *part;                     // splits > 1: [splits][N][ld_part]
-    int64_t ld_part;
+    float *part;                     // [split tile][part][kTileN][kTileK]
 };
 
 // ------------------------------------------------------------- tcgen05 -----
@@ -239,25 +239,43 @@ __device__ __forceinline__ uint32_t factor2(int E) { return (uint32_t)(127 + (E 
 // ----------------------------------------------------------------- kernel --
 
 struct Item {
-    int n0, k0, kb0, kb1, split;
+    int n0, k0, kb0, kb1, part;  // part: its place among the partial sums, -1 for a whole tile
 };
 
 // Tiles run in bands of eight along k, so that the pairs of CTAs at work at
 // one time share few columns of both operands (they meet in L2).
-__device__ __forceinline__ Item item_of(const Wg &a, int i)
+__device__ __forceinline__ void tile_of(const Wg &a, int t, int &n0, int &k0)
 {
-    const int tiles = a.tiles_k * a.tiles_n;
-    const int split = i / tiles, t = i % tiles;
     constexpr int kBand = 8;
     const int per = kBand * a.tiles_n, band = t / per, in = t % per;
     const int width = min(kBand, a.tiles_k - band * kBand);
+    k0 = (band * kBand + in % width) * kTileK;
+    n0 = in / width * kTileN;
+}
+
+// The whole tiles come first, then the parts of the others: all first parts,
+// all second ones and so on, so that neighbours in time share operands.
+__device__ __forceinline__ Item item_of(const Wg &a, int i)
+{
     Item o;
-    o.k0 = (band * kBand + in % width) * kTileK;
-    o.n0 = in / width * kTileN;
-    o.split = split;
-    o.kb0 = split * a.per_split;
-    o.kb1 = min(o.kb0 + a.per_split, a.kblocks);
+    if (i < a.whole) {
+        tile_of(a, i, o.n0, o.k0);
+        o.kb0 = 0;
+        o.kb1 = a.kblocks;
+        o.part = -1;
+    } else {
+        const int rest = a.tiles_k * a.tiles_n - a.whole, t = (i - a.whole) % rest, p = (i - a.whole) / rest;
+        tile_of(a, a.whole + t, o.n0, o.k0);
+        o.kb0 = p * a.per_split;
+        o.kb1 = min(o.kb0 + a.per_split, a.kblocks);
+        o.part = t * a.splits + p;
+    }
     return o;
+}
+
+__device__ __forceinline__ int items_of(const Wg &a)
+{
+    return a.whole + (a.tiles_k * a.tiles_n - a.whole) * a.splits;
 }
 
 // ------------------------------------------------------------- epilogue ----
@@ -314,6 +332,15 @@ __device__ __forceinline__ void store_bf16(const Wg &a, uint32_t acc, int64_t k0
     release_acc(dempty);
     uint16_t *o = static_cast<uint16_t *>(a.dw) + (n0 + (up ? 1 : 0)) * a.ld_dw + k;
     const bool two = k + 1 < a.K;
+    if (a.pairs && n0 + kTileN / 2 <= a.N && k0 + 32 <= a.K) {  // no bounds to check
+#pragma unroll
+        for (int j = 0; j < kTileN / 2; j += 2, o += 2 * a.ld_dw) {
+            const uint32_t mine = j / 2 < kStash ? stash[j / 2 * 32] : p[j / 2 - kStash];
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 8);
+            *reinterpret_cast<uint32_t *>(o) = up ? __byte_perm(mine, other, 0x3276) : __byte_perm(mine, other, 0x5410);
+        }
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < kTileN / 2; j += 2, o += 2 * a.ld_dw) {
         const uint32_t mine = j / 2 < kStash ? stash[j / 2 * 32] : p[j / 2 - kStash], other = __shfl_xor_sync(0xffffffffu, mine, 8);
@@ -328,41 +355,56 @@ __device__ __forceinline__ void store_bf16(const Wg &a, uint32_t acc, int64_t k0
     }
 }
 
-// fp32 gradients and the partial sums of a split.
-__device__ __forceinline__ void store_f32(const Wg &a, uint32_t acc, int64_t k0, int64_t n0, int split, uint64_t *dempty)
+// The two columns that this lane stores of one of the rows j, j + 1.
+__device__ __forceinline__ float2 trade(float v0, float v1)
+{
+    const bool up = threadIdx.x & 8;
+    const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
+    return up ? make_float2(got, v1) : make_float2(v0, got);
+}
+
+__device__ __forceinline__ void store_f32(const Wg &a, uint32_t acc, int64_t k0, int64_t n0, uint64_t *dempty)
 {
     const int lane = threadIdx.x & 31;
-    const bool part = a.splits > 1, up = lane & 8;
-    const bool accumulate = a.accumulate && !part;
+    const bool up = lane & 8;
     float scale = 1.f;
-    if (!part && a.scale && k0 + own_column(lane) < a.K) scale = ld_param(a.scale, a.scale_f32, k0 + own_column(lane));
+    if (a.scale && k0 + own_column(lane) < a.K) scale = ld_param(a.scale, a.scale_f32, k0 + own_column(lane));
     const int64_t k = k0 + (lane & 16) + 2 * (lane & 7);
-    const int64_t ld = part ? a.ld_part : a.ld_dw;
-    float *base = part ? a.part + (int64_t)split * a.N * a.ld_part : static_cast<float *>(a.dw);
-    // ld_part is even and its padding belongs to the row
-    const bool two = k + 1 < a.K || part, pairs = (a.pairs || part) && two;
+    const bool two = k + 1 < a.K;
+    const bool easy = a.pairs && !a.accumulate && n0 + kTileN / 2 <= a.N && k0 + 32 <= a.K;
     for (int c = 0; c < kTileN / 2; c += 32) {
         uint32_t v[32];
         tc_load32(acc + c, v);
         if (c + 32 == kTileN / 2) release_acc(dempty);
-        float *o = base + (n0 + c + (up ? 1 : 0)) * ld + k;
+        float *o = static_cast<float *>(a.dw) + (n0 + c + (up ? 1 : 0)) * a.ld_dw + k;
+        if (easy) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 2, o += 2 * ld) {
-            const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-            float x0 = up ? got : v0, x1 = up ? v1 : got;
-            if (n0 + c + j + (up ? 1 : 0) >= a.N || k >= a.K) continue;
-            if (accumulate) {
-                x0 += o[0];
-                if (two) x1 += o[1];
-            }
-            if (pairs) {
-                *reinterpret_cast<float2 *>(o) = make_float2(x0, x1);
-            } else {
-                o[0] = x0;
-                if (two) o[1] = x1;
-            }
+            for (int j = 0; j < 32; j += 2, o += 2 * a.ld_dw)
+                *reinterpret_cast<float2 *>(o) = trade(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale);
+            continue;
         }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2, o += 2 * a.ld_dw) {
+            const float2 x = trade(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale);
+            if (n0 + c + j + (up ? 1 : 0) >= a.N || k >= a.K) continue;
+            o[0] = a.accumulate ? o[0] + x.x : x.x;
+            if (two) o[1] = a.accumulate ? o[1] + x.y : x.y;
+        }
+    }
+}
+
+// A part's sums, as a whole tile of the workspace.
+__device__ __forceinline__ void store_part(float *part, uint32_t acc, int k, int n, uint64_t *dempty)
+{
+    const int lane = threadIdx.x & 31;
+    float *o = part + (n + ((lane >> 3) & 1)) * kTileK + k + (lane & 16) + 2 * (lane & 7);
+    for (int c = 0; c < kTileN / 2; c += 32, o += 32 * kTileK) {
+        uint32_t v[32];
+        tc_load32(acc + c, v);
+        if (c + 32 == kTileN / 2) release_acc(dempty);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+            *reinterpret_cast<float2 *>(o + j * kTileK) = trade(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
     }
 }
 
@@ -397,7 +439,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     cluster_sync();
     tc_after();
     const uint32_t tmem = bar.tmem;
-    const int items = a.tiles_k * a.tiles_n * a.splits;
+    const int items = items_of(a);
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
 
     // The loading and issuing warps run whole, so that addresses and descriptors
@@ -549,8 +591,9 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             tc_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * (kTileN / 2);
             const int64_t k0 = w.k0 + (int64_t)rank * kQBlock + 32 * q, n0 = w.n0 + half * (kTileN / 2);
-            if (a.splits == 1 && !a.out_f32) store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
-            else store_f32(a, acc, k0, n0, w.split, &bar.dempty);
+            if (w.part < 0 && !a.out_f32) store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
+            else if (w.part < 0) store_f32(a, acc, k0, n0, &bar.dempty);
+            else store_part(a.part + (int64_t)w.part * kTileN * kTileK, acc, (int)(k0 - w.k0), (int)(n0 - w.n0), &bar.dempty);
         }
     }
     __syncwarp();
@@ -562,33 +605,46 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     }
 }
 
-// Joins the splits in order and finishes the gradient; also writes the
-// gradient of no rows at all (splits = 0).
+// Adds a split tile's parts in order and finishes the gradient there; with no
+// parts at all (no rows) the gradient of every tile is 0.  A block takes 8 rows
+// of a tile, a thread 8 columns.
 __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
 {
     wait_prior_grid();
-    const int64_t n = blockIdx.y + (int64_t)blockIdx.z * 65535;
-    const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-    if (n >= a.N || k >= a.K) return;
-    float x0 = 0.f, x1 = 0.f;
-    const float *p = a.part + n * a.ld_part + k;
+    int n0, k0;
+    tile_of(a, a.whole + blockIdx.y, n0, k0);
+    const int n = blockIdx.x * 8 + threadIdx.x / 32, k = threadIdx.x % 32 * 8;
+    if (n0 + n >= a.N || k0 + k >= a.K) return;
+    float x[8] = {};
+    const float *p = a.part + (int64_t)blockIdx.y * a.splits * kTileN * kTileK + n * kTileK + k;
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 v = *reinterpret_cast<const float2 *>(p + (int64_t)s * a.N * a.ld_part);
-        x0 += v.x;
-        x1 += v.y;
-    }
-    const float x[2] = {x0, x1};
+    for (int s = 0; s < a.splits; ++s, p += kTileN * kTileK) {
+        Raw8<float> q;
+        float v[8];
+        q.load(p);
+        q.get(v);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        if (k + j >= a.K) break;
-        const float v = a.scale ? x[j] * ld_param(a.scale, a.scale_f32, k + j) : x[j];
-        if (a.out_f32) {
-            float *o = static_cast<float *>(a.dw) + n * a.ld_dw + k + j;
-            *o = a.accumulate ? *o + v : v;
+        for (int j = 0; j < 8; ++j) x[j] += v[j];
+    }
+    const int64_t kk = (int64_t)k0 + k;
+    const int width = kk + 8 <= a.K ? 8 : (int)(a.K - kk);
+    if (a.scale)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] *= j < width ? ld_param(a.scale, a.scale_f32, kk + j) : 0.f;
+    const int64_t at = (int64_t)(n0 + n) * a.ld_dw + kk;
+    if (a.out_f32) {
+        float *o = static_cast<float *>(a.dw) + at;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < width) o[j] = a.accumulate ? o[j] + x[j] : x[j];
+    } else {
+        uint16_t *o = static_cast<uint16_t *>(a.dw) + at;
+        if (!a.accumulate && width == 8 && ((uintptr_t)o & 15) == 0) {
+            store8(o, x);
         } else {
-            uint16_t *o = static_cast<uint16_t *>(a.dw) + n * a.ld_dw + k + j;
-            *o = to_bf16(a.accumulate ? bf_one(*o) + v : v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < width) o[j] = to_bf16(a.accumulate ? bf_one(o[j]) + x[j] : x[j]);
         }
     }
 }
@@ -644,12 +700,40 @@ bool rows_aligned(const void *dy, int64_t ld, int64_t rows)
     return (((uintptr_t)dy) & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld > 0));
 }
 
-// How a call is cut up: its tiles, the splits of the rows, and where the
-// partial sums and the aligned copy lie in the workspace.
+// How a call is cut up: its tiles, which of them are split along the rows, and
+// where the partial sums and the aligned copy lie in the workspace.
 struct Plan {
-    int tiles_k, tiles_n, splits, kblocks, per_split, clusters;
-    int64_t ld_part, ld_copy, copy_at, bytes;
+    int tiles_k, tiles_n, kblocks, clusters, whole, splits, per_split;
+    int64_t ld_copy, copy_at, bytes;
 };
+
+// The pairs of CTAs take the tiles in rounds; what a last, partial round would
+// leave idle is used by splitting its tiles along the rows.  Of the splits
+// into 1 to 16 parts the one with the least estimated time is taken, in
+// stages of the contraction (0.35 us): the rounds, about 8 stages for each
+// item's start and end, and for a split the writing and joining of its parts
+// (0.5 MB each, about 0.3 stages) and one more launch (10 stages).
+void split_rest(Plan *p)
+{
+    const int tiles = p->tiles_k * p->tiles_n;
+    p->whole = tiles / p->clusters * p->clusters;
+    const int rest = tiles - p->whole;
+    p->splits = 1;
+    p->per_split = p->kblocks;
+    if (rest == 0 || p->kblocks == 0) return;
+    double best = p->kblocks + 8;
+    for (int s = 2; s <= 16 && s * 4 <= p->kblocks; ++s) {
+        const int per = (p->kblocks + s - 1) / s, parts = (p->kblocks + per - 1) / per;
+        const int rounds = (rest * parts + p->clusters - 1) / p->clusters;
+        const double cost = (double)rounds * (per + 8) + 0.3 * rest * parts + 10;
+        if (cost < best) {
+            best = cost;
+            p->splits = parts;
+            p->per_split = per;
+        }
+    }
+    if (p->splits == 1) p->whole = tiles;
+}
 
 int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p)
 {
@@ -661,17 +745,12 @@ int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p
     const int sms = sm_count();
     if (sms == 0) return z1_fail(ZERO1_ECUDA, "%s: no CUDA device", call);
     p->clusters = sms / 2;
-    const int64_t tiles = tk * tn;
-    int64_t splits = tiles < p->clusters ? p->clusters / tiles : 1;
-    if (splits > kb / 4) splits = kb / 4;  // at least four stages each
-    if (splits < 1) splits = 1;
-    p->per_split = (int)((kb + splits - 1) / splits);
-    p->splits = p->per_split ? (int)((kb + p->per_split - 1) / p->per_split) : 0;
     p->tiles_k = (int)tk;
     p->tiles_n = (int)tn;
     p->kblocks = (int)kb;
-    p->ld_part = round_up(K, 8);
-    p->copy_at = p->splits > 1 ? round_up((int64_t)p->splits * N * p->ld_part * 4, 128) : 0;
+    split_rest(p);
+    const int64_t parts = p->splits > 1 ? (tk * tn - p->whole) * p->splits : 0;
+    p->copy_at = parts * kTileN * kTileK * 4;
     p->ld_copy = round_up(N, 8);
     p->bytes = p->copy_at + (rows_aligned(dy, ld, T) ? 0 : round_up(T * p->ld_copy * 2, 128));
     return ZERO1_OK;
@@ -731,7 +810,8 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Wg a{};
     a.T = T; a.N = n; a.K = K;
-    a.tiles_k = p.tiles_k; a.tiles_n = p.tiles_n; a.splits = p.splits; a.kblocks = p.kblocks; a.per_split = p.per_split;
+    a.tiles_k = p.tiles_k; a.tiles_n = p.tiles_n; a.kblocks = p.kblocks;
+    a.whole = p.whole; a.splits = p.splits; a.per_split = p.per_split;
     a.scale = col_scale;
     a.scale_f32 = scale_dtype == ZERO1_DTYPE_F32;
     a.dw = dw; a.ld_dw = n > 1 ? ld_dw : K;
@@ -739,7 +819,6 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     a.accumulate = accumulate != 0;
     a.pairs = ((uintptr_t)dw & (2 * eo - 1)) == 0 && a.ld_dw % 2 == 0;
     a.part = static_cast<float *>(workspace);
-    a.ld_part = p.ld_part;
     if (T > 0) {
         a.exps = x8->exps;
         a.ld_exps = x8->ld_exps;
@@ -760,22 +839,31 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
             return rc;
         cudaError_t e = cudaFuncSetAttribute(k_weight_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
-        const int64_t items = (int64_t)p.tiles_k * p.tiles_n * p.splits;
+        const int64_t items = p.whole + (int64_t)(p.tiles_k * p.tiles_n - p.whole) * p.splits;
         const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
         k_weight_grad<<<grid, kWgThreads, kWgSmem, st>>>(mdy, mx, a);
         z1_note_launch(reinterpret_cast<const void *>(k_weight_grad), grid, 1, kWgThreads, 0);
         if ((rc = launch_status("weight gradient launch")) != ZERO1_OK || p.splits == 1) return rc;
+    } else {
+        a.whole = a.splits = 0;
     }
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)((K + 511) / 512), (unsigned)(n < 65535 ? n : 65535), (unsigned)((n + 65534) / 65535));
-    lc.blockDim = dim3(256);
-    lc.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, k_weight_grad_join, a);
-    if (e != cudaSuccess) return pdl_fail(e, "weight gradient: joining the splits");
+    // (no rows: every tile is finished here, in runs that fit the grid)
+    for (int t = a.whole, tiles = p.tiles_k * p.tiles_n; t < tiles;) {
+        const int run = tiles - t < 65535 ? tiles - t : 65535;
+        Wg j = a;
+        j.whole = t;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(kTileN / 8, (unsigned)run);
+        lc.blockDim = dim3(256);
+        lc.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = at;
+        lc.numAttrs = 1;
+        const cudaError_t e = cudaLaunchKernelEx(&lc, k_weight_grad_join, j);
+        if (e != cudaSuccess) return pdl_fail(e, "weight gradient: joining the parts");
+        t += run;
+    }
     return ZERO1_OK;
 }
