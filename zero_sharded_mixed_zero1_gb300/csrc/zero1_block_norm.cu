@@ -1,6 +1,7 @@
 // zero1_block_norm.cu - norms before and after a block, fused with the
 // block's gate and residual scale: forward and backward.
 
+#include "zero1_async.cuh"
 #include "zero1_block.cuh"
 
 namespace {
@@ -479,6 +480,339 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
     }
 }
 
+// ------------------------------------------------------- staged backward ---
+//
+// Rows of more than 512 columns that 128-bit accesses can address, up to the
+// widths whose rows fit shared memory.  The inputs of R rows at a time arrive
+// by bulk copies in a ring of shared-memory stages, so that loads are in
+// flight through all phases of a row and both of its sums.  A block of at most
+// 512 threads keeps up to 128 registers per thread: the column sums, and what
+// one phase leaves to the next.  A thread owns C chunks of 8 columns of each
+// of the R rows; two units of work per thread (R C = 2) share one reading of
+// the weights and one barrier per sum.
+
+struct Ring {
+    int stages, stage_bytes, row_bytes;
+    int at_dh, at_dr, at_y, at_r, at_gate;       // offsets in a staged row
+    int by_dh, by_dr, by_y, by_r, by_gate, all;  // bytes of a row's copies (0: none)
+    int at_wpre, at_wpost, at_wgate, at_stage;   // offsets in shared memory
+};
+
+constexpr int kStagedThreads = 512;
+
+// Bytes 16 (bf16) or 32 (fp32) of a staged row.
+template <class T>
+__device__ __forceinline__ void get8(const unsigned char *p, int col, float f[8])
+{
+    if constexpr (sizeof(T) == 2) {
+        unpack8(*reinterpret_cast<const uint4 *>(p + col * 2), f);
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(p + col * 4), b = *reinterpret_cast<const float4 *>(p + col * 4 + 16);
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    }
+}
+__device__ __forceinline__ void get8(const unsigned char *p, int f32, int col, float f[8])
+{
+    if (f32) get8<float>(p, col, f);
+    else get8<uint16_t>(p, col, f);
+}
+
+// Copies a [D] vector (D a multiple of 8) into shared memory in its own type.
+__device__ __forceinline__ void keep_vector(unsigned char *dst, const void *src, int f32, int D)
+{
+    if (!src) return;
+    const int bytes = f32 ? D * 4 : D * 2;
+    if (((uintptr_t)src & 15) == 0) {
+        for (int c = threadIdx.x; c < bytes / 16; c += blockDim.x)
+            reinterpret_cast<uint4 *>(dst)[c] = __ldg(static_cast<const uint4 *>(src) + c);
+    } else if (f32) {
+#pragma unroll 8
+        for (int c = threadIdx.x; c < D; c += blockDim.x)
+            reinterpret_cast<float *>(dst)[c] = __ldg(static_cast<const float *>(src) + c);
+    } else {
+#pragma unroll 8
+        for (int c = threadIdx.x; c < D; c += blockDim.x)
+            reinterpret_cast<uint16_t *>(dst)[c] = __ldg(static_cast<const uint16_t *>(src) + c);
+    }
+}
+
+// What a thread needs of a row besides the staged bytes; fetched a row ahead.
+template <int C>
+struct RowScalars {
+    float rs_pre, rs_post, gate;
+    uint8_t ey[C], er[C];
+};
+
+template <int C>
+__device__ __forceinline__ void load_scalars(const Common &c, const float *rstd_pre, const float *rstd_post, int64_t row,
+                                             int col, int stride, RowScalars<C> &s)
+{
+    s.rs_pre = 0.f;
+    s.rs_post = s.gate = 1.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) s.ey[i] = s.er[i] = 127;
+    if (row >= c.rows) return;
+    if (c.w_pre) s.rs_pre = __ldg(rstd_pre + row);
+    if (c.w_post) s.rs_post = __ldg(rstd_post + row);
+    if (c.gate_kind == ZERO1_GATE_TOKEN) s.gate = ld_param(c.gate, c.gf32, row * c.ld_gate);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int cc = col + i * stride;
+        if (cc >= c.D) continue;
+        const int64_t block = cc / kQBlock;
+        if (c.y8.codes) s.ey[i] = __ldg(c.y8.exps + block * c.y8.ld_exps + row);
+        if (c.r8.codes) s.er[i] = __ldg(c.r8.exps + block * c.r8.ld_exps + row);
+    }
+}
+
+// The sums of R rows over the block, the same in every thread.
+template <int R>
+__device__ __forceinline__ void block_sums(float x[R], float (*red)[32])
+{
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = warp_sum(x[r]);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[r][threadIdx.x >> 5] = x[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = warp_sum(lane < (int)(blockDim.x >> 5) ? red[r][lane] : 0.f);
+}
+
+// GATE: 0 none or one value per row, 1 per channel, 2 per element.
+template <class TA, class TR, int C, int R, int GATE>
+__global__ void __launch_bounds__(kStagedThreads, 1) k_block_norm_bwd_staged(const Common c, const Bwd a, const Ring g)
+{
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red[2][R][32];
+    __shared__ __align__(8) uint64_t full[4];
+    const int tid = threadIdx.x, stride = blockDim.x * 8;
+    const bool pre = c.w_pre, post = c.w_post, r8 = c.r8.codes, y8 = c.y8.codes, ysaved = g.by_y;
+    const bool tok = GATE == 0 && a.need_gate;
+    const int64_t groups = (c.rows + R - 1) / R;
+    auto issue = [&](int64_t group, int st) {
+        const int n = (int)min((int64_t)R, c.rows - group * R);
+        mbar_expect_tx(&full[st], g.all * n);
+        for (int r = 0; r < n; ++r) {
+            const int64_t row = group * R + r;
+            unsigned char *b = smem + g.at_stage + st * g.stage_bytes + r * g.row_bytes;
+            if (g.by_dh) bulk_load(b + g.at_dh, static_cast<const TA *>(a.dh) + row * a.ld_dh, g.by_dh, &full[st]);
+            if (g.by_dr) bulk_load(b + g.at_dr, static_cast<const TR *>(a.dr) + row * a.ld_dr, g.by_dr, &full[st]);
+            if (g.by_y)
+                bulk_load(b + g.at_y, y8 ? (const void *)(c.y8.codes + row * c.y8.ld_codes)
+                                         : (const void *)(static_cast<const TA *>(a.y) + row * a.ld_y),
+                          g.by_y, &full[st]);
+            if (g.by_r)
+                bulk_load(b + g.at_r, r8 ? (const void *)(c.r8.codes + row * c.r8.ld_codes)
+                                         : (const void *)(static_cast<const TR *>(a.r) + row * a.ld_r),
+                          g.by_r, &full[st]);
+            if (g.by_gate)
+                bulk_load(b + g.at_gate, static_cast<const char *>(c.gate) + row * c.ld_gate * (c.gf32 ? 4 : 2), g.by_gate,
+                          &full[st]);
+        }
+    };
+    if (tid == 0) {
+        for (int k = 0; k < g.stages; ++k) mbar_init(&full[k], 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int k = 0; k < g.stages; ++k)
+            if (blockIdx.x + (int64_t)k * gridDim.x < groups) issue(blockIdx.x + (int64_t)k * gridDim.x, k);
+    }
+    keep_vector(smem + g.at_wpre, c.w_pre, c.pf32, c.D);
+    keep_vector(smem + g.at_wpost, c.w_post, c.pf32, c.D);
+    if (GATE == 1) keep_vector(smem + g.at_wgate, c.gate, c.gf32, c.D);
+    float acc_post[C][8] = {}, acc_pre[C][8] = {}, acc_gate[GATE == 1 ? C : 1][8] = {};
+    RowScalars<C> cur[R], next[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) load_scalars<C>(c, a.rstd_pre, a.rstd_post, (int64_t)blockIdx.x * R + r, tid * 8, stride, cur[r]);
+    __syncthreads();
+
+    bool ok = true;
+    int st = 0, lost = 0;
+    uint32_t parity = 0;
+    for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
+        const int64_t row0 = group * R;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            load_scalars<C>(c, a.rstd_pre, a.rstd_post, row0 + (int64_t)gridDim.x * R + r, tid * 8, stride, next[r]);
+        if (ok && !(ok = mbar_wait_long(&full[st], parity))) lost = 2 * st + parity;  // nothing is waited for after that
+        const unsigned char *base = smem + g.at_stage + st * g.stage_bytes;
+        float d[C][R][8], h[C][R][8];  // h: the saved row, first rh, then yh
+
+        float s[R] = {};
+        if (pre) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int col = tid * 8 + i * stride;
+                if (col >= c.D) continue;
+                float w[8];
+                get8(smem + g.at_wpre, c.pf32, col, w);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (row0 + r >= c.rows) continue;
+                    const unsigned char *b = base + r * g.row_bytes;
+                    get8<TA>(b + g.at_dh, col, d[i][r]);
+                    if (r8) {
+                        values8(*reinterpret_cast<const uint2 *>(b + g.at_r + col), scale_of(cur[r].er[i]), h[i][r]);
+                    } else {
+                        get8<TR>(b + g.at_r, col, h[i][r]);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) h[i][r][k] *= cur[r].rs_pre;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        acc_pre[i][k] = fmaf(d[i][r][k], h[i][r][k], acc_pre[i][k]);
+                        d[i][r][k] *= w[k];
+                        s[r] = fmaf(d[i][r][k], h[i][r][k], s[r]);
+                    }
+                }
+            }
+            block_sums<R>(s, red[0]);
+        }
+
+        // d: the gradient of r; then p = a d u, the gradient of the gate's
+        // factor, and a g d, the gradient of u
+        float t[R] = {}, gt[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            gt[r] = c.gate_kind != ZERO1_GATE_TOKEN ? 1.f : c.sigmoid ? sigmoid(cur[r].gate) : cur[r].gate;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = tid * 8 + i * stride;
+            if (col >= c.D) continue;
+            float w[8], gc[8];
+            if (post) {
+                get8(smem + g.at_wpost, c.pf32, col, w);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = 1.f;
+            }
+            if (GATE == 1) {
+                get8(smem + g.at_wgate, c.gf32, col, gc);
+                if (c.sigmoid) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) gc[k] = sigmoid(gc[k]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (row0 + r >= c.rows) continue;
+                const unsigned char *b = base + r * g.row_bytes;
+                float x[8];
+                if (g.by_dr) {
+                    get8<TR>(b + g.at_dr, col, x);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = 0.f;
+                }
+                if (pre) {
+                    const float m = -s[r] * c.inv_d;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[k] = fmaf(cur[r].rs_pre, fmaf(h[i][r][k], m, d[i][r][k]), x[k]);
+                }
+                store8(static_cast<TR *>(a.dx) + (row0 + r) * a.ld_dx + col, x);
+                if (y8) {
+                    values8(*reinterpret_cast<const uint2 *>(b + g.at_y + col), scale_of(cur[r].ey[i]), h[i][r]);
+                } else if (ysaved) {
+                    get8<TA>(b + g.at_y, col, h[i][r]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[i][r][k] *= cur[r].rs_post;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[i][r][k] = 0.f;
+                }
+                if (GATE == 2) {
+                    get8(b + g.at_gate, c.gf32, col, gc);
+                    if (c.sigmoid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) gc[k] = sigmoid(gc[k]);
+                    }
+                }
+                const float ag = GATE == 0 ? c.alpha * gt[r] : c.alpha;
+                float o[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float u = w[k] * h[i][r][k];
+                    float ad = ag * x[k];  // with a token gate's factor
+                    if (GATE == 0) {
+                        t[r] = fmaf(x[k], u, t[r]);  // times a: the token gate's gradient
+                    } else {
+                        const float p = ad * u;
+                        if (GATE == 1) acc_gate[GATE == 1 ? i : 0][k] += p;
+                        o[k] = p;
+                        ad *= gc[k];
+                        t[r] = fmaf(gc[k], p, t[r]);
+                    }
+                    acc_post[i][k] = fmaf(ad, h[i][r][k], acc_post[i][k]);
+                    d[i][r][k] = ad;
+                }
+                if (GATE == 2 && a.need_gate) {
+                    if (c.sigmoid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) o[k] *= gc[k] * (1.f - gc[k]);
+                    }
+                    if (c.gf32) store8(static_cast<float *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
+                    else store8(static_cast<uint16_t *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
+                }
+            }
+        }
+        if (post || tok) block_sums<R>(t, red[1]);
+        if (GATE == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                t[r] *= c.alpha;
+                if (tok && tid == r && row0 + r < c.rows) {
+                    const float dg = c.sigmoid ? t[r] * gt[r] * (1.f - gt[r]) : t[r];
+                    if (c.wf32) static_cast<float *>(a.dgate)[(row0 + r) * a.ld_dgate] = dg;
+                    else static_cast<uint16_t *>(a.dgate)[(row0 + r) * a.ld_dgate] = to_bf16(dg);
+                }
+                t[r] *= gt[r];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = tid * 8 + i * stride;
+            if (col >= c.D) continue;
+            float w[8];
+            if (post) get8(smem + g.at_wpost, c.pf32, col, w);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (row0 + r >= c.rows) continue;
+                if (post) {
+                    const float m = -t[r] * c.inv_d;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) d[i][r][k] = cur[r].rs_post * fmaf(h[i][r][k], m, d[i][r][k] * w[k]);
+                }
+                store8(static_cast<TA *>(a.dy) + (row0 + r) * a.ld_dy + col, d[i][r]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) cur[r] = next[r];
+        __syncthreads();  // the stage has been read
+        if (tid == 0 && ok && group + (int64_t)g.stages * gridDim.x < groups) issue(group + (int64_t)g.stages * gridDim.x, st);
+        if (++st == g.stages) {
+            st = 0;
+            parity ^= 1;
+        }
+    }
+    if (tid == 0 && !ok)  // copies still in flight must land before the block may exit
+        for (int k = lost / 2; k < lost / 2 + g.stages; ++k) mbar_wait(&full[k % g.stages], (lost ^ (k >= g.stages)) & 1);
+    const int64_t plane = (int64_t)gridDim.x * c.D;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int col = tid * 8 + i * stride;
+        if (col >= c.D) continue;
+        float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * c.D + col);
+        auto put = [&](float4 *p, const float f[8]) {
+            p[0] = make_float4(f[0], f[1], f[2], f[3]);
+            p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        };
+        if (a.need_post) put(part, acc_post[i]);
+        if (a.need_pre) put(part + plane / 4, acc_pre[i]);
+        if (GATE == 1 && a.need_gate) put(part + plane / 2, acc_gate[GATE == 1 ? i : 0]);
+    }
+}
+
 // Adds the blocks' partial column sums in block order: 32 columns per block,
 // 8 slices of the partials each summed in order and then joined in order.
 struct Finish {
@@ -528,11 +862,12 @@ __global__ void __launch_bounds__(256) k_block_norm_finish(const Finish f)
 // Threads of a block for D columns: narrow rows take a warp each.
 int row_threads(int64_t D) { return D <= 512 ? 256 : (int)round_up(D, 512) / 16; }
 
-// Blocks of the backward kernel: one resident wave at most.
+// Blocks of the backward kernel: one resident wave at most, with about 512
+// threads per SM at work.
 int64_t bwd_blocks(int64_t rows, int64_t D, int sms)
 {
-    const int64_t per_sm = D <= 512 ? 2 : D <= 4096 ? 512 / row_threads(D) : 1;
-    const int64_t work = D <= 512 ? (rows + kWarpRows - 1) / kWarpRows : rows;
+    const int64_t per_sm = D <= 512 ? 2 : D <= 4096 ? 4096 / round_up(D, 256) : 1;
+    const int64_t work = D <= 512 ? (rows + kWarpRows - 1) / kWarpRows : D <= 4096 ? (rows + 1) / 2 : rows;
     return work < per_sm * sms ? work : per_sm * sms;
 }
 
@@ -664,10 +999,71 @@ int launch_bwd(const Common &c, const Bwd &a, int threads, int64_t grid, cudaStr
     return launch_status("block norm backward launch");
 }
 
+constexpr int kStagedSmem = 220 * 1024;
+
+// The stages of R rows for the staged kernel; false if they do not fit.
+bool ring_of(const Common &c, const Bwd &a, int ea, int er, int R, Ring *g)
+{
+    *g = Ring{};
+    int at = 0;
+    auto place = [&](int *where, int *bytes, int64_t n) {
+        *where = at;
+        *bytes = (int)n;
+        at += (int)round_up(n, 128);
+    };
+    const int D = c.D, eg = c.gf32 ? 4 : 2;
+    const int64_t codes = round_up(D, 16);
+    place(&g->at_dh, &g->by_dh, c.w_pre ? D * ea : 0);
+    place(&g->at_dr, &g->by_dr, a.dr ? D * er : 0);
+    place(&g->at_y, &g->by_y, c.y8.codes ? codes : a.y ? D * ea : 0);
+    place(&g->at_r, &g->by_r, c.r8.codes ? codes : c.w_pre ? D * er : 0);
+    place(&g->at_gate, &g->by_gate, c.gate_kind == ZERO1_GATE_FULL ? D * eg : 0);
+    g->all = g->by_dh + g->by_dr + g->by_y + g->by_r + g->by_gate;
+    g->row_bytes = at;
+    g->stage_bytes = at * R;
+    at = 0;
+    int unused;
+    place(&g->at_wpre, &unused, c.w_pre ? D * (c.pf32 ? 4 : 2) : 0);
+    place(&g->at_wpost, &unused, c.w_post ? D * (c.pf32 ? 4 : 2) : 0);
+    place(&g->at_wgate, &unused, c.gate_kind == ZERO1_GATE_CHANNEL ? D * eg : 0);
+    g->at_stage = at;
+    g->stages = (kStagedSmem - at) / (g->stage_bytes > 0 ? g->stage_bytes : 1);
+    if (g->stages > 4) g->stages = 4;
+    return g->stages >= 1 && g->all > 0;
+}
+
+template <class TA, class TR, int C, int R>
+int launch_bwd_staged(const Common &c, const Bwd &a, const Ring &g, int threads, int64_t grid, cudaStream_t st)
+{
+    auto go = [&](auto kernel) {
+        const int smem = g.at_stage + g.stages * g.stage_bytes;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "block norm backward: %s", cudaGetErrorString(e));
+        kernel<<<(unsigned)grid, threads, smem, st>>>(c, a, g);
+        z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, 1, threads, 0);
+        return launch_status("block norm backward launch");
+    };
+    if (c.gate_kind == ZERO1_GATE_CHANNEL) return go(k_block_norm_bwd_staged<TA, TR, C, R, 1>);
+    if (c.gate_kind == ZERO1_GATE_FULL) return go(k_block_norm_bwd_staged<TA, TR, C, R, 2>);
+    return go(k_block_norm_bwd_staged<TA, TR, C, R, 0>);
+}
+
 template <class TA, class TR, bool VEC>
 int pick_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
 {
     const int threads = row_threads(c.D);
+    if constexpr (VEC) {
+        Ring g;
+        const bool fits = c.D > 512 && c.D <= 8192 && (c.gate_kind != ZERO1_GATE_FULL || (c.gvec && (!a.need_gate || a.dgvec)));
+        const int n = (int)round_up(c.D, 256) / 8;
+        const int ea = sizeof(TA), er = sizeof(TR);
+        if (fits && n <= kStagedThreads) {
+            if (ring_of(c, a, ea, er, 2, &g) && g.stages >= 2) return launch_bwd_staged<TA, TR, 1, 2>(c, a, g, n, grid, st);
+            if (ring_of(c, a, ea, er, 1, &g)) return launch_bwd_staged<TA, TR, 1, 1>(c, a, g, n, grid, st);
+        } else if (fits && ring_of(c, a, ea, er, 1, &g)) {
+            return launch_bwd_staged<TA, TR, 2, 1>(c, a, g, (int)round_up(c.D, 512) / 16, grid, st);
+        }
+    }
     if (c.D <= 256) return launch_bwd<TA, TR, 8, VEC, true, false>(c, a, threads, grid, st);
     if (c.D <= 512) return launch_bwd<TA, TR, 16, VEC, true, false>(c, a, threads, grid, st);
     if (c.D <= 8192) return launch_bwd<TA, TR, 16, VEC, false, false>(c, a, threads, grid, st);
