@@ -140,6 +140,160 @@ struct Ckpt {
     int64_t ld_codes, ld_exps;
 };
 
+// ------------------------------------------------------------ fp32 pairs ---
+//
+// Eight fp32 values as four packed pairs: the .f32x2 instructions do two
+// roundings each, the same ones as their scalar forms.
+
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(uint64_t p)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+struct V8 {
+    uint64_t p[4];
+};
+
+__device__ __forceinline__ V8 splat8(float x)
+{
+    const uint64_t p = pair(x, x);
+    return V8{{p, p, p, p}};
+}
+__device__ __forceinline__ V8 mul8(const V8 &a, const V8 &b)
+{
+    return V8{{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]), mul2(a.p[3], b.p[3])}};
+}
+__device__ __forceinline__ V8 mul8(const V8 &a, float s)
+{
+    const uint64_t p = pair(s, s);
+    return V8{{mul2(a.p[0], p), mul2(a.p[1], p), mul2(a.p[2], p), mul2(a.p[3], p)}};
+}
+__device__ __forceinline__ V8 fma8(const V8 &a, const V8 &b, const V8 &c)
+{
+    return V8{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1]), fma2(a.p[2], b.p[2], c.p[2]),
+               fma2(a.p[3], b.p[3], c.p[3])}};
+}
+__device__ __forceinline__ V8 fma8(const V8 &a, float s, const V8 &c)
+{
+    const uint64_t p = pair(s, s);
+    return V8{{fma2(a.p[0], p, c.p[0]), fma2(a.p[1], p, c.p[1]), fma2(a.p[2], p, c.p[2]), fma2(a.p[3], p, c.p[3])}};
+}
+__device__ __forceinline__ V8 add8(const V8 &a, const V8 &b)
+{
+    return V8{{add2(a.p[0], b.p[0]), add2(a.p[1], b.p[1]), add2(a.p[2], b.p[2]), add2(a.p[3], b.p[3])}};
+}
+// The sum of a . b.
+__device__ __forceinline__ float dot8(const V8 &a, const V8 &b)
+{
+    const uint64_t x = fma2(a.p[1], b.p[1], mul2(a.p[0], b.p[0])), y = fma2(a.p[3], b.p[3], mul2(a.p[2], b.p[2]));
+    const float2 s = split(add2(x, y));
+    return s.x + s.y;
+}
+template <class F>
+__device__ __forceinline__ V8 map8(const V8 &a, F &&f)
+{
+    V8 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = split(a.p[k]);
+        r.p[k] = pair(f(v.x), f(v.y));
+    }
+    return r;
+}
+
+__device__ __forceinline__ V8 from_bf16(const uint4 q)
+{
+    return V8{{pair(bf_lo(q.x), bf_hi(q.x)), pair(bf_lo(q.y), bf_hi(q.y)), pair(bf_lo(q.z), bf_hi(q.z)),
+               pair(bf_lo(q.w), bf_hi(q.w))}};
+}
+
+// Eight values of a row in shared memory.
+template <class T>
+__device__ __forceinline__ V8 take8(const unsigned char *row, int col)
+{
+    if constexpr (sizeof(T) == 2) {
+        return from_bf16(*reinterpret_cast<const uint4 *>(row + col * 2));
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(row + col * 4), b = *reinterpret_cast<const float4 *>(row + col * 4 + 16);
+        return V8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+    }
+}
+__device__ __forceinline__ V8 take8(const unsigned char *row, int f32, int col)
+{
+    return f32 ? take8<float>(row, col) : take8<uint16_t>(row, col);
+}
+
+// The values of eight codes.
+__device__ __forceinline__ V8 take_codes(const unsigned char *p, float scale)
+{
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    const uint64_t s = pair(scale, scale);
+    const float2 a = value2((uint16_t)q.x), b = value2((uint16_t)(q.x >> 16)), c = value2((uint16_t)q.y),
+                 d = value2((uint16_t)(q.y >> 16));
+    return V8{{mul2(pair(a.x, a.y), s), mul2(pair(b.x, b.y), s), mul2(pair(c.x, c.y), s), mul2(pair(d.x, d.y), s)}};
+}
+
+__device__ __forceinline__ void put8(uint16_t *p, const V8 &v)
+{
+    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
+    __stcs(reinterpret_cast<uint4 *>(p),
+           make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y)));
+}
+__device__ __forceinline__ void put8(float *p, const V8 &v)
+{
+    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
+    st_stream(p, a.x, a.y, b.x, b.y);
+    st_stream(p + 4, c.x, c.y, d.x, d.y);
+}
+
+// The larger magnitude of three, NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Eight values of a 128-column block that 16 lanes hold, as codes; the block's
+// biased scale exponent in E.
+__device__ __forceinline__ uint2 encode8(const V8 &v, int &E)
+{
+    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
+    const float m = max_abs(max_abs(a.x, a.y, b.x), max_abs(b.y, c.x, c.y), max_abs(d.x, d.y, 0.f));
+    E = scale_exp(max16(mag_bits(m)));
+    const float inv = scale_inv(E);
+    const V8 q = mul8(v, inv);
+    const float2 e = split(q.p[0]), f = split(q.p[1]), g = split(q.p[2]), h = split(q.p[3]);
+    const uint2 r = make_uint2(code2(e.x, e.y) | code2(f.x, f.y) << 16, code2(g.x, g.y) | code2(h.x, h.y) << 16);
+    return E == kNanE ? make_uint2(0, 0) : r;
+}
+
 // ------------------------------------------------------------ host checks --
 
 int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }

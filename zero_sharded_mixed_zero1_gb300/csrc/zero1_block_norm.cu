@@ -1,7 +1,6 @@
 // zero1_block_norm.cu - norms before and after a block, fused with the
 // block's gate and residual scale: forward and backward.
 
-#include "zero1_async.cuh"
 #include "zero1_block.cuh"
 
 namespace {
@@ -483,161 +482,244 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
 // ------------------------------------------------------- staged backward ---
 //
 // Rows of more than 512 columns that 128-bit accesses can address, up to the
-// widths whose rows fit shared memory.  The inputs of R rows at a time arrive
-// by bulk copies in a ring of shared-memory stages, so that loads are in
-// flight through all phases of a row and both of its sums.  A block of at most
-// 512 threads keeps up to 128 registers per thread: the column sums, and what
-// one phase leaves to the next.  A thread owns C chunks of 8 columns of each
-// of the R rows; two units of work per thread (R C = 2) share one reading of
-// the weights and one barrier per sum.
+// widths whose rows fit shared memory.  The inputs of R rows at a time travel
+// through a ring of shared-memory stages, so that loads are in flight through
+// all phases of a row and both of its sums.  A thread copies its own columns
+// (cp.async) and reads only those, so the ring needs no barrier.  Bulk copies
+// of whole rows were slower: about 12 bytes per cycle and SM came in (90 us at
+// 8192 x 4096), however many were in flight.
+//
+// A block of at most 512 threads keeps up to 128 registers per thread: the
+// column sums, and what one phase leaves to the next.  A thread owns C chunks
+// of 8 columns of each of the R rows; two units of work per thread (R C = 2)
+// share one reading of the weights and one barrier per sum.
 
 struct Ring {
     int stages, stage_bytes, row_bytes;
     int at_dh, at_dr, at_y, at_r, at_gate;       // offsets in a staged row
-    int by_dh, by_dr, by_y, by_r, by_gate, all;  // bytes of a row's copies (0: none)
+    int by_dh, by_dr, by_y, by_r, by_gate;       // bytes of a row's inputs (0: none)
     int at_wpre, at_wpost, at_wgate, at_stage;   // offsets in shared memory
 };
 
 constexpr int kStagedThreads = 512;
 
-// Bytes 16 (bf16) or 32 (fp32) of a staged row.
-template <class T>
-__device__ __forceinline__ void get8(const unsigned char *p, int col, float f[8])
-{
-    if constexpr (sizeof(T) == 2) {
-        unpack8(*reinterpret_cast<const uint4 *>(p + col * 2), f);
-    } else {
-        const float4 a = *reinterpret_cast<const float4 *>(p + col * 4), b = *reinterpret_cast<const float4 *>(p + col * 4 + 16);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    }
-}
-__device__ __forceinline__ void get8(const unsigned char *p, int f32, int col, float f[8])
-{
-    if (f32) get8<float>(p, col, f);
-    else get8<uint16_t>(p, col, f);
-}
-
-// Copies a [D] vector (D a multiple of 8) into shared memory in its own type.
-__device__ __forceinline__ void keep_vector(unsigned char *dst, const void *src, int f32, int D)
+// Keeps a [D] vector (D a multiple of 8) in shared memory as fp32 values,
+// through the logistic function if asked: the first four values of each eight,
+// then the last four, so that a warp's 16-byte reads touch every bank once.
+__device__ __forceinline__ void keep_vector(float *dst, const void *src, int f32, int D, int act)
 {
     if (!src) return;
-    const int bytes = f32 ? D * 4 : D * 2;
-    if (((uintptr_t)src & 15) == 0) {
-        for (int c = threadIdx.x; c < bytes / 16; c += blockDim.x)
-            reinterpret_cast<uint4 *>(dst)[c] = __ldg(static_cast<const uint4 *>(src) + c);
-    } else if (f32) {
-#pragma unroll 8
-        for (int c = threadIdx.x; c < D; c += blockDim.x)
-            reinterpret_cast<float *>(dst)[c] = __ldg(static_cast<const float *>(src) + c);
-    } else {
-#pragma unroll 8
-        for (int c = threadIdx.x; c < D; c += blockDim.x)
-            reinterpret_cast<uint16_t *>(dst)[c] = __ldg(static_cast<const uint16_t *>(src) + c);
+    const bool vec = ((uintptr_t)src & 15) == 0;
+    for (int c = threadIdx.x * 8; c < D; c += blockDim.x * 8) {
+        float f[8];
+        param8<true>(src, f32, vec, 0, c, D, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = act ? sigmoid(f[k]) : f[k];
+        *reinterpret_cast<float4 *>(dst + c / 2) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4 *>(dst + D / 2 + c / 2) = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
+__device__ __forceinline__ V8 kept8(const unsigned char *kept, int col, int D)
+{
+    const float4 a = *reinterpret_cast<const float4 *>(kept + col * 2), b = *reinterpret_cast<const float4 *>(kept + D * 2 + col * 2);
+    return V8{{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+}
 
-// What a thread needs of a row besides the staged bytes; fetched a row ahead.
-template <int C>
+// Loads that stay where they are written, ahead of the wait for a stage: the
+// compiler would move plain ones down to their use a group later, and their
+// latency with them (24 us of 90 at 8192 x 4096).
+__device__ __forceinline__ float ld_ahead(const float *p)
+{
+    float x;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ uint16_t ld_ahead(const uint16_t *p)
+{
+    uint16_t x;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(x) : "l"(p));
+    return x;
+}
+__device__ __forceinline__ uint16_t ld_ahead(const uint8_t *p)
+{
+    uint16_t x;
+    asm volatile("{ .reg .u16 t; ld.global.nc.u8 t, [%1]; mov.u16 %0, t; }" : "=h"(x) : "l"(p));
+    return x;
+}
+
+// What a thread needs of a group of rows besides the staged bytes, fetched a
+// group ahead.
+template <int C, int R>
 struct RowScalars {
-    float rs_pre, rs_post, gate;
-    uint8_t ey[C], er[C];
+    float rs_pre[R], rs_post[R], gate[R];
+    uint16_t ey[C], er[C];  // the scale bytes of the group's rows
 };
 
-template <int C>
-__device__ __forceinline__ void load_scalars(const Common &c, const float *rstd_pre, const float *rstd_post, int64_t row,
-                                             int col, int stride, RowScalars<C> &s)
+// Those of the group that starts at row (a row within the matrix; a missing
+// second row gets the first one's values).
+template <int C, int R>
+__device__ __forceinline__ void load_scalars(const Common &c, bool pre, bool post, const float *rstd_pre, const float *rstd_post,
+                                             const uint8_t *const (&ey)[C], const uint8_t *const (&er)[C], int64_t row,
+                                             RowScalars<C, R> &s)
 {
-    s.rs_pre = 0.f;
-    s.rs_post = s.gate = 1.f;
+    const int more = row + 1 < c.rows ? 1 : 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) s.ey[i] = s.er[i] = 127;
-    if (row >= c.rows) return;
-    if (c.w_pre) s.rs_pre = __ldg(rstd_pre + row);
-    if (c.w_post) s.rs_post = __ldg(rstd_post + row);
-    if (c.gate_kind == ZERO1_GATE_TOKEN) s.gate = ld_param(c.gate, c.gf32, row * c.ld_gate);
+    for (int r = 0; r < R; ++r) {
+        s.rs_pre[r] = pre ? ld_ahead(rstd_pre + row + r * more) : 0.f;
+        s.rs_post[r] = post ? ld_ahead(rstd_post + row + r * more) : 1.f;
+        s.gate[r] = c.gate_kind == ZERO1_GATE_TOKEN ? ld_param(c.gate, c.gf32, (row + r * more) * c.ld_gate) : 1.f;
+    }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int cc = col + i * stride;
-        if (cc >= c.D) continue;
-        const int64_t block = cc / kQBlock;
-        if (c.y8.codes) s.ey[i] = __ldg(c.y8.exps + block * c.y8.ld_exps + row);
-        if (c.r8.codes) s.er[i] = __ldg(c.r8.exps + block * c.r8.ld_exps + row);
+        if (R == 2) {  // row is even, and the scales of a block are padded to 128 rows
+            if (ey[i]) s.ey[i] = ld_ahead(reinterpret_cast<const uint16_t *>(ey[i] + row));
+            if (er[i]) s.er[i] = ld_ahead(reinterpret_cast<const uint16_t *>(er[i] + row));
+            if (!more) {
+                s.ey[i] = (uint16_t)((s.ey[i] & 255) * 257);
+                s.er[i] = (uint16_t)((s.er[i] & 255) * 257);
+            }
+        } else {
+            if (ey[i]) s.ey[i] = ld_ahead(ey[i] + row);
+            if (er[i]) s.er[i] = ld_ahead(er[i] + row);
+        }
     }
 }
 
-// The sums of R rows over the block, the same in every thread.
-template <int R>
-__device__ __forceinline__ void block_sums(float x[R], float (*red)[32])
+// A thread's column of scales, or NULL.
+__device__ __forceinline__ const uint8_t *scale_column(const Ckpt &k, int col, int D)
 {
-#pragma unroll
-    for (int r = 0; r < R; ++r) x[r] = warp_sum(x[r]);
-    const int lane = threadIdx.x & 31;
-    if (lane == 0)
-#pragma unroll
-        for (int r = 0; r < R; ++r) red[r][threadIdx.x >> 5] = x[r];
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < R; ++r) x[r] = warp_sum(lane < (int)(blockDim.x >> 5) ? red[r][lane] : 0.f);
+    return k.codes && col < D ? k.exps + (int64_t)(col / kQBlock) * k.ld_exps : nullptr;
 }
 
-// GATE: 0 none or one value per row, 1 per channel, 2 per element.
-template <class TA, class TR, int C, int R, int GATE>
+// The sums of R rows over the block (at most 16 warps), the same in every thread.
+template <int R>
+__device__ __forceinline__ void block_sums(float x[R], float *red)
+{
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if constexpr (R == 2) {
+        // from the first step on, the lower lanes carry row 0 and the upper ones row 1
+        const bool hi = lane >= 16;
+        const float got = __shfl_xor_sync(0xffffffffu, hi ? x[0] : x[1], 16);
+        float y = (hi ? x[1] : x[0]) + got;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        if ((lane & 15) == 0) red[(lane & 16) + (threadIdx.x >> 5)] = y;
+        __syncthreads();
+        y = (lane & 15) < warps ? red[lane] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        x[0] = __shfl_sync(0xffffffffu, y, 0);
+        x[1] = __shfl_sync(0xffffffffu, y, 16);
+    } else {
+        float y = warp_sum(x[0]);
+        if (lane == 0) red[threadIdx.x >> 5] = y;
+        __syncthreads();
+        y = (lane & 15) < warps ? red[lane & 15] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+        x[0] = y;
+    }
+}
+
+// Starts copying N bytes (8 or 16) to shared memory; zeros if `there` is false.
+template <int N>
+__device__ __forceinline__ void copy_ahead(unsigned char *dst, const void *src, bool there)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const int n = there ? N : 0;
+    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
+}
+// Eight elements of a row.
+template <class T>
+__device__ __forceinline__ void copy8_ahead(unsigned char *row, const T *src, int col, bool there)
+{
+    copy_ahead<16>(row + col * sizeof(T), src + col, there);
+    if (sizeof(T) == 4) copy_ahead<16>(row + col * sizeof(T) + 16, src + col + 4, there);
+}
+__device__ __forceinline__ void copies_end_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until at most the `left` latest groups of copies are still under way.
+__device__ __forceinline__ void copies_wait(int left)
+{
+    if (left <= 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// GATE: 0 none or one value per row, 1 per channel, 2 per element.  SAVED: 1
+// both norms and dr are there and both saved activations are checkpoints, 2
+// the same with tensors, 0 any other mix, decided at run time.
+template <class TA, class TR, int C, int R, int GATE, int SAVED>
 __global__ void __launch_bounds__(kStagedThreads, 1) k_block_norm_bwd_staged(const Common c, const Bwd a, const Ring g)
 {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float red[2][R][32];
-    __shared__ __align__(8) uint64_t full[4];
+    __shared__ float red[2][2][32];
     const int tid = threadIdx.x, stride = blockDim.x * 8;
-    const bool pre = c.w_pre, post = c.w_post, r8 = c.r8.codes, y8 = c.y8.codes, ysaved = g.by_y;
+    const bool pre = SAVED || c.w_pre, post = SAVED || c.w_post, dr = SAVED || a.dr;
+    const bool r8 = SAVED ? SAVED == 1 : c.r8.codes != nullptr, y8 = SAVED ? SAVED == 1 : c.y8.codes != nullptr;
+    const bool ysaved = SAVED || g.by_y;
     const bool tok = GATE == 0 && a.need_gate;
     const int64_t groups = (c.rows + R - 1) / R;
-    auto issue = [&](int64_t group, int st) {
-        const int n = (int)min((int64_t)R, c.rows - group * R);
-        mbar_expect_tx(&full[st], g.all * n);
-        for (int r = 0; r < n; ++r) {
-            const int64_t row = group * R + r;
-            unsigned char *b = smem + g.at_stage + st * g.stage_bytes + r * g.row_bytes;
-            if (g.by_dh) bulk_load(b + g.at_dh, static_cast<const TA *>(a.dh) + row * a.ld_dh, g.by_dh, &full[st]);
-            if (g.by_dr) bulk_load(b + g.at_dr, static_cast<const TR *>(a.dr) + row * a.ld_dr, g.by_dr, &full[st]);
-            if (g.by_y)
-                bulk_load(b + g.at_y, y8 ? (const void *)(c.y8.codes + row * c.y8.ld_codes)
-                                         : (const void *)(static_cast<const TA *>(a.y) + row * a.ld_y),
-                          g.by_y, &full[st]);
-            if (g.by_r)
-                bulk_load(b + g.at_r, r8 ? (const void *)(c.r8.codes + row * c.r8.ld_codes)
-                                         : (const void *)(static_cast<const TR *>(a.r) + row * a.ld_r),
-                          g.by_r, &full[st]);
-            if (g.by_gate)
-                bulk_load(b + g.at_gate, static_cast<const char *>(c.gate) + row * c.ld_gate * (c.gf32 ? 4 : 2), g.by_gate,
-                          &full[st]);
-        }
-    };
-    if (tid == 0) {
-        for (int k = 0; k < g.stages; ++k) mbar_init(&full[k], 1);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        for (int k = 0; k < g.stages; ++k)
-            if (blockIdx.x + (int64_t)k * gridDim.x < groups) issue(blockIdx.x + (int64_t)k * gridDim.x, k);
-    }
-    keep_vector(smem + g.at_wpre, c.w_pre, c.pf32, c.D);
-    keep_vector(smem + g.at_wpost, c.w_post, c.pf32, c.D);
-    if (GATE == 1) keep_vector(smem + g.at_wgate, c.gate, c.gf32, c.D);
-    float acc_post[C][8] = {}, acc_pre[C][8] = {}, acc_gate[GATE == 1 ? C : 1][8] = {};
-    RowScalars<C> cur[R], next[R];
+    // Starts the copies of a group of rows; past the last group, an empty group
+    // of copies that keeps the count.
+    auto fetch = [&](int64_t group, int st) {
+        if (group < groups) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) load_scalars<C>(c, a.rstd_pre, a.rstd_post, (int64_t)blockIdx.x * R + r, tid * 8, stride, cur[r]);
+            for (int r = 0; r < R; ++r) {
+                const bool there = r == 0 || group * R + r < c.rows;
+                const int64_t row = group * R + (there ? r : 0);
+                unsigned char *b = smem + g.at_stage + st * g.stage_bytes + r * g.row_bytes;
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    const int col = tid * 8 + i * stride;
+                    if (col >= c.D) continue;
+                    if (pre) {
+                        copy8_ahead(b + g.at_dh, static_cast<const TA *>(a.dh) + row * a.ld_dh, col, there);
+                        if (r8) copy_ahead<8>(b + g.at_r + col, c.r8.codes + row * c.r8.ld_codes + col, there);
+                        else copy8_ahead(b + g.at_r, static_cast<const TR *>(a.r) + row * a.ld_r, col, there);
+                    }
+                    if (dr) copy8_ahead(b + g.at_dr, static_cast<const TR *>(a.dr) + row * a.ld_dr, col, there);
+                    if (y8) copy_ahead<8>(b + g.at_y + col, c.y8.codes + row * c.y8.ld_codes + col, there);
+                    else if (ysaved) copy8_ahead(b + g.at_y, static_cast<const TA *>(a.y) + row * a.ld_y, col, there);
+                    if (GATE == 2) {
+                        if (c.gf32) copy8_ahead(b + g.at_gate, static_cast<const float *>(c.gate) + row * c.ld_gate, col, there);
+                        else copy8_ahead(b + g.at_gate, static_cast<const uint16_t *>(c.gate) + row * c.ld_gate, col, there);
+                    }
+                }
+            }
+        }
+        copies_end_group();
+    };
+    for (int k = 0; k + 1 < g.stages; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, k);
+    keep_vector(reinterpret_cast<float *>(smem + g.at_wpre), c.w_pre, c.pf32, c.D, 0);
+    keep_vector(reinterpret_cast<float *>(smem + g.at_wpost), c.w_post, c.pf32, c.D, 0);
+    if (GATE == 1) keep_vector(reinterpret_cast<float *>(smem + g.at_wgate), c.gate, c.gf32, c.D, c.sigmoid);
+    V8 acc_post[C], acc_pre[C], acc_gate[GATE == 1 ? C : 1];
+    const uint8_t *ey[C], *er[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        acc_post[i] = acc_pre[i] = acc_gate[GATE == 1 ? i : 0] = splat8(0.f);
+        ey[i] = scale_column(c.y8, tid * 8 + i * stride, c.D);
+        er[i] = scale_column(c.r8, tid * 8 + i * stride, c.D);
+    }
+    RowScalars<C, R> cur, next;
+    load_scalars<C, R>(c, pre, post, a.rstd_pre, a.rstd_post, ey, er, (int64_t)blockIdx.x * R, cur);
     __syncthreads();
 
-    bool ok = true;
-    int st = 0, lost = 0;
-    uint32_t parity = 0;
+    int st = 0, flip = 0;
     for (int64_t group = blockIdx.x; group < groups; group += gridDim.x) {
         const int64_t row0 = group * R;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            load_scalars<C>(c, a.rstd_pre, a.rstd_post, row0 + (int64_t)gridDim.x * R + r, tid * 8, stride, next[r]);
-        if (ok && !(ok = mbar_wait_long(&full[st], parity))) lost = 2 * st + parity;  // nothing is waited for after that
+        {
+            const int64_t following = group + gridDim.x;
+            load_scalars<C, R>(c, pre, post, a.rstd_pre, a.rstd_post, ey, er, (following < groups ? following : group) * R, next);
+        }
+        // the stage that this thread has read a group ago is filled again
+        fetch(group + (int64_t)(g.stages - 1) * gridDim.x, st == 0 ? g.stages - 1 : st - 1);
+        copies_wait(g.stages - 1);
         const unsigned char *base = smem + g.at_stage + st * g.stage_bytes;
-        float d[C][R][8], h[C][R][8];  // h: the saved row, first rh, then yh
+        const bool both = R == 1 || row0 + 1 < c.rows;  // a missing second row counts as zeros
+        V8 d[C][R], h[C][R];  // h: the saved row, first rh, then yh
 
         float s[R] = {};
         if (pre) {
@@ -645,123 +727,72 @@ __global__ void __launch_bounds__(kStagedThreads, 1) k_block_norm_bwd_staged(con
             for (int i = 0; i < C; ++i) {
                 const int col = tid * 8 + i * stride;
                 if (col >= c.D) continue;
-                float w[8];
-                get8(smem + g.at_wpre, c.pf32, col, w);
+                const V8 w = kept8(smem + g.at_wpre, col, c.D);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    if (row0 + r >= c.rows) continue;
                     const unsigned char *b = base + r * g.row_bytes;
-                    get8<TA>(b + g.at_dh, col, d[i][r]);
-                    if (r8) {
-                        values8(*reinterpret_cast<const uint2 *>(b + g.at_r + col), scale_of(cur[r].er[i]), h[i][r]);
-                    } else {
-                        get8<TR>(b + g.at_r, col, h[i][r]);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) h[i][r][k] *= cur[r].rs_pre;
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        acc_pre[i][k] = fmaf(d[i][r][k], h[i][r][k], acc_pre[i][k]);
-                        d[i][r][k] *= w[k];
-                        s[r] = fmaf(d[i][r][k], h[i][r][k], s[r]);
-                    }
+                    d[i][r] = take8<TA>(b + g.at_dh, col);
+                    if (r8) h[i][r] = take_codes(b + g.at_r + col, scale_of((cur.er[i] >> (8 * r)) & 255));
+                    else h[i][r] = mul8(take8<TR>(b + g.at_r, col), cur.rs_pre[r]);
+                    acc_pre[i] = fma8(d[i][r], h[i][r], acc_pre[i]);
+                    d[i][r] = mul8(d[i][r], w);
+                    s[r] += dot8(d[i][r], h[i][r]);
                 }
             }
-            block_sums<R>(s, red[0]);
+            block_sums<R>(s, red[flip][0]);
         }
 
-        // d: the gradient of r; then p = a d u, the gradient of the gate's
-        // factor, and a g d, the gradient of u
+        // x: the gradient of r; then p = a x u, the gradient of the gate's
+        // factor, and d = a g x, the gradient of u
         float t[R] = {}, gt[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            gt[r] = c.gate_kind != ZERO1_GATE_TOKEN ? 1.f : c.sigmoid ? sigmoid(cur[r].gate) : cur[r].gate;
+            gt[r] = GATE || c.gate_kind != ZERO1_GATE_TOKEN ? 1.f : c.sigmoid ? sigmoid(cur.gate[r]) : cur.gate[r];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int col = tid * 8 + i * stride;
             if (col >= c.D) continue;
-            float w[8], gc[8];
-            if (post) {
-                get8(smem + g.at_wpost, c.pf32, col, w);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = 1.f;
-            }
-            if (GATE == 1) {
-                get8(smem + g.at_wgate, c.gf32, col, gc);
-                if (c.sigmoid) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) gc[k] = sigmoid(gc[k]);
-                }
-            }
+            const V8 w = post ? kept8(smem + g.at_wpost, col, c.D) : splat8(1.f);
+            V8 gc = w;
+            if (GATE == 1) gc = kept8(smem + g.at_wgate, col, c.D);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (row0 + r >= c.rows) continue;
                 const unsigned char *b = base + r * g.row_bytes;
-                float x[8];
-                if (g.by_dr) {
-                    get8<TR>(b + g.at_dr, col, x);
+                const bool there = r == 0 || both;
+                V8 x = dr ? take8<TR>(b + g.at_dr, col) : splat8(0.f);
+                if (pre) x = fma8(fma8(h[i][r], -s[r] * c.inv_d, d[i][r]), cur.rs_pre[r], x);
+                if (there) put8(static_cast<TR *>(a.dx) + (row0 + r) * a.ld_dx + col, x);
+                if (y8) h[i][r] = take_codes(b + g.at_y + col, scale_of((cur.ey[i] >> (8 * r)) & 255));
+                else if (ysaved) h[i][r] = mul8(take8<TA>(b + g.at_y, col), cur.rs_post[r]);
+                else h[i][r] = splat8(0.f);
+                const V8 u = mul8(w, h[i][r]);
+                if (GATE == 0) {
+                    t[r] += dot8(x, u);  // times a: the gradient of a token's gate
+                    d[i][r] = mul8(x, c.alpha * gt[r]);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = 0.f;
-                }
-                if (pre) {
-                    const float m = -s[r] * c.inv_d;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = fmaf(cur[r].rs_pre, fmaf(h[i][r][k], m, d[i][r][k]), x[k]);
-                }
-                store8(static_cast<TR *>(a.dx) + (row0 + r) * a.ld_dx + col, x);
-                if (y8) {
-                    values8(*reinterpret_cast<const uint2 *>(b + g.at_y + col), scale_of(cur[r].ey[i]), h[i][r]);
-                } else if (ysaved) {
-                    get8<TA>(b + g.at_y, col, h[i][r]);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) h[i][r][k] *= cur[r].rs_post;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) h[i][r][k] = 0.f;
-                }
-                if (GATE == 2) {
-                    get8(b + g.at_gate, c.gf32, col, gc);
-                    if (c.sigmoid) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) gc[k] = sigmoid(gc[k]);
+                    if (GATE == 2) {
+                        gc = take8(b + g.at_gate, c.gf32, col);
+                        if (c.sigmoid) gc = map8(gc, [](float v) { return sigmoid(v); });
+                    }
+                    const V8 ax = mul8(x, c.alpha), p = mul8(ax, u);
+                    if (GATE == 1) acc_gate[GATE == 1 ? i : 0] = add8(acc_gate[GATE == 1 ? i : 0], p);
+                    t[r] += dot8(gc, p);
+                    d[i][r] = mul8(ax, gc);
+                    if (GATE == 2 && a.need_gate && there) {
+                        const V8 o = c.sigmoid ? mul8(p, map8(gc, [](float v) { return v * (1.f - v); })) : p;
+                        if (c.gf32) put8(static_cast<float *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
+                        else put8(static_cast<uint16_t *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
                     }
                 }
-                const float ag = GATE == 0 ? c.alpha * gt[r] : c.alpha;
-                float o[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float u = w[k] * h[i][r][k];
-                    float ad = ag * x[k];  // with a token gate's factor
-                    if (GATE == 0) {
-                        t[r] = fmaf(x[k], u, t[r]);  // times a: the token gate's gradient
-                    } else {
-                        const float p = ad * u;
-                        if (GATE == 1) acc_gate[GATE == 1 ? i : 0][k] += p;
-                        o[k] = p;
-                        ad *= gc[k];
-                        t[r] = fmaf(gc[k], p, t[r]);
-                    }
-                    acc_post[i][k] = fmaf(ad, h[i][r][k], acc_post[i][k]);
-                    d[i][r][k] = ad;
-                }
-                if (GATE == 2 && a.need_gate) {
-                    if (c.sigmoid) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) o[k] *= gc[k] * (1.f - gc[k]);
-                    }
-                    if (c.gf32) store8(static_cast<float *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
-                    else store8(static_cast<uint16_t *>(a.dgate) + (row0 + r) * a.ld_dgate + col, o);
-                }
+                acc_post[i] = fma8(d[i][r], h[i][r], acc_post[i]);
             }
         }
-        if (post || tok) block_sums<R>(t, red[1]);
+        if (post || tok) block_sums<R>(t, red[flip][1]);
         if (GATE == 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 t[r] *= c.alpha;
-                if (tok && tid == r && row0 + r < c.rows) {
+                if (tok && tid == r && (r == 0 || both)) {
                     const float dg = c.sigmoid ? t[r] * gt[r] * (1.f - gt[r]) : t[r];
                     if (c.wf32) static_cast<float *>(a.dgate)[(row0 + r) * a.ld_dgate] = dg;
                     else static_cast<uint16_t *>(a.dgate)[(row0 + r) * a.ld_dgate] = to_bf16(dg);
@@ -773,39 +804,27 @@ __global__ void __launch_bounds__(kStagedThreads, 1) k_block_norm_bwd_staged(con
         for (int i = 0; i < C; ++i) {
             const int col = tid * 8 + i * stride;
             if (col >= c.D) continue;
-            float w[8];
-            if (post) get8(smem + g.at_wpost, c.pf32, col, w);
+            const V8 w = post ? kept8(smem + g.at_wpost, col, c.D) : splat8(1.f);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                if (row0 + r >= c.rows) continue;
-                if (post) {
-                    const float m = -t[r] * c.inv_d;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) d[i][r][k] = cur[r].rs_post * fmaf(h[i][r][k], m, d[i][r][k] * w[k]);
-                }
-                store8(static_cast<TA *>(a.dy) + (row0 + r) * a.ld_dy + col, d[i][r]);
+                if (post) d[i][r] = mul8(fma8(h[i][r], -t[r] * c.inv_d, mul8(d[i][r], w)), cur.rs_post[r]);
+                if (r == 0 || both) put8(static_cast<TA *>(a.dy) + (row0 + r) * a.ld_dy + col, d[i][r]);
             }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) cur[r] = next[r];
-        __syncthreads();  // the stage has been read
-        if (tid == 0 && ok && group + (int64_t)g.stages * gridDim.x < groups) issue(group + (int64_t)g.stages * gridDim.x, st);
-        if (++st == g.stages) {
-            st = 0;
-            parity ^= 1;
-        }
+        cur = next;
+        flip ^= 1;
+        if (++st == g.stages) st = 0;
     }
-    if (tid == 0 && !ok)  // copies still in flight must land before the block may exit
-        for (int k = lost / 2; k < lost / 2 + g.stages; ++k) mbar_wait(&full[k % g.stages], (lost ^ (k >= g.stages)) & 1);
     const int64_t plane = (int64_t)gridDim.x * c.D;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int col = tid * 8 + i * stride;
         if (col >= c.D) continue;
         float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * c.D + col);
-        auto put = [&](float4 *p, const float f[8]) {
-            p[0] = make_float4(f[0], f[1], f[2], f[3]);
-            p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        auto put = [&](float4 *p, const V8 &v) {
+            const float2 x = split(v.p[0]), y = split(v.p[1]), z = split(v.p[2]), w = split(v.p[3]);
+            p[0] = make_float4(x.x, x.y, y.x, y.y);
+            p[1] = make_float4(z.x, z.y, w.x, w.y);
         };
         if (a.need_post) put(part, acc_post[i]);
         if (a.need_pre) put(part + plane / 4, acc_pre[i]);
@@ -1012,24 +1031,23 @@ bool ring_of(const Common &c, const Bwd &a, int ea, int er, int R, Ring *g)
         at += (int)round_up(n, 128);
     };
     const int D = c.D, eg = c.gf32 ? 4 : 2;
-    const int64_t codes = round_up(D, 16);
+    const int64_t codes = D;
     place(&g->at_dh, &g->by_dh, c.w_pre ? D * ea : 0);
     place(&g->at_dr, &g->by_dr, a.dr ? D * er : 0);
     place(&g->at_y, &g->by_y, c.y8.codes ? codes : a.y ? D * ea : 0);
     place(&g->at_r, &g->by_r, c.r8.codes ? codes : c.w_pre ? D * er : 0);
     place(&g->at_gate, &g->by_gate, c.gate_kind == ZERO1_GATE_FULL ? D * eg : 0);
-    g->all = g->by_dh + g->by_dr + g->by_y + g->by_r + g->by_gate;
     g->row_bytes = at;
     g->stage_bytes = at * R;
     at = 0;
     int unused;
-    place(&g->at_wpre, &unused, c.w_pre ? D * (c.pf32 ? 4 : 2) : 0);
-    place(&g->at_wpost, &unused, c.w_post ? D * (c.pf32 ? 4 : 2) : 0);
-    place(&g->at_wgate, &unused, c.gate_kind == ZERO1_GATE_CHANNEL ? D * eg : 0);
+    place(&g->at_wpre, &unused, c.w_pre ? D * 4 : 0);
+    place(&g->at_wpost, &unused, c.w_post ? D * 4 : 0);
+    place(&g->at_wgate, &unused, c.gate_kind == ZERO1_GATE_CHANNEL ? D * 4 : 0);
     g->at_stage = at;
     g->stages = (kStagedSmem - at) / (g->stage_bytes > 0 ? g->stage_bytes : 1);
     if (g->stages > 4) g->stages = 4;
-    return g->stages >= 1 && g->all > 0;
+    return g->stages >= 2;
 }
 
 template <class TA, class TR, int C, int R>
@@ -1043,9 +1061,17 @@ int launch_bwd_staged(const Common &c, const Bwd &a, const Ring &g, int threads,
         z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, 1, threads, 0);
         return launch_status("block norm backward launch");
     };
-    if (c.gate_kind == ZERO1_GATE_CHANNEL) return go(k_block_norm_bwd_staged<TA, TR, C, R, 1>);
-    if (c.gate_kind == ZERO1_GATE_FULL) return go(k_block_norm_bwd_staged<TA, TR, C, R, 2>);
-    return go(k_block_norm_bwd_staged<TA, TR, C, R, 0>);
+    const int codes = (c.y8.codes != nullptr) + (c.r8.codes != nullptr);
+    const int saved = !c.w_pre || !c.w_post || !a.dr ? 0 : codes == 2 ? 1 : codes == 0 ? 2 : 0;
+    auto with = [&](auto gate) {
+        constexpr int G = decltype(gate)::value;
+        if (saved == 1) return go(k_block_norm_bwd_staged<TA, TR, C, R, G, 1>);
+        if (saved == 2) return go(k_block_norm_bwd_staged<TA, TR, C, R, G, 2>);
+        return go(k_block_norm_bwd_staged<TA, TR, C, R, G, 0>);
+    };
+    if (c.gate_kind == ZERO1_GATE_CHANNEL) return with(std::integral_constant<int, 1>{});
+    if (c.gate_kind == ZERO1_GATE_FULL) return with(std::integral_constant<int, 2>{});
+    return with(std::integral_constant<int, 0>{});
 }
 
 template <class TA, class TR, bool VEC>
@@ -1058,7 +1084,7 @@ int pick_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
         const int n = (int)round_up(c.D, 256) / 8;
         const int ea = sizeof(TA), er = sizeof(TR);
         if (fits && n <= kStagedThreads) {
-            if (ring_of(c, a, ea, er, 2, &g) && g.stages >= 2) return launch_bwd_staged<TA, TR, 1, 2>(c, a, g, n, grid, st);
+            if (ring_of(c, a, ea, er, 2, &g)) return launch_bwd_staged<TA, TR, 1, 2>(c, a, g, n, grid, st);
             if (ring_of(c, a, ea, er, 1, &g)) return launch_bwd_staged<TA, TR, 1, 1>(c, a, g, n, grid, st);
         } else if (fits && ring_of(c, a, ea, er, 1, &g)) {
             return launch_bwd_staged<TA, TR, 2, 1>(c, a, g, (int)round_up(c.D, 512) / 16, grid, st);

@@ -170,14 +170,6 @@ __device__ __forceinline__ void arrive_leader(uint64_t *bar)
         : "memory");
 }
 
-// One lane of a converged warp, the same one each time.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-    return p != 0;
-}
-
 // A bounded wait of a whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
 {
