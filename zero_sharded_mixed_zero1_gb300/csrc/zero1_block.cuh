@@ -6,7 +6,17 @@
 #include "zero1_checks.h"
 #include "zero1_device.cuh"
 
+// A checkpoint as the kernels take it (codes NULL: none).
+namespace z1bn {
+struct Ckpt {
+    uint8_t *codes, *exps;
+    int64_t ld_codes, ld_exps;
+};
+}  // namespace z1bn
+
 namespace {
+
+using z1bn::Ckpt;
 
 constexpr int kQBlock = 128;  // columns that share a checkpoint scale
 constexpr int kMinE = 8;      // biased exponents of the scales: 127 - 119 .. 127 + 119
@@ -134,11 +144,6 @@ __device__ __forceinline__ uint32_t max16(uint32_t a)
     return a;
 }
 __device__ __forceinline__ uint32_t max32(uint32_t a) { return __reduce_max_sync(0xffffffffu, a); }
-
-struct Ckpt {
-    uint8_t *codes, *exps;
-    int64_t ld_codes, ld_exps;
-};
 
 // ------------------------------------------------------------ fp32 pairs ---
 //

@@ -1,0 +1,494 @@
+// zero1_block_norm_bwd.cuh - the backward kernels of the block norms
+// (library-internal; each source that includes this compiles one pair of types).
+#pragma once
+
+#include "zero1_block_norm.cuh"
+
+namespace {
+
+// ------------------------------------------------------------ backward -----
+//
+// One pass: dh, dr and the saved activations are read once, dx and dy written
+// once: 10 bytes per bf16 element from both checkpoints, 12 from tensors.
+// Each thread keeps the column sums of its own columns over all rows that its
+// block visits (in registers, or in shared memory where a row takes 1024
+// threads and registers are short); a second kernel adds the blocks' sums in
+// block order.
+
+template <class TA, class TR, int V, bool VEC, bool WARP, bool SACC>
+__global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm_bwd(const Common c, const Bwd a)
+{
+    constexpr int C = V / 8;
+    __shared__ float red[2][32];
+    extern __shared__ float sacc[];  // SACC: [3][V][threads]; WARP: [D] for the blocks' sum
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int nthr = WARP ? 32 : blockDim.x;
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    float acc[SACC ? 1 : 3][C][8];
+    if constexpr (SACC) {
+        for (int q = 0; q < 3 * V; ++q) sacc[q * nthr + tid] = 0.f;
+    } else {
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) acc[s][i][k] = 0.f;
+    }
+    auto add = [&](int s, int i, int k, float x) {
+        if constexpr (SACC) sacc[(s * V + i * 8 + k) * nthr + tid] += x;
+        else acc[s][i][k] += x;
+    };
+
+    for (int64_t row = row0; row < c.rows; row += step) {
+        Chunk<TA, VEC> hq[C], yq[C];
+        Chunk<TR, VEC> dq[C], rq[C];
+        uint2 y8[C], r8[C];
+        int ey[C], er[C];
+        const bool pre = c.w_pre, post = c.w_post;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = chunk_col<VEC>(i, tid, nthr);
+            if (pre) {
+                hq[i].load(static_cast<const TA *>(a.dh) + row * a.ld_dh, col, c.D);
+                if (c.r8.codes) load_codes<VEC>(c.r8, row, col, c.D, r8[i], er[i]);
+                else rq[i].load(static_cast<const TR *>(a.r) + row * a.ld_r, col, c.D);
+            }
+            if (a.dr) dq[i].load(static_cast<const TR *>(a.dr) + row * a.ld_dr, col, c.D);
+            if (c.y8.codes) load_codes<VEC>(c.y8, row, col, c.D, y8[i], ey[i]);
+            else if (a.y) yq[i].load(static_cast<const TA *>(a.y) + row * a.ld_y, col, c.D);
+        }
+        const float gt = token_gate(c, row);
+        const float rs_pre = pre ? a.rstd_pre[row] : 0.f, rs_post = post ? a.rstd_post[row] : 1.f;
+        float d[C][8], rh[C][8];
+        float s1 = 0.f;
+        if (pre) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int col = chunk_col<VEC>(i, tid, nthr);
+                float w[8];
+                param8<VEC>(c.w_pre, c.pf32, c.pvec, 0, col, c.D, w);
+                hq[i].get(d[i]);
+                if (c.r8.codes) {
+                    values8(r8[i], scale_of(er[i]), rh[i]);
+                } else {
+                    rq[i].get(rh[i]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) rh[i][k] *= rs_pre;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (a.need_pre) add(1, i, k, d[i][k] * rh[i][k]);
+                    d[i][k] *= w[k];
+                    s1 = fmaf(d[i][k], rh[i][k], s1);
+                }
+            }
+            s1 = row_sum<WARP>(s1, red[0]) * c.inv_d;
+        }
+        float s2 = 0.f;
+        float yh[C][8];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = chunk_col<VEC>(i, tid, nthr);
+            float r0[8], g[8], w[8], o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) r0[k] = 0.f;
+            if (a.dr) dq[i].get(r0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[i][k] = pre ? fmaf(rs_pre, fmaf(-rh[i][k], s1, d[i][k]), r0[k]) : r0[k];
+            store_chunk<TR, VEC>(static_cast<TR *>(a.dx) + row * a.ld_dx, col, c.D, d[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) yh[i][k] = 0.f;
+            if (c.y8.codes) {
+                values8(y8[i], scale_of(ey[i]), yh[i]);
+            } else if (a.y) {
+                yq[i].get(yh[i]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) yh[i][k] *= rs_post;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) { g[k] = 1.f; w[k] = 1.f; }
+            gate8<VEC>(c, row, col, g);
+            if (post) param8<VEC>(c.w_post, c.pf32, c.pvec, 0, col, c.D, w);
+            // p = a d u, the gradient of the gate's factor; d becomes a g d, the
+            // gradient of u
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float ad = c.alpha * d[i][k];
+                const float p = ad * (w[k] * yh[i][k]);
+                if (a.need_gate && c.gate_kind == ZERO1_GATE_CHANNEL) add(2, i, k, p);
+                o[k] = p * (c.sigmoid ? g[k] * (1.f - g[k]) : 1.f);
+                d[i][k] = ad * g[k];
+                s2 = fmaf(g[k], p, s2);
+            }
+            if (a.need_gate && c.gate_kind == ZERO1_GATE_FULL) {
+                if (VEC && a.dgvec) {
+                    if (c.gf32) store_chunk<float, true>(static_cast<float *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
+                    else store_chunk<uint16_t, true>(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int cc = col + kStep<VEC> * k;
+                        if (cc >= c.D) continue;
+                        if (c.gf32) st1(static_cast<float *>(a.dgate) + row * a.ld_dgate + cc, o[k]);
+                        else st1(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate + cc, o[k]);
+                    }
+                }
+            }
+        }
+        const bool tok = a.need_gate && c.gate_kind == ZERO1_GATE_TOKEN;
+        if (post || tok) s2 = row_sum<WARP>(s2, red[1]);
+        if (tok && tid == 0) {
+            const float dg = c.sigmoid ? s2 * gt * (1.f - gt) : s2;
+            if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;
+            else static_cast<uint16_t *>(a.dgate)[row * a.ld_dgate] = to_bf16(dg);
+        }
+        s2 *= c.inv_d * gt;  // a token gate's factor is the same over the row
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = chunk_col<VEC>(i, tid, nthr);
+            float w[8];
+            if (post) param8<VEC>(c.w_post, c.pf32, c.pvec, 0, col, c.D, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float dyh = d[i][k] * gt;
+                if (a.need_post) add(0, i, k, dyh * yh[i][k]);
+                d[i][k] = post ? rs_post * fmaf(-yh[i][k], s2, dyh * w[k]) : dyh;
+            }
+            store_chunk<TA, VEC>(static_cast<TA *>(a.dy) + row * a.ld_dy, col, c.D, d[i]);
+        }
+    }
+
+    // this block's column sums
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+        const bool need = s == 0 ? a.need_post : s == 1 ? a.need_pre
+                                                        : a.need_gate && c.gate_kind == ZERO1_GATE_CHANNEL;
+        if (!need) continue;
+        float *part = a.part + ((int64_t)s * gridDim.x + blockIdx.x) * c.D;
+        if constexpr (WARP) {  // the warps add up in turn
+            for (int w = 0; w < kWarpRows; ++w) {
+                if ((int)(threadIdx.x >> 5) == w) {
+#pragma unroll
+                    for (int i = 0; i < C; ++i)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int cc = chunk_col<VEC>(i, tid, nthr) + kStep<VEC> * k;
+                            if (cc < c.D) sacc[cc] = (w ? sacc[cc] : 0.f) + acc[s][i][k];
+                        }
+                }
+                __syncthreads();
+            }
+            for (int cc = threadIdx.x; cc < c.D; cc += blockDim.x) part[cc] = sacc[cc];
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int cc = chunk_col<VEC>(i, tid, nthr) + kStep<VEC> * k;
+                    if (cc < c.D) part[cc] = SACC ? sacc[(s * V + i * 8 + k) * nthr + tid] : acc[SACC ? 0 : s][i][k];
+                }
+        }
+    }
+}
+
+// ------------------------------------------------------- staged backward ---
+
+// A row's statistics and scale bytes travel through the ring as well: plain
+// loads a row ahead ended in waits that the compiler put where it liked (20 to
+// 100 us on the larger sizes).  Each warp has 16 words per stage: rstd_pre,
+// rstd_post, and from word 4 on the aligned words around the scale bytes of
+// its 128-column blocks, two per chunk, those of y8 first.  This lane copies
+// word `lane`.
+template <int T, int C>
+struct RowWords {
+    const char *from = nullptr;
+    int bytes_per_row = 1;
+
+    __device__ __forceinline__ RowWords(const Common &c, const float *rstd_pre, const float *rstd_post)
+    {
+        const int lane = threadIdx.x & 31, k = lane - 4;
+        if (lane < 2) {
+            from = reinterpret_cast<const char *>(lane == 0 ? rstd_pre : rstd_post);
+            bytes_per_row = 4;
+        } else if (k >= 0 && k < 4 * C) {
+            const Ckpt &q = k < 2 * C ? c.y8 : c.r8;
+            const int col = (threadIdx.x / 32 * 32 + (k % 2) * 16) * 8 + k / 2 % C * T * 8;
+            if (q.codes && col < c.D) from = reinterpret_cast<const char *>(q.exps + (int64_t)(col / kQBlock) * q.ld_exps);
+        }
+    }
+    __device__ __forceinline__ void copy_ahead(uint32_t *words, int64_t row) const
+    {
+        if (!from) return;
+        const uint32_t d = (uint32_t)__cvta_generic_to_shared(words + (threadIdx.x & 31));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(from + ((row * bytes_per_row) & ~INT64_C(3)))
+                     : "memory");
+    }
+    // The scale of this thread's chunk i: of y8, or (half 1) of r8.
+    static __device__ __forceinline__ float scale(const uint32_t *words, int64_t row, int half, int i)
+    {
+        const uint32_t w = words[4 + 2 * (C * half + i) + (threadIdx.x >> 4 & 1)];
+        return scale_of((w >> (8 * ((int)row & 3))) & 255);
+    }
+};
+
+// Where a row's inputs lie in a stage of T threads with C chunks of 8 columns.
+// SAVED: 1 both norms and dr are there and both saved activations are
+// checkpoints, 2 the same with tensors, 0 any other mix, decided at run time.
+template <class TA, class TR, int T, int C, int SAVED>
+struct Stage {
+    static constexpr int n = 8 * C * T;
+    static constexpr int dh = 0, dr = dh + n * (int)sizeof(TA), y = dr + n * (int)sizeof(TR);
+    static constexpr int r = y + n * (SAVED == 1 ? 1 : (int)sizeof(TA));
+    static constexpr int words = r + n * (SAVED == 1 ? 1 : (int)sizeof(TR));
+    static constexpr int words_bytes = SAVED == 2 ? 16 : 64;  // of a warp
+    static constexpr int gate = words + T / 32 * words_bytes;
+};
+
+// GATE: 0 none or one value per row, 1 per channel, 2 per element.  FULL: the
+// row has exactly 8 C T columns.
+template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL>
+__global__ void __launch_bounds__(T, kOwnRegs / T)
+k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int stage_bytes)
+{
+    using S = Stage<TA, TR, T, C, SAVED>;
+    constexpr int A = sizeof(TA), B = sizeof(TR), kVector = S::n * 4;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red[2][2][16];
+    const int tid = threadIdx.x;
+    const bool pre = SAVED || c.w_pre, post = SAVED || c.w_post, dr = SAVED || a.dr;
+    const bool r8 = SAVED ? SAVED == 1 : c.r8.codes != nullptr, y8 = SAVED ? SAVED == 1 : c.y8.codes != nullptr;
+    const bool ysaved = SAVED || y8 || a.y;
+    const bool tok = GATE == 0 && a.need_gate;
+    unsigned char *kept = smem;  // w_pre, w_post, the channel gate's factor
+    unsigned char *ring = smem + (GATE == 1 ? 3 : 2) * kVector;
+    auto in = [&](int i) { return FULL || tid * 8 + i * T * 8 < c.D; };
+
+    const RowWords<T, C> row_words(c, a.rstd_pre, a.rstd_post);
+    auto words_of = [&](unsigned char *stage) { return reinterpret_cast<uint32_t *>(stage + S::words + tid / 32 * S::words_bytes); };
+
+    // Starts the copies of a row; past the last row, an empty group that keeps the count.
+    auto fetch = [&](int64_t row, unsigned char *to) {
+        if (row < c.rows) {
+            row_words.copy_ahead(words_of(to), row);
+            const TA *dh = static_cast<const TA *>(a.dh) + row * a.ld_dh;
+            const TR *ddr = static_cast<const TR *>(a.dr) + row * a.ld_dr;
+            const void *y = y8 ? (const void *)(c.y8.codes + row * c.y8.ld_codes)
+                               : (const void *)(static_cast<const TA *>(a.y) + row * a.ld_y);
+            const void *r = r8 ? (const void *)(c.r8.codes + row * c.r8.ld_codes)
+                               : (const void *)(static_cast<const TR *>(a.r) + row * a.ld_r);
+            const char *gate = static_cast<const char *>(c.gate) + row * c.ld_gate * (c.gf32 ? 4 : 2);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int col = tid * 8 + i * T * 8;
+                if (!in(i)) continue;
+                if (pre) {
+                    copy8_ahead<A>(to + S::dh + chunk_at<T, A>(i), dh, col);
+                    if (r8) copy8_ahead<1>(to + S::r + chunk_at<T, 1>(i), r, col);
+                    else copy8_ahead<B>(to + S::r + chunk_at<T, B>(i), r, col);
+                }
+                if (dr) copy8_ahead<B>(to + S::dr + chunk_at<T, B>(i), ddr, col);
+                if (y8) copy8_ahead<1>(to + S::y + chunk_at<T, 1>(i), y, col);
+                else if (ysaved) copy8_ahead<A>(to + S::y + chunk_at<T, A>(i), y, col);
+                if (GATE == 2) {
+                    if (c.gf32) copy8_ahead<4>(to + S::gate + chunk_at<T, 4>(i), gate, col);
+                    else copy8_ahead<2>(to + S::gate + chunk_at<T, 2>(i), gate, col);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k + 1 < stages; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, ring + k * stage_bytes);
+
+    keep_vector<T, C>(kept, c.w_pre, c.pf32, c.D, 0);
+    keep_vector<T, C>(kept + kVector, c.w_post, c.pf32, c.D, 0);
+    if (GATE == 1) keep_vector<T, C>(kept + 2 * kVector, c.gate, c.gf32, c.D, c.sigmoid);
+    V8 acc_post[C], acc_pre[C], acc_gate[GATE == 1 ? C : 1];
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc_post[i] = acc_pre[i] = acc_gate[GATE == 1 ? i : 0] = splat8(0.f);
+
+    int st = 0, flip = 0;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+        float gt = 1.f;
+        if (GATE == 0 && c.gate_kind == ZERO1_GATE_TOKEN) gt = token_gate(c, row);
+        // the stage that this warp has read a row ago is filled again
+        __syncwarp();
+        fetch(row + (int64_t)(stages - 1) * gridDim.x, ring + (st == 0 ? stages - 1 : st - 1) * stage_bytes);
+        copies_wait(stages - 1);
+        __syncwarp();
+        unsigned char *b = ring + st * stage_bytes;
+        const uint32_t *words = words_of(b);
+        V8 d[C], h[C];  // h: the saved row, first rh, then yh
+
+        const float rs_pre = pre ? __uint_as_float(words[0]) : 0.f, rs_post = post ? __uint_as_float(words[1]) : 1.f;
+        float s = 0.f;
+        if (pre) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                if (!in(i)) continue;
+                const V8 w = kept8<T, C>(kept, i);
+                d[i] = take8<TA>(b + S::dh + chunk_at<T, A>(i), 0);
+                if (r8) h[i] = take_codes(b + S::r + chunk_at<T, 1>(i), row_words.scale(words, row, 1, i));
+                else h[i] = mul8(take8<TR>(b + S::r + chunk_at<T, B>(i), 0), rs_pre);
+                acc_pre[i] = fma8(d[i], h[i], acc_pre[i]);
+                d[i] = mul8(d[i], w);
+                s += dot8(d[i], h[i]);
+            }
+            s = block_sum<T>(s, red[flip][0]) * -c.inv_d;
+        }
+
+        // x: the gradient of r; then p = a x u, the gradient of the gate's
+        // factor, and d = a g x, the gradient of u
+        float t = 0.f;
+        TR *dx = static_cast<TR *>(a.dx) + row * a.ld_dx;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = tid * 8 + i * T * 8;
+            if (!in(i)) continue;
+            V8 x = dr ? take8<TR>(b + S::dr + chunk_at<T, B>(i), 0) : splat8(0.f);
+            if (pre) x = fma8(fma8(h[i], s, d[i]), rs_pre, x);
+            put8(dx + col, x);
+            if (y8) h[i] = take_codes(b + S::y + chunk_at<T, 1>(i), row_words.scale(words, row, 0, i));
+            else if (ysaved) h[i] = mul8(take8<TA>(b + S::y + chunk_at<T, A>(i), 0), rs_post);
+            else h[i] = splat8(0.f);
+            const V8 u = post ? mul8(kept8<T, C>(kept + kVector, i), h[i]) : h[i];
+            if (GATE == 0) {
+                t += dot8(x, u);  // times a: the gradient of a token's gate
+                d[i] = mul8(x, c.alpha * gt);
+            } else {
+                V8 gc;
+                if (GATE == 1) {
+                    gc = kept8<T, C>(kept + 2 * kVector, i);
+                } else {
+                    gc = c.gf32 ? take8<float>(b + S::gate + chunk_at<T, 4>(i), 0) : take8<uint16_t>(b + S::gate + chunk_at<T, 2>(i), 0);
+                    if (c.sigmoid) gc = map8(gc, [](float v) { return sigmoid(v); });
+                }
+                const V8 ax = mul8(x, c.alpha), p = mul8(ax, u);
+                if (GATE == 1) acc_gate[GATE == 1 ? i : 0] = add8(acc_gate[GATE == 1 ? i : 0], p);
+                t += dot8(gc, p);
+                d[i] = mul8(ax, gc);
+                if (GATE == 2 && a.need_gate) {
+                    const V8 o = c.sigmoid ? mul8(p, map8(gc, [](float v) { return v * (1.f - v); })) : p;
+                    if (c.gf32) put8(static_cast<float *>(a.dgate) + row * a.ld_dgate + col, o);
+                    else put8(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate + col, o);
+                }
+            }
+            acc_post[i] = fma8(d[i], h[i], acc_post[i]);
+        }
+        if (post || tok) t = block_sum<T>(t, red[flip][1]);
+        if (GATE == 0) {
+            t *= c.alpha;
+            if (tok && tid == 0) {
+                const float dg = c.sigmoid ? t * gt * (1.f - gt) : t;
+                if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;
+                else static_cast<uint16_t *>(a.dgate)[row * a.ld_dgate] = to_bf16(dg);
+            }
+            t *= gt;
+        }
+        t *= -c.inv_d;
+        TA *dy = static_cast<TA *>(a.dy) + row * a.ld_dy;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if (!in(i)) continue;
+            if (post) d[i] = mul8(fma8(h[i], t, mul8(d[i], kept8<T, C>(kept + kVector, i))), rs_post);
+            put8(dy + tid * 8 + i * T * 8, d[i]);
+        }
+        flip ^= 1;
+        if (++st == stages) st = 0;
+    }
+    const int64_t plane = (int64_t)gridDim.x * c.D;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        if (!in(i)) continue;
+        float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * c.D + tid * 8 + i * T * 8);
+        auto put = [&](float4 *p, const V8 &v) {
+            const float2 x = split(v.p[0]), y = split(v.p[1]), z = split(v.p[2]), w = split(v.p[3]);
+            p[0] = make_float4(x.x, x.y, y.x, y.y);
+            p[1] = make_float4(z.x, z.y, w.x, w.y);
+        };
+        if (a.need_post) put(part, acc_post[i]);
+        if (a.need_pre) put(part + plane / 4, acc_pre[i]);
+        if (GATE == 1 && a.need_gate) put(part + plane / 2, acc_gate[GATE == 1 ? i : 0]);
+    }
+}
+
+template <class TA, class TR, int V, bool VEC, bool WARP, bool SACC>
+int launch_bwd(const Common &c, const Bwd &a, int threads, int64_t grid, cudaStream_t st)
+{
+    auto kernel = k_block_norm_bwd<TA, TR, V, VEC, WARP, SACC>;
+    const int smem = SACC ? 3 * V * threads * 4 : WARP ? c.D * 4 : 0;
+    if (SACC) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "block norm backward: %s", cudaGetErrorString(e));
+    }
+    kernel<<<(unsigned)grid, threads, smem, st>>>(c, a);
+    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, 1, threads, 0);
+    return launch_status("block norm backward launch");
+}
+
+// One resident wave of staged blocks (`grid`); false, with nothing launched, if
+// a row does not fit.
+template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL>
+bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st, int *rc)
+{
+    auto kernel = k_block_norm_bwd_staged<TA, TR, T, C, GATE, SAVED, FULL>;
+    using S = Stage<TA, TR, T, C, SAVED>;
+    constexpr int kept = (GATE == 1 ? 3 : 2) * S::n * 4;
+    const int stage = S::gate + (GATE == 2 ? S::n * (c.gf32 ? 4 : 2) : 0);
+    const int stages = stages_that_fit(T, kept, stage);
+    if (stages == 0) return false;
+    const int smem = kept + stages * stage;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+        *rc = z1_fail(ZERO1_ECUDA, "block norm backward: %s", cudaGetErrorString(e));
+        return true;
+    }
+    kernel<<<(unsigned)grid, T, smem, st>>>(c, a, stages, stage);
+    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, kOwnRegs / T, T, 0);
+    *rc = launch_status("block norm backward launch");
+    return true;
+}
+
+template <class TA, class TR>
+bool backward_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st, int *rc)
+{
+    if (c.D > 8192 || (c.gate_kind == ZERO1_GATE_FULL && (!c.gvec || (a.need_gate && !a.dgvec)))) return false;
+    const int codes = (c.y8.codes != nullptr) + (c.r8.codes != nullptr);
+    const int kinds = !c.w_pre || !c.w_post || !a.dr ? 0 : codes == 2 ? 1 : codes == 0 ? 2 : 0;
+    return pick_threads(c.D, [&](auto t, auto n) {
+        constexpr int T = decltype(t)::value, C = decltype(n)::value;
+        return pick_gate(c.gate_kind, [&](auto gate) {
+            constexpr int G = decltype(gate)::value;
+            if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
+                const int saved = c.D == 8 * C * T ? kinds : 0;
+                if (saved == 1) return launch_bwd_staged<TA, TR, T, C, G, 1, true>(c, a, grid, st, rc);
+                if (saved == 2) return launch_bwd_staged<TA, TR, T, C, G, 2, true>(c, a, grid, st, rc);
+            }
+            return launch_bwd_staged<TA, TR, T, C, G, 0, false>(c, a, grid, st, rc);
+        });
+    });
+}
+
+template <class TA, class TR, bool VEC>
+int pick_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
+{
+    const int threads = row_threads(c.D);
+    if constexpr (!VEC) {
+        if (c.D <= 256) return launch_bwd<TA, TR, 8, VEC, true, false>(c, a, threads, grid, st);
+        if (c.D <= 512) return launch_bwd<TA, TR, 16, VEC, true, false>(c, a, threads, grid, st);
+    }
+    if (c.D <= 8192) return launch_bwd<TA, TR, 16, VEC, false, false>(c, a, threads, grid, st);
+    return launch_bwd<TA, TR, 16, VEC, false, true>(c, a, threads, grid, st);
+}
+
+}  // namespace
+
+template <class TA, class TR>
+int z1bn::run_backward(const Common &c, const Bwd &a, bool vec, int64_t grid, cudaStream_t st)
+{
+    int rc;
+    if (vec && backward_staged<TA, TR>(c, a, grid, st, &rc)) return rc;
+    return vec ? pick_bwd<TA, TR, true>(c, a, grid, st) : pick_bwd<TA, TR, false>(c, a, grid, st);
+}

@@ -1,0 +1,273 @@
+// zero1_block_norm_fwd.cuh - the forward kernels of the block norms
+// (library-internal; each source that includes this compiles one pair of types).
+#pragma once
+
+#include "zero1_block_norm.cuh"
+
+namespace {
+
+// ------------------------------------------------------------- forward -----
+//
+// One pass: y and x are read once, both statistics come from registers, and
+// r, h and the checkpoints are written once: 10 bytes per bf16 element with
+// both checkpoints, 8 without.  HBM is the bound.
+
+template <class TA, class TR, int V, bool VEC, bool WARP>
+__global__ void __launch_bounds__(V == 16 && !WARP ? 1024 : 256) k_block_norm_fwd(const Common c, const Fwd a)
+{
+    constexpr int C = V / 8;
+    __shared__ float red[2][32];
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int nthr = WARP ? 32 : blockDim.x;
+    const int64_t row0 = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    for (int64_t row = row0; row < c.rows; row += step) {
+        Chunk<TA, VEC> yq[C];
+        Chunk<TR, VEC> xq[C];
+        const TA *y = static_cast<const TA *>(a.y) + row * a.ld_y;
+        const TR *x = static_cast<const TR *>(a.x) + row * a.ld_x;
+#pragma unroll
+        for (int i = 0; i < C; ++i) yq[i].load(y, chunk_col<VEC>(i, tid, nthr), c.D);
+#pragma unroll
+        for (int i = 0; i < C; ++i) xq[i].load(x, chunk_col<VEC>(i, tid, nthr), c.D);
+        const float gt = token_gate(c, row);
+        float f[C][8];
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            yq[i].get(f[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss = fmaf(f[i][k], f[i][k], ss);
+        }
+        float rs = 1.f;
+        if (c.w_post) {
+            rs = rstd_of(row_sum<WARP>(ss, red[0]), c);
+            if (tid == 0) a.rstd_post[row] = rs;
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = chunk_col<VEC>(i, tid, nthr);
+            float w[8], g[8], xv[8];
+            if (c.w_post) {
+                param8<VEC>(c.w_post, c.pf32, c.pvec, 0, col, c.D, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f[i][k] *= rs;
+            }
+            if (c.y8.codes) pack_chunk<VEC>(c.y8, row, col, c.D, f[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[k] = gt;
+            gate8<VEC>(c, row, col, g);
+            xq[i].get(xv);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float u = c.w_post ? f[i][k] * w[k] : f[i][k];
+                f[i][k] = fmaf(c.alpha * g[k], u, xv[k]);
+            }
+            store_chunk<TR, VEC>(static_cast<TR *>(a.r) + row * a.ld_r, col, c.D, f[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss = fmaf(f[i][k], f[i][k], ss);
+        }
+        if (!c.w_pre) continue;
+        rs = rstd_of(row_sum<WARP>(ss, red[1]), c);
+        if (tid == 0) a.rstd_pre[row] = rs;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int col = chunk_col<VEC>(i, tid, nthr);
+            float w[8];
+            param8<VEC>(c.w_pre, c.pf32, c.pvec, 0, col, c.D, w);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[i][k] *= rs;
+            if (c.r8.codes) pack_chunk<VEC>(c.r8, row, col, c.D, f[i]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[i][k] *= w[k];
+            store_chunk<TA, VEC>(static_cast<TA *>(a.h) + row * a.ld_h, col, c.D, f[i]);
+        }
+    }
+}
+
+// ------------------------------------------------------- staged forward ----
+//
+// KEPT: 1 both norms are there and both checkpoints wanted, 2 both norms and
+// no checkpoint, 0 any other mix, decided at run time.  FULL: the row has
+// exactly 8 C T columns.
+
+template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL>
+__global__ void __launch_bounds__(T, kOwnRegs / T)
+k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int stage_bytes)
+{
+    constexpr int A = sizeof(TA), B = sizeof(TR), N = 8 * C * T, kVector = N * 4;
+    constexpr int at_y = 0, at_x = N * A, at_gate = at_x + N * B;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float red[2][2][16];
+    const int tid = threadIdx.x;
+    const bool post = KEPT || c.w_post, pre = KEPT || c.w_pre;
+    const bool y8 = KEPT ? KEPT == 1 : c.y8.codes != nullptr, r8 = KEPT ? KEPT == 1 : c.r8.codes != nullptr;
+    unsigned char *kept = smem;  // w_post, w_pre, the channel gate's factor
+    unsigned char *ring = smem + (GATE == 1 ? 3 : 2) * kVector;
+    auto in = [&](int i) { return FULL || tid * 8 + i * T * 8 < c.D; };
+
+    auto fetch = [&](int64_t row, unsigned char *to) {
+        if (row < c.rows) {
+            const TA *y = static_cast<const TA *>(a.y) + row * a.ld_y;
+            const TR *x = static_cast<const TR *>(a.x) + row * a.ld_x;
+            const char *gate = static_cast<const char *>(c.gate) + row * c.ld_gate * (c.gf32 ? 4 : 2);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int col = tid * 8 + i * T * 8;
+                if (!in(i)) continue;
+                copy8_ahead<A>(to + at_y + chunk_at<T, A>(i), y, col);
+                copy8_ahead<B>(to + at_x + chunk_at<T, B>(i), x, col);
+                if (GATE == 2) {
+                    if (c.gf32) copy8_ahead<4>(to + at_gate + chunk_at<T, 4>(i), gate, col);
+                    else copy8_ahead<2>(to + at_gate + chunk_at<T, 2>(i), gate, col);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // Codes of a chunk, and their block's scale from one of its 16 lanes.
+    auto keep = [&](const Ckpt &k, int64_t row, int i, const V8 &v) {
+        const int col = tid * 8 + i * T * 8;
+        int E;
+        const uint2 q = encode8(v, E);
+        if (!FULL && col / kQBlock * kQBlock >= c.D) return;
+        __stcs(reinterpret_cast<uint2 *>(k.codes + row * k.ld_codes + col), q);
+        if ((tid & 15) == 0) k.exps[(int64_t)(col / kQBlock) * k.ld_exps + row] = (uint8_t)E;
+    };
+    for (int k = 0; k + 1 < stages; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, ring + k * stage_bytes);
+    keep_vector<T, C>(kept, c.w_post, c.pf32, c.D, 0);
+    keep_vector<T, C>(kept + kVector, c.w_pre, c.pf32, c.D, 0);
+    if (GATE == 1) keep_vector<T, C>(kept + 2 * kVector, c.gate, c.gf32, c.D, c.sigmoid);
+
+    int st = 0, flip = 0;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+        float gt = 1.f;
+        if (GATE == 0 && c.gate_kind == ZERO1_GATE_TOKEN) gt = token_gate(c, row);
+        // what this thread has read a row ago is filled again
+        fetch(row + (int64_t)(stages - 1) * gridDim.x, ring + (st == 0 ? stages - 1 : st - 1) * stage_bytes);
+        copies_wait(stages - 1);
+        const unsigned char *b = ring + st * stage_bytes;
+        V8 v[C];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            v[i] = in(i) ? take8<TA>(b + at_y + chunk_at<T, A>(i), 0) : splat8(0.f);
+            if (post) s += dot8(v[i], v[i]);
+        }
+        float rs = 1.f;
+        if (post) {
+            rs = rstd_of(block_sum<T>(s, red[flip][0]), c);
+            if (tid == 0) a.rstd_post[row] = rs;
+        }
+        s = 0.f;
+        TR *r = static_cast<TR *>(a.r) + row * a.ld_r;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if (post) v[i] = mul8(v[i], rs);
+            if (y8) keep(c.y8, row, i, v[i]);
+            if (!in(i)) continue;
+            if (post) v[i] = mul8(v[i], kept8<T, C>(kept, i));
+            if (GATE == 1) {
+                v[i] = mul8(v[i], kept8<T, C>(kept + 2 * kVector, i));
+            } else if (GATE == 2) {
+                V8 g = c.gf32 ? take8<float>(b + at_gate + chunk_at<T, 4>(i), 0) : take8<uint16_t>(b + at_gate + chunk_at<T, 2>(i), 0);
+                if (c.sigmoid) g = map8(g, [](float x) { return sigmoid(x); });
+                v[i] = mul8(v[i], g);
+            }
+            v[i] = fma8(v[i], c.alpha * gt, take8<TR>(b + at_x + chunk_at<T, B>(i), 0));
+            put8(r + tid * 8 + i * T * 8, v[i]);
+            if (pre) s += dot8(v[i], v[i]);
+        }
+        if (pre) {
+            rs = rstd_of(block_sum<T>(s, red[flip][1]), c);
+            if (tid == 0) a.rstd_pre[row] = rs;
+            TA *h = static_cast<TA *>(a.h) + row * a.ld_h;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                v[i] = mul8(v[i], rs);
+                if (r8) keep(c.r8, row, i, v[i]);
+                if (in(i)) put8(h + tid * 8 + i * T * 8, mul8(v[i], kept8<T, C>(kept + kVector, i)));
+            }
+        }
+        flip ^= 1;
+        if (++st == stages) st = 0;
+    }
+}
+
+template <class TA, class TR, int V, bool VEC, bool WARP>
+int launch_fwd(const Common &c, const Fwd &a, int threads, int sms, cudaStream_t st)
+{
+    auto kernel = k_block_norm_fwd<TA, TR, V, VEC, WARP>;
+    const int per_sm = blocks_per_sm(reinterpret_cast<const void *>(kernel), threads);
+    const int64_t work = WARP ? (c.rows + kWarpRows - 1) / kWarpRows : c.rows;
+    const int64_t grid = work < (int64_t)sms * per_sm ? work : (int64_t)sms * per_sm;
+    kernel<<<(unsigned)grid, threads, 0, st>>>(c, a);
+    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, per_sm, threads, 0);
+    return launch_status("block norm forward launch");
+}
+
+template <class TA, class TR, bool VEC>
+int pick_fwd(const Common &c, const Fwd &a, int sms, cudaStream_t st)
+{
+    const int threads = row_threads(c.D);
+    if constexpr (!VEC) {
+        if (c.D <= 256) return launch_fwd<TA, TR, 8, VEC, true>(c, a, threads, sms, st);
+        if (c.D <= 512) return launch_fwd<TA, TR, 16, VEC, true>(c, a, threads, sms, st);
+    }
+    return launch_fwd<TA, TR, 16, VEC, false>(c, a, threads, sms, st);
+}
+
+// One resident wave of staged blocks; false, with nothing launched, if a row
+// does not fit.
+template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL>
+bool launch_fwd_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, int *rc)
+{
+    auto kernel = k_block_norm_fwd_staged<TA, TR, T, C, GATE, KEPT, FULL>;
+    constexpr int N = 8 * C * T, kept = (GATE == 1 ? 3 : 2) * N * 4;
+    const int stage = N * (int)(sizeof(TA) + sizeof(TR)) + (GATE == 2 ? N * (c.gf32 ? 4 : 2) : 0);
+    const int stages = stages_that_fit(T, kept, stage);
+    if (stages == 0) return false;
+    const int smem = kept + stages * stage;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) {
+        *rc = z1_fail(ZERO1_ECUDA, "block norm forward: %s", cudaGetErrorString(e));
+        return true;
+    }
+    const int64_t wave = (int64_t)sms * (kOwnRegs / T);
+    const int64_t grid = c.rows < wave ? c.rows : wave;
+    kernel<<<(unsigned)grid, T, smem, st>>>(c, a, stages, stage);
+    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, kOwnRegs / T, T, 0);
+    *rc = launch_status("block norm forward launch");
+    return true;
+}
+
+template <class TA, class TR>
+bool forward_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, int *rc)
+{
+    if (c.D > 8192 || (c.gate_kind == ZERO1_GATE_FULL && !c.gvec)) return false;
+    const int codes = (c.y8.codes != nullptr) + (c.r8.codes != nullptr);
+    const int kinds = !c.w_pre || !c.w_post ? 0 : codes == 2 ? 1 : codes == 0 ? 2 : 0;
+    return pick_threads(c.D, [&](auto t, auto n) {
+        constexpr int T = decltype(t)::value, C = decltype(n)::value;
+        return pick_gate(c.gate_kind, [&](auto gate) {
+            constexpr int G = decltype(gate)::value;
+            if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
+                const int kept = c.D == 8 * C * T ? kinds : 0;
+                if (kept == 1) return launch_fwd_staged<TA, TR, T, C, G, 1, true>(c, a, sms, st, rc);
+                if (kept == 2) return launch_fwd_staged<TA, TR, T, C, G, 2, true>(c, a, sms, st, rc);
+            }
+            return launch_fwd_staged<TA, TR, T, C, G, 0, false>(c, a, sms, st, rc);
+        });
+    });
+}
+
+}  // namespace
+
+template <class TA, class TR>
+int z1bn::run_forward(const Common &c, const Fwd &a, bool vec, int sms, cudaStream_t st)
+{
+    int rc;
+    if (vec && forward_staged<TA, TR>(c, a, sms, st, &rc)) return rc;
+    return vec ? pick_fwd<TA, TR, true>(c, a, sms, st) : pick_fwd<TA, TR, false>(c, a, sms, st);
+}
