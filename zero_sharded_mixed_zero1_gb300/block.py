@@ -10,6 +10,7 @@ stream's allocator when the caller passes none.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -25,27 +26,13 @@ _GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_FULL = 0, 1, 2, 3
 _GATE_ACTS = {"linear": 0, "sigmoid": 1}
 
 
-class _CkptStruct(ctypes.Structure):
-    _fields_ = [("codes", _vp), ("exps", _vp), ("ld_codes", _i64), ("ld_exps", _i64), ("rows", _i64),
-                ("cols", _i64)]
-
-
-class _CfgStruct(ctypes.Structure):
-    _fields_ = [("rows", _i64), ("cols", _i64), ("eps", _f32), ("residual_scale", _f32), ("act_dtype", _i32),
-                ("res_dtype", _i32), ("param_dtype", _i32), ("gate_dtype", _i32), ("grad_dtype", _i32),
-                ("gate_kind", _i32), ("gate_act", _i32), ("accumulate", _i32)]
-
-
-class _FwdStruct(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("y", "x", "w_post", "w_pre", "gate", "r", "h", "rstd_post", "rstd_pre", "y8", "r8")] \
-        + [(n, _i64) for n in ("ld_y", "ld_x", "ld_gate", "ld_r", "ld_h")]
-
-
-class _BwdStruct(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("dh", "dr", "y", "r", "w_post", "w_pre", "gate", "rstd_post", "rstd_pre", "y8", "r8",
-                                   "dy", "dx", "dw_post", "dw_pre", "dgate")] \
-        + [(n, _i64) for n in ("ld_dh", "ld_dr", "ld_y", "ld_r", "ld_gate", "ld_dy", "ld_dx", "ld_dgate")]
-
+# The C structs of include/zero1.h, packed by hand (pointers as integers, 0 for
+# NULL): a few times faster than filling ctypes structures, which shows on
+# small calls.
+_CKPT = struct.Struct("=QQqqqq")
+_CFG = struct.Struct("=qqff8i")
+_FWD = struct.Struct("=11Q5q")
+_BWD = struct.Struct("=16Q8q")
 
 _ready = None
 
@@ -65,25 +52,38 @@ def _lib():
     return _ready
 
 
+_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_stream(stream) -> int:
+    """_stream, by the short way for the current stream."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(_get_device())
+    return _stream(stream)
+
+
 def _usable(t: torch.Tensor, what: str) -> None:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{what}: expected a torch.Tensor")
-    if t.is_cuda:
-        if t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{what}: on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
-    elif not (t.device.type == "cpu" and t.is_pinned()):
+    """Raises unless the kernels can address t: on the current device, or pinned."""
+    if isinstance(t, torch.Tensor):
+        device = t.get_device()  # -1 on the host
+        if device == _get_device() or (device < 0 and t.device.type == "cpu" and t.is_pinned()):
+            return
+        if device >= 0:
+            raise ValueError(f"{what}: on cuda:{device}, the current device is cuda:{_get_device()}")
         raise ValueError(f"{what}: must be a CUDA tensor or a pinned host tensor")
+    raise TypeError(f"{what}: expected a torch.Tensor")
 
 
-def _matrix(t: torch.Tensor, rows: int, cols: int, dtype, what: str) -> tuple[int, int]:
-    """(pointer, row stride) of a [rows, cols] tensor with contiguous columns."""
+def _matrix(t: torch.Tensor, shape: tuple, dtype, what: str) -> tuple[int, int]:
+    """(pointer, row stride) of a tensor of this shape with contiguous columns."""
     _usable(t, what)
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{what}: expected shape ({rows}, {cols}), got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     ld, step = t.stride()
-    if step != 1 and cols > 1:
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"{what}: columns must be contiguous")
     return t.data_ptr(), ld
 
@@ -92,11 +92,15 @@ def _vector(t: torch.Tensor, numel: int, dtype, what: str) -> int:
     _usable(t, what)
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != numel:
+    if t.shape != (numel,):
         raise ValueError(f"{what}: expected shape ({numel},), got {tuple(t.shape)}")
     if numel > 1 and t.stride(0) != 1:
         raise ValueError(f"{what}: must be contiguous")
     return t.data_ptr()
+
+
+def _optional(t, numel: int, dtype, what: str) -> int:
+    return 0 if t is None else _vector(t, numel, dtype, what)
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -129,15 +133,17 @@ class Checkpoint8:
             _usable(t, what)
             if t.dtype is not torch.uint8:
                 raise TypeError(f"{what}: expected torch.uint8, got {t.dtype}")
-            if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
                 raise ValueError(f"{what}: expected a matrix with contiguous columns")
         blocks = -(-cols // CHECKPOINT_BLOCK)
-        if codes.shape[0] < rows or codes.shape[1] < blocks * CHECKPOINT_BLOCK:
-            raise ValueError(f"codes: shape {tuple(codes.shape)} is too small for {rows} x {cols}")
-        if exps.shape[0] < blocks or exps.shape[1] < -(-rows // CHECKPOINT_BLOCK) * CHECKPOINT_BLOCK:
-            raise ValueError(f"exps: shape {tuple(exps.shape)} is too small for {rows} x {cols}")
+        (h, w), (eh, ew) = codes.shape, exps.shape
+        if h < rows or w < blocks * CHECKPOINT_BLOCK:
+            raise ValueError(f"codes: shape {(h, w)} is too small for {rows} x {cols}")
+        if eh < blocks or ew < -(-rows // CHECKPOINT_BLOCK) * CHECKPOINT_BLOCK:
+            raise ValueError(f"exps: shape {(eh, ew)} is too small for {rows} x {cols}")
         self.rows, self.cols, self.codes, self.exps = rows, cols, codes, exps
-        self.c = _CkptStruct(codes.data_ptr(), exps.data_ptr(), codes.stride(0), exps.stride(0), rows, cols)
+        self.c = ctypes.create_string_buffer(
+            _CKPT.pack(codes.data_ptr(), exps.data_ptr(), codes.stride(0), exps.stride(0), rows, cols), _CKPT.size)
 
     @property
     def nbytes(self) -> int:
@@ -152,28 +158,28 @@ def new_checkpoint(rows: int, cols: int, device) -> Checkpoint8:
                        torch.empty((blocks, padded), dtype=torch.uint8, device=device))
 
 
-def _ckpt(k, rows: int, cols: int, what: str):
+def _ckpt(k, shape: tuple, what: str) -> int:
     if not isinstance(k, Checkpoint8):
         raise TypeError(f"{what}: expected a Checkpoint8")
-    if k.rows != rows or k.cols != cols:
-        raise ValueError(f"{what}: checkpoint of {k.rows} x {k.cols}, expected {rows} x {cols}")
+    if (k.rows, k.cols) != shape:
+        raise ValueError(f"{what}: checkpoint of {k.rows} x {k.cols}, expected {shape[0]} x {shape[1]}")
     return ctypes.addressof(k.c)
 
 
 def zero1_checkpoint_pack(x: torch.Tensor, ckpt: Checkpoint8, stream=None) -> None:
     """Pack x (bf16 or fp32, [rows, cols]) into ckpt."""
-    code = _code(x, "x")
-    k = _ckpt(ckpt, *_dims(x, "x"), "ckpt")
-    p, ld = _matrix(x, ckpt.rows, ckpt.cols, x.dtype, "x")
-    _check_rc(_lib().zero1_checkpoint_pack(p, ld, code, k, _stream(stream)))
+    code, shape = _code(x, "x"), _dims(x, "x")
+    k = _ckpt(ckpt, shape, "ckpt")
+    p, ld = _matrix(x, shape, x.dtype, "x")
+    _check_rc(_lib().zero1_checkpoint_pack(p, ld, code, k, _launch_stream(stream)))
 
 
 def zero1_checkpoint_unpack(ckpt: Checkpoint8, out: torch.Tensor, stream=None) -> torch.Tensor:
     """Write the values ckpt stands for into out (bf16 or fp32, [rows, cols])."""
-    code = _code(out, "out")
-    k = _ckpt(ckpt, *_dims(out, "out"), "ckpt")
-    p, ld = _matrix(out, ckpt.rows, ckpt.cols, out.dtype, "out")
-    _check_rc(_lib().zero1_checkpoint_unpack(k, p, ld, code, _stream(stream)))
+    code, shape = _code(out, "out"), _dims(out, "out")
+    k = _ckpt(ckpt, shape, "ckpt")
+    p, ld = _matrix(out, shape, out.dtype, "out")
+    _check_rc(_lib().zero1_checkpoint_unpack(k, p, ld, code, _launch_stream(stream)))
     return out
 
 
@@ -186,34 +192,34 @@ class BlockNorm:
     gate_act: str = "linear"
 
 
-def _gate(gate, rows: int, cols: int):
+def _gate(gate, shape: tuple):
     """(kind, dtype code, pointer, ld) from the gate's shape: (cols,),
-    (rows, 1) or (rows, cols)."""
+    (rows, 1) or (rows, cols); with one column the last two are the same, a
+    gate per element."""
     if gate is None:
-        return _GATE_NONE, 0, None, 0
+        return _GATE_NONE, 0, 0, 0
     code = _code(gate, "gate")
     if gate.dim() == 1:
-        return _GATE_CHANNEL, code, _vector(gate, cols, gate.dtype, "gate"), 0
-    if gate.dim() == 2 and gate.shape[1] == 1 and cols != 1:
-        return (_GATE_TOKEN, code, *_matrix(gate, rows, 1, gate.dtype, "gate"))
-    return (_GATE_FULL, code, *_matrix(gate, rows, cols, gate.dtype, "gate"))
+        return _GATE_CHANNEL, code, _vector(gate, shape[1], gate.dtype, "gate"), 0
+    if gate.shape == (shape[0], 1) and shape[1] != 1:
+        return (_GATE_TOKEN, code, *_matrix(gate, (shape[0], 1), gate.dtype, "gate"))
+    return (_GATE_FULL, code, *_matrix(gate, shape, gate.dtype, "gate"))
 
 
 def _params(w_post, w_pre, cols: int):
     """(dtype code, pointers) of the two weights, which share a type."""
     w = w_post if w_post is not None else w_pre
     if w is None:
-        return ZERO1_DTYPE_BF16, None, None
-    code = _code(w, "w_post" if w is w_post else "w_pre")
-    return (code, None if w_post is None else _vector(w_post, cols, w.dtype, "w_post"),
-            None if w_pre is None else _vector(w_pre, cols, w.dtype, "w_pre"))
+        return ZERO1_DTYPE_BF16, 0, 0
+    code, dtype = _code(w, "w_post" if w is w_post else "w_pre"), w.dtype
+    return code, _optional(w_post, cols, dtype, "w_post"), _optional(w_pre, cols, dtype, "w_pre")
 
 
-def _cfg_struct(cfg: BlockNorm, rows, cols, act, res, param, gate, grad, kind, accumulate) -> _CfgStruct:
+def _cfg(cfg: BlockNorm, shape, act, res, param, gate, grad, kind, accumulate) -> bytes:
     a = _GATE_ACTS.get(cfg.gate_act)
     if a is None:
         raise ValueError(f"gate_act: {cfg.gate_act!r} is neither 'linear' nor 'sigmoid'")
-    return _CfgStruct(rows, cols, cfg.eps, cfg.residual_scale, act, res, param, gate, grad, kind, a, accumulate)
+    return _CFG.pack(*shape, cfg.eps, cfg.residual_scale, act, res, param, gate, grad, kind, a, accumulate)
 
 
 def zero1_block_norm_forward(cfg: BlockNorm, y, x, r, h=None, rstd_post=None, rstd_pre=None, *, w_post=None, w_pre=None,
@@ -225,21 +231,20 @@ def zero1_block_norm_forward(cfg: BlockNorm, y, x, r, h=None, rstd_post=None, rs
     w_pre None leaves that norm out, with its rstd (and h).  gate: None, or of
     shape (D,), (T, 1) or (T, D).  rstd_post, rstd_pre: fp32 [T], written.
     y8, r8: checkpoints of the normalised rows, written when given."""
-    rows, cols = _dims(y, "y")
-    act, res = _code(y, "y"), _code(x, "x")
-    py, ly = _matrix(y, rows, cols, y.dtype, "y")
-    px, lx = _matrix(x, rows, cols, x.dtype, "x")
-    pr, lr = _matrix(r, rows, cols, x.dtype, "r")
-    ph, lh = (None, 0) if h is None else _matrix(h, rows, cols, y.dtype, "h")
-    kind, gcode, pg, lg = _gate(gate, rows, cols)
+    shape = _dims(y, "y")
+    rows, cols = shape
+    act, res, ta, tr = _code(y, "y"), _code(x, "x"), y.dtype, x.dtype
+    py, ly = _matrix(y, shape, ta, "y")
+    px, lx = _matrix(x, shape, tr, "x")
+    pr, lr = _matrix(r, shape, tr, "r")
+    ph, lh = (0, 0) if h is None else _matrix(h, shape, ta, "h")
+    kind, gcode, pg, lg = _gate(gate, shape)
     pcode, wq, wp = _params(w_post, w_pre, cols)
-    c = _cfg_struct(cfg, rows, cols, act, res, pcode, gcode, 0, kind, 0)
-    io = _FwdStruct(py, px, wq, wp, pg, pr, ph,
-                    None if rstd_post is None else _vector(rstd_post, rows, torch.float32, "rstd_post"),
-                    None if rstd_pre is None else _vector(rstd_pre, rows, torch.float32, "rstd_pre"),
-                    None if y8 is None else _ckpt(y8, rows, cols, "y8"),
-                    None if r8 is None else _ckpt(r8, rows, cols, "r8"), ly, lx, lg, lr, lh)
-    _check_rc(_lib().zero1_block_norm_forward(ctypes.addressof(c), ctypes.addressof(io), _stream(stream)))
+    c = _cfg(cfg, shape, act, res, pcode, gcode, 0, kind, 0)
+    io = _FWD.pack(py, px, wq, wp, pg, pr, ph, _optional(rstd_post, rows, torch.float32, "rstd_post"),
+                   _optional(rstd_pre, rows, torch.float32, "rstd_pre"), 0 if y8 is None else _ckpt(y8, shape, "y8"),
+                   0 if r8 is None else _ckpt(r8, shape, "r8"), ly, lx, lg, lr, lh)
+    _check_rc(_lib().zero1_block_norm_forward(c, io, _launch_stream(stream)))
 
 
 def _scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -265,9 +270,9 @@ def _workspace(workspace, nbytes: int, device, stream) -> tuple[int | None, int,
 
 def zero1_block_norm_workspace(cfg: BlockNorm, rows: int, cols: int) -> int:
     """Bytes of scratch memory that zero1_block_norm_backward needs."""
-    c = _cfg_struct(cfg, rows, cols, 0, 0, 0, 0, 0, 0, 0)
+    c = _cfg(cfg, (rows, cols), 0, 0, 0, 0, 0, 0, 0)
     n = _i64()
-    _check_rc(_lib().zero1_block_norm_workspace(ctypes.addressof(c), ctypes.addressof(n)))
+    _check_rc(_lib().zero1_block_norm_workspace(c, ctypes.addressof(n)))
     return n.value
 
 
@@ -281,57 +286,56 @@ def zero1_block_norm_backward(cfg: BlockNorm, dh, dr, y, r, rstd_post, rstd_pre,
     may be dh, dx may be dr), dw_post and dw_pre [D] and dgate (the gate's
     shape; a [T, D] dgate has the gate's type, the other sums share one type),
     each only if given.  accumulate adds to dw_post, dw_pre and a (D,) dgate."""
-    rows, cols = _dims(dy, "dy")
-    act, res = _code(dy, "dy"), _code(dx, "dx")
-    pdy, ldy = _matrix(dy, rows, cols, dy.dtype, "dy")
-    pdx, ldx = _matrix(dx, rows, cols, dx.dtype, "dx")
-    pdh, ldh = (None, 0) if dh is None else _matrix(dh, rows, cols, dy.dtype, "dh")
-    pdr, ldr = (None, 0) if dr is None else _matrix(dr, rows, cols, dx.dtype, "dr")
-    py = pr = py8 = pr8 = None
-    ly = lr = 0
+    shape = _dims(dy, "dy")
+    rows, cols = shape
+    act, res, ta, tr = _code(dy, "dy"), _code(dx, "dx"), dy.dtype, dx.dtype
+    pdy, ldy = _matrix(dy, shape, ta, "dy")
+    pdx, ldx = _matrix(dx, shape, tr, "dx")
+    pdh, ldh = (0, 0) if dh is None else _matrix(dh, shape, ta, "dh")
+    pdr, ldr = (0, 0) if dr is None else _matrix(dr, shape, tr, "dr")
+    py = pr = py8 = pr8 = ly = lr = 0
     if isinstance(y, Checkpoint8):
-        py8 = _ckpt(y, rows, cols, "y")
+        py8 = _ckpt(y, shape, "y")
     elif y is not None:
-        py, ly = _matrix(y, rows, cols, dy.dtype, "y")
+        py, ly = _matrix(y, shape, ta, "y")
     if isinstance(r, Checkpoint8):
-        pr8 = _ckpt(r, rows, cols, "r")
+        pr8 = _ckpt(r, shape, "r")
     elif r is not None:
-        pr, lr = _matrix(r, rows, cols, dx.dtype, "r")
-    kind, gcode, pg, lg = _gate(gate, rows, cols)
+        pr, lr = _matrix(r, shape, tr, "r")
+    kind, gcode, pg, lg = _gate(gate, shape)
     pcode, wq, wp = _params(w_post, w_pre, cols)
-    sums = [t for t in (dw_post, dw_pre, dgate if kind != _GATE_FULL else None) if t is not None]
-    wcode = _code(sums[0], "a weight gradient") if sums else 0
-    wdtype = sums[0].dtype if sums else None
-    pgd, lgd = None, 0
+    first = dw_post if dw_post is not None else dw_pre if dw_pre is not None else dgate if kind != _GATE_FULL else None
+    wcode, tw = (0, None) if first is None else (_code(first, "a weight gradient"), first.dtype)
+    pgd = lgd = 0
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate: there is no gate")
         if kind == _GATE_CHANNEL:
-            pgd = _vector(dgate, cols, wdtype, "dgate")
+            pgd = _vector(dgate, cols, tw, "dgate")
         else:
-            pgd, lgd = _matrix(dgate, rows, gate.shape[1], gate.dtype if kind == _GATE_FULL else wdtype, "dgate")
-    c = _cfg_struct(cfg, rows, cols, act, res, pcode, gcode, wcode, kind, int(bool(accumulate)))
-    io = _BwdStruct(pdh, pdr, py, pr, wq, wp, pg,
-                    None if rstd_post is None else _vector(rstd_post, rows, torch.float32, "rstd_post"),
-                    None if rstd_pre is None else _vector(rstd_pre, rows, torch.float32, "rstd_pre"), py8, pr8, pdy, pdx,
-                    None if dw_post is None else _vector(dw_post, cols, wdtype, "dw_post"),
-                    None if dw_pre is None else _vector(dw_pre, cols, wdtype, "dw_pre"), pgd,
-                    ldh, ldr, ly, lr, lg, ldy, ldx, lgd)
+            pgd, lgd = _matrix(dgate, gate.shape, gate.dtype if kind == _GATE_FULL else tw, "dgate")
+    c = _cfg(cfg, shape, act, res, pcode, gcode, wcode, kind, 1 if accumulate else 0)
+    io = _BWD.pack(pdh, pdr, py, pr, wq, wp, pg, _optional(rstd_post, rows, torch.float32, "rstd_post"),
+                   _optional(rstd_pre, rows, torch.float32, "rstd_pre"), py8, pr8, pdy, pdx,
+                   _optional(dw_post, cols, tw, "dw_post"), _optional(dw_pre, cols, tw, "dw_pre"), pgd,
+                   ldh, ldr, ly, lr, lg, ldy, ldx, lgd)
     lib = _lib()
-    need = _i64()
-    if sums and workspace is None:
-        _check_rc(lib.zero1_block_norm_workspace(ctypes.addressof(c), ctypes.addressof(need)))
-    ws, nbytes, keep = _workspace(workspace, need.value, dy.device, stream)
-    _check_rc(lib.zero1_block_norm_backward(ctypes.addressof(c), ctypes.addressof(io), ws, nbytes, _stream(stream)))
+    nbytes = 0
+    if first is not None and workspace is None:
+        need = _i64()
+        _check_rc(lib.zero1_block_norm_workspace(c, ctypes.addressof(need)))
+        nbytes = need.value
+    ws, nbytes, keep = _workspace(workspace, nbytes, dy.device, stream)
+    _check_rc(lib.zero1_block_norm_backward(c, io, ws, nbytes, _launch_stream(stream)))
 
 
 def zero1_weight_grad_workspace(dy: torch.Tensor, cols: int) -> int:
     """Bytes of scratch memory that zero1_weight_grad needs for this dy and an
     input of `cols` columns."""
-    rows, n = _dims(dy, "dy")
-    p, ld = _matrix(dy, rows, n, torch.bfloat16, "dy")
+    shape = _dims(dy, "dy")
+    p, ld = _matrix(dy, shape, torch.bfloat16, "dy")
     out = _i64()
-    _check_rc(_lib().zero1_weight_grad_workspace(rows, n, cols, p, ld, ctypes.addressof(out)))
+    _check_rc(_lib().zero1_weight_grad_workspace(*shape, cols, p, ld, ctypes.addressof(out)))
     return out.value
 
 
@@ -340,19 +344,23 @@ def zero1_weight_grad(dy, x8: Checkpoint8, dw, *, col_scale=None, accumulate: bo
     """dw (+)= dy^T X * col_scale, X the values of x8: dy bf16 [T, N], x8 a
     checkpoint of [T, K], dw [N, K] bf16 or fp32 (for instance a view into a
     replica's flat gradient buffer), col_scale [K] bf16 or fp32."""
-    rows, n = _dims(dy, "dy")
-    pdy, ld = _matrix(dy, rows, n, torch.bfloat16, "dy")
-    k = _ckpt(x8, rows, x8.cols if isinstance(x8, Checkpoint8) else 0, "x8")
+    shape = _dims(dy, "dy")
+    rows, n = shape
+    pdy, ld = _matrix(dy, shape, torch.bfloat16, "dy")
+    k = _ckpt(x8, (rows, x8.cols if isinstance(x8, Checkpoint8) else 0), "x8")
+    cols = x8.cols
     code = _code(dw, "dw")
-    pw, lw = _matrix(dw, n, x8.cols, dw.dtype, "dw")
-    pc, ccode = None, 0
+    pw, lw = _matrix(dw, (n, cols), dw.dtype, "dw")
+    pc, ccode = 0, 0
     if col_scale is not None:
         ccode = _code(col_scale, "col_scale")
-        pc = _vector(col_scale, x8.cols, col_scale.dtype, "col_scale")
+        pc = _vector(col_scale, cols, col_scale.dtype, "col_scale")
     lib = _lib()
-    need = _i64()
+    nbytes = 0
     if workspace is None:
-        _check_rc(lib.zero1_weight_grad_workspace(rows, n, x8.cols, pdy, ld, ctypes.addressof(need)))
-    ws, nbytes, keep = _workspace(workspace, need.value, dy.device, stream)
-    _check_rc(lib.zero1_weight_grad(pdy, ld, n, k, pc, ccode, pw, lw, code, int(bool(accumulate)), ws, nbytes,
-                                    _stream(stream)))
+        need = _i64()
+        _check_rc(lib.zero1_weight_grad_workspace(rows, n, cols, pdy, ld, ctypes.addressof(need)))
+        nbytes = need.value
+    ws, nbytes, keep = _workspace(workspace, nbytes, dy.device, stream)
+    _check_rc(lib.zero1_weight_grad(pdy, ld, n, k, pc, ccode, pw, lw, code, 1 if accumulate else 0, ws, nbytes,
+                                    _launch_stream(stream)))

@@ -384,4 +384,19 @@ Mat exps_mat(const zero1_checkpoint8_t *c, const char *what)
 // Rows that the 128-bit path can address.
 bool vec_ok(const Mat &m) { return !m.p || ((((uintptr_t)m.p) | (uintptr_t)m.pitch) & 15) == 0; }
 
+// Lets a kernel use up to `bytes` of dynamic shared memory; asked of the
+// runtime once per kernel and device.
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = UINT64_C(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace

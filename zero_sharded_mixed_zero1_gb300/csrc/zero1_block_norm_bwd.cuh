@@ -440,7 +440,8 @@ bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t
     const int stages = stages_that_fit(T, kept, stage);
     if (stages == 0) return false;
     const int smem = kept + stages * stage;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kernel, kSmemPerSm - 1024, done);
     if (e != cudaSuccess) {
         *rc = z1_fail(ZERO1_ECUDA, "block norm backward: %s", cudaGetErrorString(e));
         return true;

@@ -229,7 +229,8 @@ bool launch_fwd_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, 
     const int stages = stages_that_fit(T, kept, stage);
     if (stages == 0) return false;
     const int smem = kept + stages * stage;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kernel, kSmemPerSm - 1024, done);
     if (e != cudaSuccess) {
         *rc = z1_fail(ZERO1_ECUDA, "block norm forward: %s", cudaGetErrorString(e));
         return true;

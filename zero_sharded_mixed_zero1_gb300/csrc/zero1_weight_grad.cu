@@ -829,7 +829,8 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
             (rc = make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
                            "the codes")))
             return rc;
-        cudaError_t e = cudaFuncSetAttribute(k_weight_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, kWgSmem);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(k_weight_grad, kWgSmem, done);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
         const int64_t items = p.whole + (int64_t)(p.tiles_k * p.tiles_n - p.whole) * p.splits;
         const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
