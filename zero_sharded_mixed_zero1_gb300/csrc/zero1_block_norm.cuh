@@ -56,10 +56,9 @@ using z1bn::Common;
 using z1bn::Fwd;
 
 constexpr int kMaxCols = ZERO1_BLOCK_NORM_MAX_COLS;
-constexpr int kWarpRows = 8;  // rows (one per warp) of a block in the narrow shapes
 
-// Threads of a block for D columns: narrow rows take a warp each.
-int row_threads(int64_t D) { return D <= 512 ? 256 : (int)round_up(D, 512) / 16; }
+// Threads of a block of the direct kernels for D columns, 16 each.
+int row_threads(int64_t D) { return (int)round_up(D, 512) / 16; }
 
 // Blocks of the backward kernel for `rows` rows: one resident wave of the
 // staged kernel at most (the per-element kernels use the same number).
@@ -71,10 +70,10 @@ int64_t bwd_blocks(int64_t rows, int64_t D, int sms)
 
 // ---------------------------------------------------------- row geometry ---
 //
-// A row lives in the registers of one warp (narrow rows) or of one block, V
-// elements per thread in chunks of 8.  On the vector path a chunk is 8
-// consecutive columns; otherwise its elements are 16 columns apart.  Either
-// way 16 neighbouring lanes hold one 128-column checkpoint block per chunk.
+// A row is shared out over a block in chunks of 8 elements per thread.  Here,
+// for the direct kernels, a chunk is 8 consecutive columns on the vector path;
+// otherwise its elements are 16 columns apart.  Either way 16 neighbouring
+// lanes hold one 128-column checkpoint block per chunk.
 
 template <bool VEC>
 __device__ __forceinline__ int chunk_col(int i, int tid, int nthr)
@@ -160,19 +159,15 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// The sum over a row, the same in every thread.  Consecutive calls in a block
-// alternate between two `red` buffers, so one barrier per call is enough.
-template <bool WARP>
+// The sum over a row, the same in every thread.  Consecutive calls alternate
+// between two `red` buffers, so one barrier per call is enough.
 __device__ __forceinline__ float row_sum(float x, float *red)
 {
+    const int lane = threadIdx.x & 31;
     x = warp_sum(x);
-    if constexpr (!WARP) {
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) red[threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.f);
-    }
-    return x;
+    if (lane == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.f);
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
@@ -241,8 +236,7 @@ __device__ __forceinline__ void load_codes(const Ckpt &c, int64_t row, int col, 
 
 // ----------------------------------------------------------------- ring ----
 //
-// Rows that 128-bit accesses can address, up to the widths whose rows fit
-// shared memory, travel through a ring of shared-memory stages, so that loads
+// Rows up to the widths that fit shared memory travel through a ring of shared-memory stages, so that loads
 // are in flight through all phases of a row and both of its sums.  A thread
 // copies its own columns (cp.async) and reads only those, so the ring needs no
 // barrier.  Bulk copies of whole rows were slower: about 12 bytes per cycle and
@@ -296,6 +290,122 @@ __device__ __forceinline__ void copy8_ahead(unsigned char *dst, const void *row,
     else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
     if constexpr (BYTES == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16), "l"(src + 16) : "memory");
 }
+
+// The same for rows at any element offset, a 4-byte word at a time: the words
+// that hold the thread's eight elements (five for bf16, whose first element
+// may be the upper half of a word) go to a slot of an odd number of words.
+// Elements from column D on arrive as zeros.  `first`: nothing of the matrix
+// lies before this row.
+template <int BYTES>
+constexpr int kSlot = BYTES == 2 ? 20 : 36;
+
+template <int BYTES>
+__device__ __forceinline__ void copy8_words(unsigned char *dst, const void *row, int col, int D, bool first)
+{
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    const char *src = static_cast<const char *>(row) + (uint32_t)(col * BYTES);
+    const int phase = BYTES == 2 ? (int)((uintptr_t)src & 2) : 0;
+    int left = (D - col) * BYTES + phase;  // bytes from the first word to the row's end
+    src -= phase;
+#pragma unroll
+    for (int j = 0; j < (BYTES == 2 ? 5 : 8); ++j, left -= 4) {
+        if (BYTES == 2 && j == 0 && phase && first && col == 0) {  // the word's lower half is before the matrix
+            reinterpret_cast<uint16_t *>(dst)[1] = *reinterpret_cast<const uint16_t *>(src + 2);
+            continue;
+        }
+        const int n = left >= 4 ? 4 : left > 0 ? left : 0;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 4 * j), "l"(n ? src + 4 * j : src), "r"(n) : "memory");
+    }
+}
+
+// Eight elements of such a slot; `row` is where the row lies in memory.
+template <class T>
+__device__ __forceinline__ V8 take8_words(const unsigned char *slot, const void *row)
+{
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(slot);
+    if constexpr (sizeof(T) == 2) {
+        const int shift = ((uintptr_t)row & 2) ? 16 : 0;
+        return from_bf16(make_uint4(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift),
+                                    __funnelshift_r(w[2], w[3], shift), __funnelshift_r(w[3], w[4], shift)));
+    } else {
+        const float *f = reinterpret_cast<const float *>(slot);
+        return V8{{pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7])}};
+    }
+}
+
+// Stores eight elements at any element offset, those from column D on left out.
+__device__ __forceinline__ void put8_any(uint16_t *row, int col, int D, const V8 &v)
+{
+    uint16_t *p = row + col;
+    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
+    const uint32_t q[4] = {pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y)};
+    if (col + 8 > D) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (col + k < D) p[k] = (uint16_t)(k & 1 ? q[k / 2] >> 16 : q[k / 2]);
+    } else if ((uintptr_t)p & 2) {
+        p[0] = (uint16_t)q[0];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(p + 1 + 2 * k) = __funnelshift_r(q[k], q[k + 1], 16);
+        p[7] = (uint16_t)(q[3] >> 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t *>(p + 2 * k) = q[k];
+    }
+}
+__device__ __forceinline__ void put8_any(float *row, int col, int D, const V8 &v)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = split(v.p[k]);
+        if (col + 2 * k < D) row[col + 2 * k] = f.x;
+        if (col + 2 * k + 1 < D) row[col + 2 * k + 1] = f.y;
+    }
+}
+
+// The values below column D, zeros beyond.
+__device__ __forceinline__ V8 below(const V8 &v, int col, int D)
+{
+    if (col + 8 <= D) return v;
+    V8 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = split(v.p[k]);
+        r.p[k] = pair(col + 2 * k < D ? f.x : 0.f, col + 2 * k + 1 < D ? f.y : 0.f);
+    }
+    return r;
+}
+
+// The ring's accesses to a row of E-byte elements, N columns in all; AL: in
+// 128-bit accesses, else at any offset.
+template <int T, bool AL>
+struct Row {
+    template <int E>
+    static __host__ __device__ constexpr int bytes(int n) { return AL ? n * E : n / 8 * kSlot<E>; }
+    template <int E>
+    static __device__ __forceinline__ int at(int i)
+    {
+        return (i * T + threadIdx.x) * (AL ? 8 * E : kSlot<E>);
+    }
+    template <int E>
+    static __device__ __forceinline__ void copy(unsigned char *region, int i, const void *row, int col, int D, bool first)
+    {
+        if constexpr (AL) copy8_ahead<E>(region + at<E>(i), row, col);
+        else copy8_words<E>(region + at<E>(i), row, col, D, first);
+    }
+    template <class V>
+    static __device__ __forceinline__ V8 take(const unsigned char *region, int i, const V *row)
+    {
+        if constexpr (AL) return take8<V>(region + at<sizeof(V)>(i), 0);
+        else return take8_words<V>(region + at<sizeof(V)>(i), row);
+    }
+    template <class V>
+    static __device__ __forceinline__ void put(V *row, int col, int D, const V8 &v)
+    {
+        if constexpr (AL) put8(row + col, v);
+        else put8_any(row, col, D, v);
+    }
+};
 
 // Waits until at most the `left` latest groups of copies are still under way.
 __device__ __forceinline__ void copies_wait(int left)

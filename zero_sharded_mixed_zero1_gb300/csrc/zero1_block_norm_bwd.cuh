@@ -15,16 +15,13 @@ namespace {
 // threads and registers are short); a second kernel adds the blocks' sums in
 // block order.
 
-template <class TA, class TR, int V, bool VEC, bool WARP, bool SACC>
-__global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm_bwd(const Common c, const Bwd a)
+template <class TA, class TR, bool VEC, bool SACC>
+__global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Common c, const Bwd a)
 {
-    constexpr int C = V / 8;
+    constexpr int C = 2, V = 8 * C;
     __shared__ float red[2][32];
-    extern __shared__ float sacc[];  // SACC: [3][V][threads]; WARP: [D] for the blocks' sum
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int nthr = WARP ? 32 : blockDim.x;
-    const int64_t row0 = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
+    extern __shared__ float sacc[];  // SACC: [3][V][threads]
+    const int tid = threadIdx.x, nthr = blockDim.x;
     float acc[SACC ? 1 : 3][C][8];
     if constexpr (SACC) {
         for (int q = 0; q < 3 * V; ++q) sacc[q * nthr + tid] = 0.f;
@@ -41,7 +38,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
         else acc[s][i][k] += x;
     };
 
-    for (int64_t row = row0; row < c.rows; row += step) {
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
         Chunk<TA, VEC> hq[C], yq[C];
         Chunk<TR, VEC> dq[C], rq[C];
         uint2 y8[C], r8[C];
@@ -84,7 +81,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
                     s1 = fmaf(d[i][k], rh[i][k], s1);
                 }
             }
-            s1 = row_sum<WARP>(s1, red[0]) * c.inv_d;
+            s1 = row_sum(s1, red[0]) * c.inv_d;
         }
         float s2 = 0.f;
         float yh[C][8];
@@ -138,7 +135,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
             }
         }
         const bool tok = a.need_gate && c.gate_kind == ZERO1_GATE_TOKEN;
-        if (post || tok) s2 = row_sum<WARP>(s2, red[1]);
+        if (post || tok) s2 = row_sum(s2, red[1]);
         if (tok && tid == 0) {
             const float dg = c.sigmoid ? s2 * gt * (1.f - gt) : s2;
             if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;
@@ -167,30 +164,13 @@ __global__ void __launch_bounds__(SACC ? 1024 : (WARP ? 256 : 512)) k_block_norm
                                                         : a.need_gate && c.gate_kind == ZERO1_GATE_CHANNEL;
         if (!need) continue;
         float *part = a.part + ((int64_t)s * gridDim.x + blockIdx.x) * c.D;
-        if constexpr (WARP) {  // the warps add up in turn
-            for (int w = 0; w < kWarpRows; ++w) {
-                if ((int)(threadIdx.x >> 5) == w) {
 #pragma unroll
-                    for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int cc = chunk_col<VEC>(i, tid, nthr) + kStep<VEC> * k;
-                            if (cc < c.D) sacc[cc] = (w ? sacc[cc] : 0.f) + acc[s][i][k];
-                        }
-                }
-                __syncthreads();
+            for (int k = 0; k < 8; ++k) {
+                const int cc = chunk_col<VEC>(i, tid, nthr) + kStep<VEC> * k;
+                if (cc < c.D) part[cc] = SACC ? sacc[(s * V + i * 8 + k) * nthr + tid] : acc[SACC ? 0 : s][i][k];
             }
-            for (int cc = threadIdx.x; cc < c.D; cc += blockDim.x) part[cc] = sacc[cc];
-            __syncthreads();
-        } else {
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int cc = chunk_col<VEC>(i, tid, nthr) + kStep<VEC> * k;
-                    if (cc < c.D) part[cc] = SACC ? sacc[(s * V + i * 8 + k) * nthr + tid] : acc[SACC ? 0 : s][i][k];
-                }
-        }
     }
 }
 
@@ -237,23 +217,26 @@ struct RowWords {
 // Where a row's inputs lie in a stage of T threads with C chunks of 8 columns.
 // SAVED: 1 both norms and dr are there and both saved activations are
 // checkpoints, 2 the same with tensors, 0 any other mix, decided at run time.
-template <class TA, class TR, int T, int C, int SAVED>
+template <class TA, class TR, int T, int C, int SAVED, bool AL>
 struct Stage {
+    using Ld = Row<T, AL>;
     static constexpr int n = 8 * C * T;
-    static constexpr int dh = 0, dr = dh + n * (int)sizeof(TA), y = dr + n * (int)sizeof(TR);
-    static constexpr int r = y + n * (SAVED == 1 ? 1 : (int)sizeof(TA));
-    static constexpr int words = r + n * (SAVED == 1 ? 1 : (int)sizeof(TR));
+    static constexpr int A = Ld::template bytes<sizeof(TA)>(n), B = Ld::template bytes<sizeof(TR)>(n);
+    static constexpr int dh = 0, dr = dh + A, y = dr + B;
+    static constexpr int r = y + (SAVED == 1 ? n : A);
+    static constexpr int words = r + (SAVED == 1 ? n : B);
     static constexpr int words_bytes = SAVED == 2 ? 16 : 64;  // of a warp
     static constexpr int gate = words + T / 32 * words_bytes;
 };
 
 // GATE: 0 none or one value per row, 1 per channel, 2 per element.  FULL: the
 // row has exactly 8 C T columns.
-template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL>
+template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL, bool AL>
 __global__ void __launch_bounds__(T, kOwnRegs / T)
 k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int stage_bytes)
 {
-    using S = Stage<TA, TR, T, C, SAVED>;
+    using S = Stage<TA, TR, T, C, SAVED, AL>;
+    using Ld = Row<T, AL>;
     constexpr int A = sizeof(TA), B = sizeof(TR), kVector = S::n * 4;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][2][16];
@@ -285,16 +268,16 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
                 const int col = tid * 8 + i * T * 8;
                 if (!in(i)) continue;
                 if (pre) {
-                    copy8_ahead<A>(to + S::dh + chunk_at<T, A>(i), dh, col);
+                    Ld::template copy<A>(to + S::dh, i, dh, col, c.D, row * a.ld_dh == 0);
                     if (r8) copy8_ahead<1>(to + S::r + chunk_at<T, 1>(i), r, col);
-                    else copy8_ahead<B>(to + S::r + chunk_at<T, B>(i), r, col);
+                    else Ld::template copy<B>(to + S::r, i, r, col, c.D, row * a.ld_r == 0);
                 }
-                if (dr) copy8_ahead<B>(to + S::dr + chunk_at<T, B>(i), ddr, col);
+                if (dr) Ld::template copy<B>(to + S::dr, i, ddr, col, c.D, row * a.ld_dr == 0);
                 if (y8) copy8_ahead<1>(to + S::y + chunk_at<T, 1>(i), y, col);
-                else if (ysaved) copy8_ahead<A>(to + S::y + chunk_at<T, A>(i), y, col);
+                else if (ysaved) Ld::template copy<A>(to + S::y, i, y, col, c.D, row * a.ld_y == 0);
                 if (GATE == 2) {
-                    if (c.gf32) copy8_ahead<4>(to + S::gate + chunk_at<T, 4>(i), gate, col);
-                    else copy8_ahead<2>(to + S::gate + chunk_at<T, 2>(i), gate, col);
+                    if (c.gf32) Ld::template copy<4>(to + S::gate, i, gate, col, c.D, row * c.ld_gate == 0);
+                    else Ld::template copy<2>(to + S::gate, i, gate, col, c.D, row * c.ld_gate == 0);
                 }
             }
         }
@@ -329,9 +312,10 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
             for (int i = 0; i < C; ++i) {
                 if (!in(i)) continue;
                 const V8 w = kept8<T, C>(kept, i);
-                d[i] = take8<TA>(b + S::dh + chunk_at<T, A>(i), 0);
+                d[i] = Ld::take(b + S::dh, i, static_cast<const TA *>(a.dh) + row * a.ld_dh);
                 if (r8) h[i] = take_codes(b + S::r + chunk_at<T, 1>(i), row_words.scale(words, row, 1, i));
-                else h[i] = mul8(take8<TR>(b + S::r + chunk_at<T, B>(i), 0), rs_pre);
+                else h[i] = mul8(Ld::take(b + S::r, i, static_cast<const TR *>(a.r) + row * a.ld_r), rs_pre);
+                if (!AL) h[i] = below(h[i], tid * 8 + i * T * 8, c.D);
                 acc_pre[i] = fma8(d[i], h[i], acc_pre[i]);
                 d[i] = mul8(d[i], w);
                 s += dot8(d[i], h[i]);
@@ -347,12 +331,13 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
         for (int i = 0; i < C; ++i) {
             const int col = tid * 8 + i * T * 8;
             if (!in(i)) continue;
-            V8 x = dr ? take8<TR>(b + S::dr + chunk_at<T, B>(i), 0) : splat8(0.f);
+            V8 x = dr ? Ld::take(b + S::dr, i, static_cast<const TR *>(a.dr) + row * a.ld_dr) : splat8(0.f);
             if (pre) x = fma8(fma8(h[i], s, d[i]), rs_pre, x);
-            put8(dx + col, x);
+            Ld::put(dx, col, c.D, x);
             if (y8) h[i] = take_codes(b + S::y + chunk_at<T, 1>(i), row_words.scale(words, row, 0, i));
-            else if (ysaved) h[i] = mul8(take8<TA>(b + S::y + chunk_at<T, A>(i), 0), rs_post);
+            else if (ysaved) h[i] = mul8(Ld::take(b + S::y, i, static_cast<const TA *>(a.y) + row * a.ld_y), rs_post);
             else h[i] = splat8(0.f);
+            if (!AL) h[i] = below(h[i], col, c.D);
             const V8 u = post ? mul8(kept8<T, C>(kept + kVector, i), h[i]) : h[i];
             if (GATE == 0) {
                 t += dot8(x, u);  // times a: the gradient of a token's gate
@@ -362,7 +347,8 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
                 if (GATE == 1) {
                     gc = kept8<T, C>(kept + 2 * kVector, i);
                 } else {
-                    gc = c.gf32 ? take8<float>(b + S::gate + chunk_at<T, 4>(i), 0) : take8<uint16_t>(b + S::gate + chunk_at<T, 2>(i), 0);
+                    gc = c.gf32 ? Ld::take(b + S::gate, i, static_cast<const float *>(c.gate) + row * c.ld_gate)
+                                : Ld::take(b + S::gate, i, static_cast<const uint16_t *>(c.gate) + row * c.ld_gate);
                     if (c.sigmoid) gc = map8(gc, [](float v) { return sigmoid(v); });
                 }
                 const V8 ax = mul8(x, c.alpha), p = mul8(ax, u);
@@ -371,8 +357,8 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
                 d[i] = mul8(ax, gc);
                 if (GATE == 2 && a.need_gate) {
                     const V8 o = c.sigmoid ? mul8(p, map8(gc, [](float v) { return v * (1.f - v); })) : p;
-                    if (c.gf32) put8(static_cast<float *>(a.dgate) + row * a.ld_dgate + col, o);
-                    else put8(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate + col, o);
+                    if (c.gf32) Ld::put(static_cast<float *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
+                    else Ld::put(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
                 }
             }
             acc_post[i] = fma8(d[i], h[i], acc_post[i]);
@@ -393,7 +379,7 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
         for (int i = 0; i < C; ++i) {
             if (!in(i)) continue;
             if (post) d[i] = mul8(fma8(h[i], t, mul8(d[i], kept8<T, C>(kept + kVector, i))), rs_post);
-            put8(dy + tid * 8 + i * T * 8, d[i]);
+            Ld::put(dy, tid * 8 + i * T * 8, c.D, d[i]);
         }
         flip ^= 1;
         if (++st == stages) st = 0;
@@ -402,7 +388,15 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         if (!in(i)) continue;
-        float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * c.D + tid * 8 + i * T * 8);
+        const int col = tid * 8 + i * T * 8;
+        if (!AL) {
+            float *part = a.part + (int64_t)blockIdx.x * c.D;
+            if (a.need_post) put8_any(part, col, c.D, acc_post[i]);
+            if (a.need_pre) put8_any(part + plane, col, c.D, acc_pre[i]);
+            if (GATE == 1 && a.need_gate) put8_any(part + 2 * plane, col, c.D, acc_gate[GATE == 1 ? i : 0]);
+            continue;
+        }
+        float4 *part = reinterpret_cast<float4 *>(a.part + (int64_t)blockIdx.x * c.D + col);
         auto put = [&](float4 *p, const V8 &v) {
             const float2 x = split(v.p[0]), y = split(v.p[1]), z = split(v.p[2]), w = split(v.p[3]);
             p[0] = make_float4(x.x, x.y, y.x, y.y);
@@ -414,13 +408,14 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
     }
 }
 
-template <class TA, class TR, int V, bool VEC, bool WARP, bool SACC>
-int launch_bwd(const Common &c, const Bwd &a, int threads, int64_t grid, cudaStream_t st)
+template <class TA, class TR, bool VEC, bool SACC>
+int launch_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
 {
-    auto kernel = k_block_norm_bwd<TA, TR, V, VEC, WARP, SACC>;
-    const int smem = SACC ? 3 * V * threads * 4 : WARP ? c.D * 4 : 0;
+    auto kernel = k_block_norm_bwd<TA, TR, VEC, SACC>;
+    const int threads = row_threads(c.D), smem = SACC ? 3 * 16 * threads * 4 : 0;
     if (SACC) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(kernel, 3 * 16 * 1024 * 4, done);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "block norm backward: %s", cudaGetErrorString(e));
     }
     kernel<<<(unsigned)grid, threads, smem, st>>>(c, a);
@@ -428,15 +423,22 @@ int launch_bwd(const Common &c, const Bwd &a, int threads, int64_t grid, cudaStr
     return launch_status("block norm backward launch");
 }
 
+template <class TA, class TR, bool VEC>
+int direct_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
+{
+    if (c.D <= 8192) return launch_bwd<TA, TR, VEC, false>(c, a, grid, st);
+    return launch_bwd<TA, TR, VEC, true>(c, a, grid, st);
+}
+
 // One resident wave of staged blocks (`grid`); false, with nothing launched, if
 // a row does not fit.
-template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL>
+template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL, bool AL>
 bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st, int *rc)
 {
-    auto kernel = k_block_norm_bwd_staged<TA, TR, T, C, GATE, SAVED, FULL>;
-    using S = Stage<TA, TR, T, C, SAVED>;
+    auto kernel = k_block_norm_bwd_staged<TA, TR, T, C, GATE, SAVED, FULL, AL>;
+    using S = Stage<TA, TR, T, C, SAVED, AL>;
     constexpr int kept = (GATE == 1 ? 3 : 2) * S::n * 4;
-    const int stage = S::gate + (GATE == 2 ? S::n * (c.gf32 ? 4 : 2) : 0);
+    const int stage = S::gate + (GATE != 2 ? 0 : c.gf32 ? S::Ld::template bytes<4>(S::n) : S::Ld::template bytes<2>(S::n));
     const int stages = stages_that_fit(T, kept, stage);
     if (stages == 0) return false;
     const int smem = kept + stages * stage;
@@ -453,35 +455,25 @@ bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t
 }
 
 template <class TA, class TR>
-bool backward_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st, int *rc)
+bool backward_staged(const Common &c, const Bwd &a, bool vec, int64_t grid, cudaStream_t st, int *rc)
 {
-    if (c.D > 8192 || (c.gate_kind == ZERO1_GATE_FULL && (!c.gvec || (a.need_gate && !a.dgvec)))) return false;
+    if (c.D > 8192) return false;
+    if (c.gate_kind == ZERO1_GATE_FULL && (!c.gvec || (a.need_gate && !a.dgvec))) vec = false;
     const int codes = (c.y8.codes != nullptr) + (c.r8.codes != nullptr);
     const int kinds = !c.w_pre || !c.w_post || !a.dr ? 0 : codes == 2 ? 1 : codes == 0 ? 2 : 0;
     return pick_threads(c.D, [&](auto t, auto n) {
         constexpr int T = decltype(t)::value, C = decltype(n)::value;
         return pick_gate(c.gate_kind, [&](auto gate) {
             constexpr int G = decltype(gate)::value;
+            if (!vec) return launch_bwd_staged<TA, TR, T, C, G, 0, false, false>(c, a, grid, st, rc);
             if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
                 const int saved = c.D == 8 * C * T ? kinds : 0;
-                if (saved == 1) return launch_bwd_staged<TA, TR, T, C, G, 1, true>(c, a, grid, st, rc);
-                if (saved == 2) return launch_bwd_staged<TA, TR, T, C, G, 2, true>(c, a, grid, st, rc);
+                if (saved == 1) return launch_bwd_staged<TA, TR, T, C, G, 1, true, true>(c, a, grid, st, rc);
+                if (saved == 2) return launch_bwd_staged<TA, TR, T, C, G, 2, true, true>(c, a, grid, st, rc);
             }
-            return launch_bwd_staged<TA, TR, T, C, G, 0, false>(c, a, grid, st, rc);
+            return launch_bwd_staged<TA, TR, T, C, G, 0, false, true>(c, a, grid, st, rc);
         });
     });
-}
-
-template <class TA, class TR, bool VEC>
-int pick_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
-{
-    const int threads = row_threads(c.D);
-    if constexpr (!VEC) {
-        if (c.D <= 256) return launch_bwd<TA, TR, 8, VEC, true, false>(c, a, threads, grid, st);
-        if (c.D <= 512) return launch_bwd<TA, TR, 16, VEC, true, false>(c, a, threads, grid, st);
-    }
-    if (c.D <= 8192) return launch_bwd<TA, TR, 16, VEC, false, false>(c, a, threads, grid, st);
-    return launch_bwd<TA, TR, 16, VEC, false, true>(c, a, threads, grid, st);
 }
 
 }  // namespace
@@ -490,6 +482,6 @@ template <class TA, class TR>
 int z1bn::run_backward(const Common &c, const Bwd &a, bool vec, int64_t grid, cudaStream_t st)
 {
     int rc;
-    if (vec && backward_staged<TA, TR>(c, a, grid, st, &rc)) return rc;
-    return vec ? pick_bwd<TA, TR, true>(c, a, grid, st) : pick_bwd<TA, TR, false>(c, a, grid, st);
+    if (backward_staged<TA, TR>(c, a, vec, grid, st, &rc)) return rc;
+    return vec ? direct_bwd<TA, TR, true>(c, a, grid, st) : direct_bwd<TA, TR, false>(c, a, grid, st);
 }

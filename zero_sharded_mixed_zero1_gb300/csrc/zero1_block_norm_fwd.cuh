@@ -10,18 +10,17 @@ namespace {
 //
 // One pass: y and x are read once, both statistics come from registers, and
 // r, h and the checkpoints are written once: 10 bytes per bf16 element with
-// both checkpoints, 8 without.  HBM is the bound.
+// both checkpoints, 8 without.  HBM is the bound.  This direct kernel takes
+// the rows that do not fit the ring of the staged one below: above 8192
+// columns, and wide fp32 rows.
 
-template <class TA, class TR, int V, bool VEC, bool WARP>
-__global__ void __launch_bounds__(V == 16 && !WARP ? 1024 : 256) k_block_norm_fwd(const Common c, const Fwd a)
+template <class TA, class TR, bool VEC>
+__global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const Fwd a)
 {
-    constexpr int C = V / 8;
+    constexpr int C = 2;
     __shared__ float red[2][32];
-    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-    const int nthr = WARP ? 32 : blockDim.x;
-    const int64_t row0 = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = WARP ? (int64_t)gridDim.x * kWarpRows : gridDim.x;
-    for (int64_t row = row0; row < c.rows; row += step) {
+    const int tid = threadIdx.x, nthr = blockDim.x;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
         Chunk<TA, VEC> yq[C];
         Chunk<TR, VEC> xq[C];
         const TA *y = static_cast<const TA *>(a.y) + row * a.ld_y;
@@ -41,7 +40,7 @@ __global__ void __launch_bounds__(V == 16 && !WARP ? 1024 : 256) k_block_norm_fw
         }
         float rs = 1.f;
         if (c.w_post) {
-            rs = rstd_of(row_sum<WARP>(ss, red[0]), c);
+            rs = rstd_of(row_sum(ss, red[0]), c);
             if (tid == 0) a.rstd_post[row] = rs;
         }
         ss = 0.f;
@@ -69,7 +68,7 @@ __global__ void __launch_bounds__(V == 16 && !WARP ? 1024 : 256) k_block_norm_fw
             for (int k = 0; k < 8; ++k) ss = fmaf(f[i][k], f[i][k], ss);
         }
         if (!c.w_pre) continue;
-        rs = rstd_of(row_sum<WARP>(ss, red[1]), c);
+        rs = rstd_of(row_sum(ss, red[1]), c);
         if (tid == 0) a.rstd_pre[row] = rs;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -92,12 +91,13 @@ __global__ void __launch_bounds__(V == 16 && !WARP ? 1024 : 256) k_block_norm_fw
 // no checkpoint, 0 any other mix, decided at run time.  FULL: the row has
 // exactly 8 C T columns.
 
-template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL>
+template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL, bool AL>
 __global__ void __launch_bounds__(T, kOwnRegs / T)
 k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int stage_bytes)
 {
+    using Ld = Row<T, AL>;
     constexpr int A = sizeof(TA), B = sizeof(TR), N = 8 * C * T, kVector = N * 4;
-    constexpr int at_y = 0, at_x = N * A, at_gate = at_x + N * B;
+    constexpr int at_y = 0, at_x = Ld::template bytes<A>(N), at_gate = at_x + Ld::template bytes<B>(N);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][2][16];
     const int tid = threadIdx.x;
@@ -116,11 +116,11 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
             for (int i = 0; i < C; ++i) {
                 const int col = tid * 8 + i * T * 8;
                 if (!in(i)) continue;
-                copy8_ahead<A>(to + at_y + chunk_at<T, A>(i), y, col);
-                copy8_ahead<B>(to + at_x + chunk_at<T, B>(i), x, col);
+                Ld::template copy<A>(to + at_y, i, y, col, c.D, row * a.ld_y == 0);
+                Ld::template copy<B>(to + at_x, i, x, col, c.D, row * a.ld_x == 0);
                 if (GATE == 2) {
-                    if (c.gf32) copy8_ahead<4>(to + at_gate + chunk_at<T, 4>(i), gate, col);
-                    else copy8_ahead<2>(to + at_gate + chunk_at<T, 2>(i), gate, col);
+                    if (c.gf32) Ld::template copy<4>(to + at_gate, i, gate, col, c.D, row * c.ld_gate == 0);
+                    else Ld::template copy<2>(to + at_gate, i, gate, col, c.D, row * c.ld_gate == 0);
                 }
             }
         }
@@ -152,7 +152,7 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            v[i] = in(i) ? take8<TA>(b + at_y + chunk_at<T, A>(i), 0) : splat8(0.f);
+            v[i] = in(i) ? Ld::take(b + at_y, i, static_cast<const TA *>(a.y) + row * a.ld_y) : splat8(0.f);
             if (post) s += dot8(v[i], v[i]);
         }
         float rs = 1.f;
@@ -171,12 +171,13 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
             if (GATE == 1) {
                 v[i] = mul8(v[i], kept8<T, C>(kept + 2 * kVector, i));
             } else if (GATE == 2) {
-                V8 g = c.gf32 ? take8<float>(b + at_gate + chunk_at<T, 4>(i), 0) : take8<uint16_t>(b + at_gate + chunk_at<T, 2>(i), 0);
+                V8 g = c.gf32 ? Ld::take(b + at_gate, i, static_cast<const float *>(c.gate) + row * c.ld_gate)
+                              : Ld::take(b + at_gate, i, static_cast<const uint16_t *>(c.gate) + row * c.ld_gate);
                 if (c.sigmoid) g = map8(g, [](float x) { return sigmoid(x); });
                 v[i] = mul8(v[i], g);
             }
-            v[i] = fma8(v[i], c.alpha * gt, take8<TR>(b + at_x + chunk_at<T, B>(i), 0));
-            put8(r + tid * 8 + i * T * 8, v[i]);
+            v[i] = fma8(v[i], c.alpha * gt, Ld::take(b + at_x, i, static_cast<const TR *>(a.x) + row * a.ld_x));
+            Ld::put(r, tid * 8 + i * T * 8, c.D, v[i]);
             if (pre) s += dot8(v[i], v[i]);
         }
         if (pre) {
@@ -187,7 +188,7 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
             for (int i = 0; i < C; ++i) {
                 v[i] = mul8(v[i], rs);
                 if (r8) keep(c.r8, row, i, v[i]);
-                if (in(i)) put8(h + tid * 8 + i * T * 8, mul8(v[i], kept8<T, C>(kept + kVector, i)));
+                if (in(i)) Ld::put(h, tid * 8 + i * T * 8, c.D, mul8(v[i], kept8<T, C>(kept + kVector, i)));
             }
         }
         flip ^= 1;
@@ -195,37 +196,28 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
     }
 }
 
-template <class TA, class TR, int V, bool VEC, bool WARP>
-int launch_fwd(const Common &c, const Fwd &a, int threads, int sms, cudaStream_t st)
+template <class TA, class TR, bool VEC>
+int launch_fwd(const Common &c, const Fwd &a, int sms, cudaStream_t st)
 {
-    auto kernel = k_block_norm_fwd<TA, TR, V, VEC, WARP>;
+    auto kernel = k_block_norm_fwd<TA, TR, VEC>;
+    const int threads = row_threads(c.D);
     const int per_sm = blocks_per_sm(reinterpret_cast<const void *>(kernel), threads);
-    const int64_t work = WARP ? (c.rows + kWarpRows - 1) / kWarpRows : c.rows;
-    const int64_t grid = work < (int64_t)sms * per_sm ? work : (int64_t)sms * per_sm;
+    const int64_t grid = c.rows < (int64_t)sms * per_sm ? c.rows : (int64_t)sms * per_sm;
     kernel<<<(unsigned)grid, threads, 0, st>>>(c, a);
     z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, per_sm, threads, 0);
     return launch_status("block norm forward launch");
 }
 
-template <class TA, class TR, bool VEC>
-int pick_fwd(const Common &c, const Fwd &a, int sms, cudaStream_t st)
-{
-    const int threads = row_threads(c.D);
-    if constexpr (!VEC) {
-        if (c.D <= 256) return launch_fwd<TA, TR, 8, VEC, true>(c, a, threads, sms, st);
-        if (c.D <= 512) return launch_fwd<TA, TR, 16, VEC, true>(c, a, threads, sms, st);
-    }
-    return launch_fwd<TA, TR, 16, VEC, false>(c, a, threads, sms, st);
-}
-
 // One resident wave of staged blocks; false, with nothing launched, if a row
 // does not fit.
-template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL>
+template <class TA, class TR, int T, int C, int GATE, int KEPT, bool FULL, bool AL>
 bool launch_fwd_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, int *rc)
 {
-    auto kernel = k_block_norm_fwd_staged<TA, TR, T, C, GATE, KEPT, FULL>;
+    auto kernel = k_block_norm_fwd_staged<TA, TR, T, C, GATE, KEPT, FULL, AL>;
+    using Ld = Row<T, AL>;
     constexpr int N = 8 * C * T, kept = (GATE == 1 ? 3 : 2) * N * 4;
-    const int stage = N * (int)(sizeof(TA) + sizeof(TR)) + (GATE == 2 ? N * (c.gf32 ? 4 : 2) : 0);
+    const int stage = Ld::template bytes<sizeof(TA)>(N) + Ld::template bytes<sizeof(TR)>(N) +
+                      (GATE != 2 ? 0 : c.gf32 ? Ld::template bytes<4>(N) : Ld::template bytes<2>(N));
     const int stages = stages_that_fit(T, kept, stage);
     if (stages == 0) return false;
     const int smem = kept + stages * stage;
@@ -244,21 +236,23 @@ bool launch_fwd_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, 
 }
 
 template <class TA, class TR>
-bool forward_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, int *rc)
+bool forward_staged(const Common &c, const Fwd &a, bool vec, int sms, cudaStream_t st, int *rc)
 {
-    if (c.D > 8192 || (c.gate_kind == ZERO1_GATE_FULL && !c.gvec)) return false;
+    if (c.D > 8192) return false;
+    if (c.gate_kind == ZERO1_GATE_FULL && !c.gvec) vec = false;
     const int codes = (c.y8.codes != nullptr) + (c.r8.codes != nullptr);
     const int kinds = !c.w_pre || !c.w_post ? 0 : codes == 2 ? 1 : codes == 0 ? 2 : 0;
     return pick_threads(c.D, [&](auto t, auto n) {
         constexpr int T = decltype(t)::value, C = decltype(n)::value;
         return pick_gate(c.gate_kind, [&](auto gate) {
             constexpr int G = decltype(gate)::value;
+            if (!vec) return launch_fwd_staged<TA, TR, T, C, G, 0, false, false>(c, a, sms, st, rc);
             if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
                 const int kept = c.D == 8 * C * T ? kinds : 0;
-                if (kept == 1) return launch_fwd_staged<TA, TR, T, C, G, 1, true>(c, a, sms, st, rc);
-                if (kept == 2) return launch_fwd_staged<TA, TR, T, C, G, 2, true>(c, a, sms, st, rc);
+                if (kept == 1) return launch_fwd_staged<TA, TR, T, C, G, 1, true, true>(c, a, sms, st, rc);
+                if (kept == 2) return launch_fwd_staged<TA, TR, T, C, G, 2, true, true>(c, a, sms, st, rc);
             }
-            return launch_fwd_staged<TA, TR, T, C, G, 0, false>(c, a, sms, st, rc);
+            return launch_fwd_staged<TA, TR, T, C, G, 0, false, true>(c, a, sms, st, rc);
         });
     });
 }
@@ -269,6 +263,6 @@ template <class TA, class TR>
 int z1bn::run_forward(const Common &c, const Fwd &a, bool vec, int sms, cudaStream_t st)
 {
     int rc;
-    if (vec && forward_staged<TA, TR>(c, a, sms, st, &rc)) return rc;
-    return vec ? pick_fwd<TA, TR, true>(c, a, sms, st) : pick_fwd<TA, TR, false>(c, a, sms, st);
+    if (forward_staged<TA, TR>(c, a, vec, sms, st, &rc)) return rc;
+    return vec ? launch_fwd<TA, TR, true>(c, a, sms, st) : launch_fwd<TA, TR, false>(c, a, sms, st);
 }
