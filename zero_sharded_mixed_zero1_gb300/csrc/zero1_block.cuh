@@ -277,6 +277,57 @@ __device__ __forceinline__ void put8(float *p, const V8 &v)
     st_stream(p + 4, c.x, c.y, d.x, d.y);
 }
 
+// Stores eight elements at any element offset, those from column D on left out.
+__device__ __forceinline__ void put8_any(uint16_t *row, int64_t col, int64_t D, const V8 &v)
+{
+    uint16_t *p = row + col;
+    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
+    const uint32_t q[4] = {pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y)};
+    if (col + 8 > D) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (col + k < D) p[k] = (uint16_t)(k & 1 ? q[k / 2] >> 16 : q[k / 2]);
+    } else if ((uintptr_t)p & 2) {
+        p[0] = (uint16_t)q[0];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(p + 1 + 2 * k) = __funnelshift_r(q[k], q[k + 1], 16);
+        p[7] = (uint16_t)(q[3] >> 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t *>(p + 2 * k) = q[k];
+    }
+}
+__device__ __forceinline__ void put8_any(float *row, int64_t col, int64_t D, const V8 &v)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = split(v.p[k]);
+        if (col + 2 * k < D) row[col + 2 * k] = f.x;
+        if (col + 2 * k + 1 < D) row[col + 2 * k + 1] = f.y;
+    }
+}
+
+// Eight bf16 elements at any element offset, zeros from column D on, by the
+// aligned words that hold them.  `first`: nothing of the matrix lies before
+// this row.
+__device__ __forceinline__ V8 load8_any(const uint16_t *row, int64_t col, int64_t D, bool first)
+{
+    const uint16_t *p = row + col;
+    const int odd = (int)(((uintptr_t)p & 2) >> 1);
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p - odd);
+    const int64_t left = D - col + odd;  // elements from the first word to the row's end
+    uint32_t w[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) {
+        w[j] = 0;
+        if (j == 0 && odd && first && col == 0) w[j] = (uint32_t)p[0] << 16;
+        else if (left >= 2 * j + 2) w[j] = __ldg(q + j);
+        else if (left == 2 * j + 1) w[j] = reinterpret_cast<const uint16_t *>(q + j)[0];
+    }
+    return from_bf16(make_uint4(__funnelshift_r(w[0], w[1], 16 * odd), __funnelshift_r(w[1], w[2], 16 * odd),
+                                __funnelshift_r(w[2], w[3], 16 * odd), __funnelshift_r(w[3], w[4], 16 * odd)));
+}
+
 // The larger magnitude of three, NaN if one is.
 __device__ __forceinline__ float max_abs(float a, float b, float c)
 {

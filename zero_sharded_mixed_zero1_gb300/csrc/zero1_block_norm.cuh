@@ -333,36 +333,6 @@ __device__ __forceinline__ V8 take8_words(const unsigned char *slot, const void 
     }
 }
 
-// Stores eight elements at any element offset, those from column D on left out.
-__device__ __forceinline__ void put8_any(uint16_t *row, int col, int D, const V8 &v)
-{
-    uint16_t *p = row + col;
-    const float2 a = split(v.p[0]), b = split(v.p[1]), c = split(v.p[2]), d = split(v.p[3]);
-    const uint32_t q[4] = {pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y), pack_bf16x2(d.x, d.y)};
-    if (col + 8 > D) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (col + k < D) p[k] = (uint16_t)(k & 1 ? q[k / 2] >> 16 : q[k / 2]);
-    } else if ((uintptr_t)p & 2) {
-        p[0] = (uint16_t)q[0];
-#pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t *>(p + 1 + 2 * k) = __funnelshift_r(q[k], q[k + 1], 16);
-        p[7] = (uint16_t)(q[3] >> 16);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t *>(p + 2 * k) = q[k];
-    }
-}
-__device__ __forceinline__ void put8_any(float *row, int col, int D, const V8 &v)
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = split(v.p[k]);
-        if (col + 2 * k < D) row[col + 2 * k] = f.x;
-        if (col + 2 * k + 1 < D) row[col + 2 * k + 1] = f.y;
-    }
-}
-
 // The values below column D, zeros beyond.
 __device__ __forceinline__ V8 below(const V8 &v, int col, int D)
 {

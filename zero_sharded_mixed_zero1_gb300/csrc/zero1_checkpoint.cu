@@ -6,10 +6,13 @@
 namespace {
 
 // Both kernels are one pass over the matrix: 3 bytes per bf16 element (2 + 1)
-// plus 1/128 of scales, bound by HBM.  A thread owns 8 columns of kRows
-// consecutive rows, so that 16 lanes hold one 128-column block (its maximum is
-// four shuffles), kRows 16-byte loads are in flight per thread, and the four
-// scale bytes of a column block leave as one 32-bit store.
+// plus 1/128 of scales, bound by HBM (8192 x 14336 bf16: pack 6.0, unpack 6.3
+// TB/s).  A thread owns 8 columns of kRows consecutive rows, so that 16 lanes
+// hold one 128-column block (its maximum is four shuffles), kRows 16-byte loads
+// are in flight per thread, and the four scale bytes of a column block leave as
+// one 32-bit store.  Off the 128-bit path a thread's columns are 16 apart, but
+// consecutive where bf16 is packed: the aligned words that hold them are read
+// (20000 x 3001: 130 -> 63 us; written that way they took longer, 49 -> 54 us).
 constexpr int kRows = 4;
 constexpr int kThreads = 256;
 
@@ -23,46 +26,52 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(const T *__restrict__ x,
 {
     const int64_t kp = (s.cols + kQBlock - 1) / kQBlock * kQBlock;
     const int64_t row0 = ((int64_t)blockIdx.x * (kThreads / s.tx) + threadIdx.x / s.tx) * kRows;
-    // the thread's 8 columns: consecutive on the vector path; 16 apart from
-    // one another, in the same 128-column block, on the per-element path
+    constexpr bool kNext = VEC || sizeof(T) == 2;  // the thread's 8 columns are consecutive, else 16 apart
     const int64_t v = (int64_t)blockIdx.y * s.tx + threadIdx.x % s.tx;
-    const int64_t col0 = VEC ? v * 8 : v / 16 * kQBlock + v % 16;
-    constexpr int step = VEC ? 1 : 16;
-    float f[kRows][8];
+    const int64_t col0 = kNext ? v * 8 : v / 16 * kQBlock + v % 16;
+    V8 f[kRows];
+    if constexpr (VEC) {  // all loads before the first use
+        Raw8<T> q[kRows];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        const bool in = row0 + r < s.rows;
-        const T *p = x + (row0 + r) * ld + col0;
-        if constexpr (VEC) {
-            Raw8<T> q;
-            q.zero();
-            if (in && col0 < s.cols) q.load(p);
-            q.get(f[r]);
-        } else {
+        for (int r = 0; r < kRows; ++r) {
+            q[r].zero();
+            if (row0 + r < s.rows && col0 < s.cols) q[r].load(x + (row0 + r) * ld + col0);
+        }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) f[r][k] = in && col0 + k * step < s.cols ? ld1(p + k * step) : 0.f;
+        for (int r = 0; r < kRows; ++r) {
+            float e[8];
+            q[r].get(e);
+            f[r] = V8{{pair(e[0], e[1]), pair(e[2], e[3]), pair(e[4], e[5]), pair(e[6], e[7])}};
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            const T *row = x + (row0 + r) * ld;
+            f[r] = splat8(0.f);
+            if (row0 + r >= s.rows || col0 >= s.cols) continue;
+            if constexpr (kNext) {
+                f[r] = load8_any(row, col0, s.cols, (row0 + r) * ld == 0);
+            } else {
+                float e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = col0 + 16 * k < s.cols ? ld1(row + col0 + 16 * k) : 0.f;
+                f[r] = V8{{pair(e[0], e[1]), pair(e[2], e[3]), pair(e[4], e[5]), pair(e[6], e[7])}};
+            }
         }
     }
     uint32_t exps = 0;
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, mag_bits(f[r][k]));
-        const int E = scale_exp(max16(m));
-        const float inv = scale_inv(E);
-        const bool ok = E != kNanE;
+        int E;
+        const uint2 q = encode8(f[r], E);
         exps |= (uint32_t)E << (8 * r);
-        uint2 q;
-        q.x = code4(f[r][0], f[r][1], f[r][2], f[r][3], inv, ok);
-        q.y = code4(f[r][4], f[r][5], f[r][6], f[r][7], inv, ok);
         if (row0 + r < s.rows && col0 < kp) {
             uint8_t *o = c.codes + (row0 + r) * c.ld_codes + col0;
-            if constexpr (VEC) {
+            if constexpr (kNext) {
                 __stcs(reinterpret_cast<uint2 *>(o), q);
             } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k * step] = (uint8_t)((k < 4 ? q.x : q.y) >> (8 * (k & 3)));
+                for (int k = 0; k < 8; ++k) o[16 * k] = (uint8_t)((k < 4 ? q.x : q.y) >> (8 * (k & 3)));
             }
         }
     }
@@ -82,7 +91,6 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(Ckpt c, Tiles s, T *__
     const int64_t row0 = ((int64_t)blockIdx.x * (kThreads / s.tx) + threadIdx.x / s.tx) * kRows;
     const int64_t v = (int64_t)blockIdx.y * s.tx + threadIdx.x % s.tx;
     const int64_t col0 = VEC ? v * 8 : v / 16 * kQBlock + v % 16;
-    constexpr int step = VEC ? 1 : 16;
     if (row0 >= s.rows || col0 >= s.cols) return;
     uint2 q[kRows];
     uint32_t exps = 0;
@@ -97,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(Ckpt c, Tiles s, T *__
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (col0 + k * step < s.cols) (k < 4 ? q[r].x : q[r].y) |= (uint32_t)p[k * step] << (8 * (k & 3));
+                if (col0 + 16 * k < s.cols) (k < 4 ? q[r].x : q[r].y) |= (uint32_t)p[16 * k] << (8 * (k & 3));
         }
         exps |= (uint32_t)e[r] << (8 * r);
     }
@@ -112,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_unpack(Ckpt c, Tiles s, T *__
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (col0 + k * step < s.cols) st1(p + k * step, f[k]);
+                if (col0 + 16 * k < s.cols) st1(p + 16 * k, f[k]);
         }
     }
 }
