@@ -310,7 +310,7 @@ __device__ __forceinline__ void put8_any(float *row, int64_t col, int64_t D, con
 // Eight bf16 elements at any element offset, zeros from column D on, by the
 // aligned words that hold them.  `first`: nothing of the matrix lies before
 // this row.
-__device__ __forceinline__ V8 load8_any(const uint16_t *row, int64_t col, int64_t D, bool first)
+__device__ __forceinline__ uint4 load8_any(const uint16_t *row, int64_t col, int64_t D, bool first)
 {
     const uint16_t *p = row + col;
     const int odd = (int)(((uintptr_t)p & 2) >> 1);
@@ -324,8 +324,8 @@ __device__ __forceinline__ V8 load8_any(const uint16_t *row, int64_t col, int64_
         else if (left >= 2 * j + 2) w[j] = __ldg(q + j);
         else if (left == 2 * j + 1) w[j] = reinterpret_cast<const uint16_t *>(q + j)[0];
     }
-    return from_bf16(make_uint4(__funnelshift_r(w[0], w[1], 16 * odd), __funnelshift_r(w[1], w[2], 16 * odd),
-                                __funnelshift_r(w[2], w[3], 16 * odd), __funnelshift_r(w[3], w[4], 16 * odd)));
+    return make_uint4(__funnelshift_r(w[0], w[1], 16 * odd), __funnelshift_r(w[1], w[2], 16 * odd),
+                      __funnelshift_r(w[2], w[3], 16 * odd), __funnelshift_r(w[3], w[4], 16 * odd));
 }
 
 // The larger magnitude of three, NaN if one is.
@@ -448,6 +448,24 @@ cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t> &done)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
+}
+
+// launch_pdl with any grid and dynamic shared memory: the kernel calls
+// wait_prior_grid() before it touches global memory.
+template <class K, class... Args>
+cudaError_t launch_after(K kernel, dim3 grid, int block, int smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace

@@ -306,16 +306,7 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
     f.out[2] = chan ? io->dgate : nullptr;
     f.gate = chan && cfg->gate_act == ZERO1_GATE_SIGMOID ? io->gate : nullptr;
     f.gf32 = cfg->gate_dtype == ZERO1_DTYPE_F32;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)((D + 31) / 32), 3);
-    lc.blockDim = dim3(256);
-    lc.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, k_block_norm_finish, f);
+    const cudaError_t e = launch_after(k_block_norm_finish, dim3((unsigned)((D + 31) / 32), 3), 256, 0, st, f);
     if (e != cudaSuccess) return pdl_fail(e, "block norm backward: column sums");
     return ZERO1_OK;
 }

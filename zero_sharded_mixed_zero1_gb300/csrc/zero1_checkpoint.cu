@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) k_ckpt_pack(const T *__restrict__ x,
             f[r] = splat8(0.f);
             if (row0 + r >= s.rows || col0 >= s.cols) continue;
             if constexpr (kNext) {
-                f[r] = load8_any(row, col0, s.cols, (row0 + r) * ld == 0);
+                f[r] = from_bf16(load8_any(row, col0, s.cols, (row0 + r) * ld == 0));
             } else {
                 float e[8];
 #pragma unroll

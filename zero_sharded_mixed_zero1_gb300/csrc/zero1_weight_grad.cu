@@ -430,6 +430,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     __syncthreads();
     cluster_sync();
     tc_after();
+    wait_prior_grid();  // up to here this kernel may run beside the one before it
     const uint32_t tmem = bar.tmem;
     const int items = items_of(a);
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -641,13 +642,13 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
     }
 }
 
-// Copies dy to rows that start on 16-byte boundaries.
+// Copies dy to rows that start on 16-byte boundaries, eight elements per thread.
 __global__ void __launch_bounds__(256)
 k_align_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t T, int64_t N, uint16_t *__restrict__ dst, int64_t ld_dst)
 {
-    for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
-        for (int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x; c < ld_dst; c += gridDim.y * 256)
-            dst[t * ld_dst + c] = c < N ? src[t * ld + c] : (uint16_t)0;
+    for (int64_t c = ((int64_t)blockIdx.y * 32 + threadIdx.x % 32) * 8; c < N; c += (int64_t)gridDim.y * 256)
+        for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; t < T; t += (int64_t)gridDim.x * 8)
+            *reinterpret_cast<uint4 *>(dst + t * ld_dst + c) = load8_any(src + t * ld, c, N, t * ld == 0);
 }
 
 // --------------------------------------------------------------- launch ----
@@ -818,7 +819,7 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
         int64_t ld = T > 1 ? ld_dy : round_up(n, 8);
         if (!rows_aligned(dy, ld_dy, T)) {
             uint16_t *copy = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + p.copy_at);
-            const dim3 grid((unsigned)(T < 4096 ? T : 4096), (unsigned)(p.ld_copy < 256 * 65535 ? (p.ld_copy + 255) / 256 : 65535));
+            const dim3 grid((unsigned)(T < 32768 ? (T + 7) / 8 : 4096), (unsigned)(p.ld_copy < 256 * 65535 ? (p.ld_copy + 255) / 256 : 65535));
             k_align_rows<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(dy), T > 1 ? ld_dy : 0, T, n, copy, p.ld_copy);
             if ((rc = launch_status("weight gradient: aligned copy")) != ZERO1_OK) return rc;
             src = copy;
@@ -834,9 +835,10 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
         const int64_t items = p.whole + (int64_t)(p.tiles_k * p.tiles_n - p.whole) * p.splits;
         const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
-        k_weight_grad<<<grid, kWgThreads, kWgSmem, st>>>(mdy, mx, a);
+        const cudaError_t le = launch_after(k_weight_grad, dim3(grid), kWgThreads, kWgSmem, st, mdy, mx, a);
+        if (le != cudaSuccess) return pdl_fail(le, "weight gradient launch");
         z1_note_launch(reinterpret_cast<const void *>(k_weight_grad), grid, 1, kWgThreads, 0);
-        if ((rc = launch_status("weight gradient launch")) != ZERO1_OK || p.splits == 1) return rc;
+        if (p.splits == 1) return ZERO1_OK;
     } else {
         a.whole = a.splits = 0;
     }
@@ -845,16 +847,7 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
         const int run = tiles - t < 65535 ? tiles - t : 65535;
         Wg j = a;
         j.whole = t;
-        cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(kTileN / 8, (unsigned)run);
-        lc.blockDim = dim3(256);
-        lc.stream = st;
-        cudaLaunchAttribute at[1];
-        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[0].val.programmaticStreamSerializationAllowed = 1;
-        lc.attrs = at;
-        lc.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&lc, k_weight_grad_join, j);
+        const cudaError_t e = launch_after(k_weight_grad_join, dim3(kTileN / 8, (unsigned)run), 256, 0, st, j);
         if (e != cudaSuccess) return pdl_fail(e, "weight gradient: joining the parts");
         t += run;
     }
