@@ -65,14 +65,14 @@ def _launch_stream(stream) -> int:
 
 def _usable(t: torch.Tensor, what: str) -> None:
     """Raises unless the kernels can address t: on the current device, or pinned."""
-    if isinstance(t, torch.Tensor):
-        device = t.get_device()  # -1 on the host
-        if device == _get_device() or (device < 0 and t.device.type == "cpu" and t.is_pinned()):
-            return
-        if device >= 0:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{what}: expected a torch.Tensor")
+    device = t.get_device()  # -1 on the host
+    if device >= 0:
+        if device != _get_device():
             raise ValueError(f"{what}: on cuda:{device}, the current device is cuda:{_get_device()}")
+    elif not (t.device.type == "cpu" and t.is_pinned()):
         raise ValueError(f"{what}: must be a CUDA tensor or a pinned host tensor")
-    raise TypeError(f"{what}: expected a torch.Tensor")
 
 
 def _matrix(t: torch.Tensor, shape: tuple, dtype, what: str) -> tuple[int, int]:

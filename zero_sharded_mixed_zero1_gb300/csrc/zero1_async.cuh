@@ -9,6 +9,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+// The status word of the weight-gradient kernel's source (a cudaError_t as int),
+// part of what zero1_device_status reports.
+int z1_weight_grad_status(uint32_t *status, int32_t clear);
+
 namespace {
 
 __device__ uint32_t g_zero1_status;  // bit 0: a bounded wait ran out

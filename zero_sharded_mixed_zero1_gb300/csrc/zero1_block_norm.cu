@@ -261,6 +261,7 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
         (io->dw_pre && (rc = check_natural(io->dw_pre, ew, "dw_pre"))) ||
         (io->dgate && (rc = check_mat(out[4], edg, true, call))))
         return rc;
+    if ((rc = check_overlaps(out, in_place, 6, in, 13, call)) != ZERO1_OK) return rc;
     const int sms = sm_count();
     if (sms == 0) return z1_fail(ZERO1_ECUDA, "%s: no CUDA device", call);
     const int64_t grid = bwd_blocks(T, D, sms);
@@ -273,7 +274,6 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
                            (long long)(workspace ? workspace_bytes : 0), (long long)need);
         if ((uintptr_t)workspace & 15) return z1_fail(ZERO1_EALIGN, "%s: the workspace is not 16-byte aligned", call);
     }
-    if ((rc = check_overlaps(out, in_place, 6, in, 13, call)) != ZERO1_OK) return rc;
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (T > 0) {

@@ -71,10 +71,6 @@ int z1_scaler_advance(zero1_scaler_t *scaler, const zero1_loss_scale_policy_t *p
 int z1_check_scaler_and_policy(const zero1_scaler_t *scaler, const zero1_loss_scale_policy_t *policy,
                                const zero1_adamw_t *hp, int32_t M);
 
-// The status word of the weight-gradient kernel's bounded waits (a cudaError_t
-// as int; part of zero1_device_status).
-int z1_weight_grad_status(uint32_t *status, int32_t clear);
-
 // Record a kernel launch for zero1_debug_last_launch (per host thread): the
 // kernel, its grid, the resident blocks per SM the grid was sized from, and
 // whether the vector body moved fp32 in 32-byte accesses.

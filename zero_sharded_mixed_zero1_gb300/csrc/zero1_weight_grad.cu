@@ -783,6 +783,10 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     if ((rc = check_mat(my, 2, false, call)) || (rc = check_mat(mo, eo, true, call)) ||
         (col_scale && (rc = check_natural(col_scale, es, "col_scale"))))
         return rc;
+    const Mat in[] = {my, codes_mat(x8, "the codes of x8"), exps_mat(x8, "the exps of x8"),
+                      mat(col_scale, 1, K, 0, es, "col_scale")};
+    for (const Mat &m : in)
+        if (mats_overlap(mo, m)) return z1_fail(ZERO1_EINVAL, "%s: dw and %s overlap", call, m.what);
     Plan p;
     if ((rc = plan_of(T, n, K, dy, ld_dy, &p)) != ZERO1_OK) return rc;
     if (p.bytes > 0) {
@@ -790,13 +794,10 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
             return z1_fail(ZERO1_EINVAL, "%s: workspace of %lld bytes, needs %lld", call,
                            (long long)(workspace ? workspace_bytes : 0), (long long)p.bytes);
         if ((uintptr_t)workspace & 127) return z1_fail(ZERO1_EALIGN, "%s: the workspace is not 128-byte aligned", call);
+        const Mat w{workspace, 1, p.bytes, p.bytes, "the workspace"};
+        for (const Mat &m : {mo, in[0], in[1], in[2], in[3]})
+            if (mats_overlap(w, m)) return z1_fail(ZERO1_EINVAL, "%s: the workspace and %s overlap", call, m.what);
     }
-    const Mat in[] = {my, codes_mat(x8, "the codes of x8"), exps_mat(x8, "the exps of x8"),
-                      mat(col_scale, 1, K, 0, es, "col_scale"), Mat{workspace, 1, p.bytes, p.bytes, "the workspace"}};
-    for (const Mat &m : in)
-        if (mats_overlap(mo, m)) return z1_fail(ZERO1_EINVAL, "%s: dw and %s overlap", call, m.what);
-    for (int q = 0; q < 4; ++q)
-        if (mats_overlap(in[4], in[q])) return z1_fail(ZERO1_EINVAL, "%s: the workspace and %s overlap", call, in[q].what);
     if (T > 0 && (in_host_memory(dy) || in_host_memory(x8->codes) || in_host_memory(x8->exps)))
         return z1_fail(ZERO1_EINVAL, "%s: dy and x8 must be device memory", call);
 
