@@ -444,6 +444,29 @@ def test_weight_grad(cuda_device, T, N, K, out, scaled):
     check_weight_grad(dw, dy, checkpoint_values(k), col if scaled else None, T)
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("T,N,K", [(4500, 300, 200), (4096, 2600, 2300), (131200, 40, 72)])
+def test_weight_grad_over_many_rows(cuda_device, T, N, K, out, accumulate):
+    """Sums of several runs of the accumulator, in whole tiles and in parts; an
+    fp32 result is near fp32 rounding however many rows there are."""
+    g = torch.Generator(device=cuda_device).manual_seed(T)
+    x = torch.randn((T, K), generator=g, device=cuda_device)
+    dy = (torch.randn((T, N), generator=g, device=cuda_device) * 1e-2).to(BF16)
+    k = z.new_checkpoint(T, K, cuda_device)
+    z.zero1_checkpoint_pack(x, k)
+    xv = torch.empty((T, K), device=cuda_device)
+    z.zero1_checkpoint_unpack(k, xv)
+    start = 0.25 if accumulate else 0.0
+    dw = torch.full((N, K), start, dtype=out, device=cuda_device)
+    z.zero1_weight_grad(dy, k, dw, accumulate=accumulate)
+    want = dy.double().t() @ xv.double()
+    err = (dw.double() - start - want).norm() / (want.norm() + start * (N * K) ** 0.5)
+    # a run of 2048 rows in the tensor cores is within 1e-6 of its norm, the
+    # addition of the runs within T / 2048 half ulps; bf16 adds 2^-9
+    assert err <= 1e-6 + T / 2048 * ref.U + (2.0 ** -9 if out == BF16 else 0.0)
+
+
 @pytest.mark.parametrize("pad", [0, 1, 8])
 @pytest.mark.parametrize("off", [0, 1, 8])
 @pytest.mark.parametrize("out", [BF16, F32])

@@ -25,6 +25,11 @@ namespace {
 // of the contraction where a CTA alone would load 40.  Products are exact in
 // fp32; sums are fp32 in the accumulator.
 //
+// The tensor cores truncate where fp32 would round, an error that grows with
+// the number of additions: 2e-7 of a gradient's norm over 777 rows, 1.5e-6 over
+// 4096, 9e-6 over 16384.  For bf16 results that is nothing; for fp32 ones the
+// accumulator is emptied every 2048 rows and the runs are added in fp32.
+//
 // Roles (28 warps): warp 0 loads dy and warp 3 the codes, warp 1 of the
 // leading CTA issues the MMAs, warps 4-19 convert (four sets of four take
 // stages in turn), warps 20-27 store the result (each 32 lanes and half of the
@@ -34,6 +39,7 @@ namespace {
 
 constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
 constexpr int kDeep = 64;                  // rows of the contraction per stage
+constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time
 constexpr int kStages = 8;                 // of B in shared and A in tensor memory
 constexpr int kCodeStages = 8;             // of codes and scales in shared memory
 constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;  // of a CTA, per stage
@@ -55,6 +61,7 @@ struct Wg {
     int64_t T, N, K;
     int tiles_k, tiles_n, kblocks;      // kblocks: stages of the whole contraction
     int whole, splits, per_split;       // tiles done whole; the others in this many parts of per_split stages
+    int run;                            // stages summed in the accumulator at one time
     const uint8_t *exps;
     int64_t ld_exps;
     const void *scale;
@@ -347,56 +354,46 @@ __device__ __forceinline__ void store_bf16(const Wg &a, uint32_t acc, int64_t k0
     }
 }
 
-// The two columns that this lane stores of one of the rows j, j + 1.
-__device__ __forceinline__ float2 trade(float v0, float v1)
+// Adds to what this thread stored before, or to the caller's gradient.  Only
+// this thread ever adds there, one addition after the other, so the order of
+// the sum is fixed; a reduction leaves no value to wait for.
+__device__ __forceinline__ void add_to(float *p, float x) { asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory"); }
+__device__ __forceinline__ void add_to(float *p, float2 x)
+{
+    asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x.x), "f"(x.y) : "memory");
+}
+// fp32 results, 32 lanes x 128 rows, two columns of a row per lane as above
+// (one column per lane, in the lanes' order, took twice the instructions and
+// more time).  rows: how many of the 128 are stored; cols: of this lane's two.
+template <bool ADD>
+__device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int cols, bool pairs, float scale, uint32_t acc,
+                                          uint64_t *dempty)
 {
     const bool up = threadIdx.x & 8;
-    const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-    return up ? make_float2(got, v1) : make_float2(v0, got);
-}
-
-__device__ __forceinline__ void store_f32(const Wg &a, uint32_t acc, int64_t k0, int64_t n0, uint64_t *dempty)
-{
-    const int lane = threadIdx.x & 31;
-    const bool up = lane & 8;
-    float scale = 1.f;
-    if (a.scale && k0 + own_column(lane) < a.K) scale = ld_param(a.scale, a.scale_f32, k0 + own_column(lane));
-    const int64_t k = k0 + (lane & 16) + 2 * (lane & 7);
-    const bool two = k + 1 < a.K;
-    const bool easy = a.pairs && !a.accumulate && n0 + kTileN / 2 <= a.N && k0 + 32 <= a.K;
+    const bool easy = pairs && cols == 2 && rows == kTileN / 2;
+    o += up ? ld : 0;
+#pragma unroll 1
     for (int c = 0; c < kTileN / 2; c += 32) {
         uint32_t v[32];
         tc_load32(acc + c, v);
         if (c + 32 == kTileN / 2) release_acc(dempty);
-        float *o = static_cast<float *>(a.dw) + (n0 + c + (up ? 1 : 0)) * a.ld_dw + k;
-        if (easy) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 2, o += 2 * a.ld_dw)
-                *reinterpret_cast<float2 *>(o) = trade(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale);
-            continue;
+        for (int j = 0; j < 32; j += 2, o += 2 * ld) {
+            const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
+            const float2 x = up ? make_float2(got, v1) : make_float2(v0, got);
+            if (easy) {
+                if (ADD) add_to(o, x);
+                else *reinterpret_cast<float2 *>(o) = x;
+            } else if (c + j + up < rows) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= cols) continue;
+                    if (ADD) add_to(o + e, e ? x.y : x.x);
+                    else o[e] = e ? x.y : x.x;
+                }
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 32; j += 2, o += 2 * a.ld_dw) {
-            const float2 x = trade(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale);
-            if (n0 + c + j + (up ? 1 : 0) >= a.N || k >= a.K) continue;
-            o[0] = a.accumulate ? o[0] + x.x : x.x;
-            if (two) o[1] = a.accumulate ? o[1] + x.y : x.y;
-        }
-    }
-}
-
-// A part's sums, as a whole tile of the workspace.
-__device__ __forceinline__ void store_part(float *part, uint32_t acc, int k, int n, uint64_t *dempty)
-{
-    const int lane = threadIdx.x & 31;
-    float *o = part + (n + ((lane >> 3) & 1)) * kTileK + k + (lane & 16) + 2 * (lane & 7);
-    for (int c = 0; c < kTileN / 2; c += 32, o += 32 * kTileK) {
-        uint32_t v[32];
-        tc_load32(acc + c, v);
-        if (c + 32 == kTileN / 2) release_acc(dempty);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2)
-            *reinterpret_cast<float2 *>(o + j * kTileK) = trade(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
     }
 }
 
@@ -484,27 +481,30 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             warp_wait(&bar.cfull[q % kCodeStages], (q / kCodeStages) & 1);
     } else if (warp == 1) {
         if (rank == 0) {
-            uint32_t it = 0, tile = 0;
+            uint32_t it = 0, tile = 0;  // stages and accumulator fills so far
             bool ok = true;
             const uint64_t b0 = b_desc(smem_u32(smem));
-            for (int i = first; i < items && ok; i += step, ++tile) {
+            for (int i = first; i < items && ok; i += step) {
                 const Item w = item_of(a, i);
-                if (tile > 0 && !(ok = warp_wait(&bar.dempty, (tile - 1) & 1))) break;
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const int s = it % kStages;
-                    const uint32_t ph = (it / kStages) & 1;
-                    if (!(ok = warp_wait(&bar.bfull[s], ph) && warp_wait(&bar.afull[s], ph))) break;
-                    tc_after();
-                    if (elect_one()) {
-                        const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
-                        const uint32_t ta = tmem + kTmemA + s * kTmemAStage;
+                for (int kb = w.kb0; kb < w.kb1 && ok; ++tile) {
+                    if (tile > 0 && !(ok = warp_wait(&bar.dempty, (tile - 1) & 1))) break;
+                    const int start = kb, end = min(kb + a.run, w.kb1);
+                    for (; kb < end; ++kb, ++it) {
+                        const int s = it % kStages;
+                        const uint32_t ph = (it / kStages) & 1;
+                        if (!(ok = warp_wait(&bar.bfull[s], ph) && warp_wait(&bar.afull[s], ph))) break;
+                        tc_after();
+                        if (elect_one()) {
+                            const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
+                            const uint32_t ta = tmem + kTmemA + s * kTmemAStage;
 #pragma unroll
-                        for (int j = 0; j < kDeep / 16; ++j)
-                            tc_mma(tmem, ta + 8 * j, b + j * (2048 >> 4), kIdesc, kb > w.kb0 || j > 0);
-                        tc_commit(&bar.empty[s]);
-                        if (kb + 1 == w.kb1) tc_commit(&bar.dfull);
+                            for (int j = 0; j < kDeep / 16; ++j)
+                                tc_mma(tmem, ta + 8 * j, b + j * (2048 >> 4), kIdesc, kb > start || j > 0);
+                            tc_commit(&bar.empty[s]);
+                            if (kb + 1 == end) tc_commit(&bar.dfull);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             // the MMAs must have finished with both CTAs' memory before the exit
@@ -578,15 +578,30 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
         uint32_t tile = 0;
-        for (int i = first; i < items; i += step, ++tile) {
+        bool ok = true;
+        for (int i = first; i < items && ok; i += step) {
             const Item w = item_of(a, i);
-            if (!warp_wait(&bar.dfull, tile & 1)) break;
-            tc_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * (kTileN / 2);
             const int64_t k0 = w.k0 + (int64_t)rank * kQBlock + 32 * q, n0 = w.n0 + half * (kTileN / 2);
-            if (w.part < 0 && !a.out_f32) store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
-            else if (w.part < 0) store_f32(a, acc, k0, n0, &bar.dempty);
-            else store_part(a.part + (int64_t)w.part * kTileN * kTileK, acc, (int)(k0 - w.k0), (int)(n0 - w.n0), &bar.dempty);
+            for (int kb = w.kb0; kb < w.kb1; kb += a.run, ++tile) {
+                if (!(ok = warp_wait(&bar.dfull, tile & 1))) break;
+                tc_after();
+                const bool add = kb > w.kb0;
+                if (w.part >= 0 || a.out_f32) {
+                    const bool part = w.part >= 0;
+                    const int64_t own = k0 + own_column(lane), k = k0 + (lane & 16) + 2 * (lane & 7);
+                    const int64_t ld = part ? kTileK : a.ld_dw;
+                    float *o = part ? a.part + (int64_t)w.part * kTileN * kTileK + (n0 - w.n0) * kTileK + (k - w.k0)
+                                    : static_cast<float *>(a.dw) + n0 * a.ld_dw + k;
+                    const int rows = part ? kTileN / 2 : (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
+                    const int cols = part ? 2 : (int)max((int64_t)0, min((int64_t)2, a.K - k));
+                    const float scale = !part && a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
+                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
+                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
+                } else {
+                    store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
+                }
+            }
         }
     }
     __syncwarp();
@@ -709,12 +724,14 @@ struct Plan {
 void split_rest(Plan *p)
 {
     const int tiles = p->tiles_k * p->tiles_n;
-    p->whole = tiles / p->clusters * p->clusters;
+    // (a bf16 tile done whole is stored once, so its rows fit one run)
+    const bool all = p->kblocks > kRunBf16;
+    p->whole = all ? 0 : tiles / p->clusters * p->clusters;
     const int rest = tiles - p->whole;
     p->splits = 1;
     p->per_split = p->kblocks;
     if (rest == 0 || p->kblocks == 0) return;
-    double best = p->kblocks + 8;
+    double best = all ? 1e30 : p->kblocks + 8;
     for (int s = 2; s <= 16 && s * 4 <= p->kblocks; ++s) {
         const int per = (p->kblocks + s - 1) / s, parts = (p->kblocks + per - 1) / per;
         const int rounds = (rest * parts + p->clusters - 1) / p->clusters;
@@ -806,6 +823,7 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     a.T = T; a.N = n; a.K = K;
     a.tiles_k = p.tiles_k; a.tiles_n = p.tiles_n; a.kblocks = p.kblocks;
     a.whole = p.whole; a.splits = p.splits; a.per_split = p.per_split;
+    a.run = out_dtype == ZERO1_DTYPE_F32 ? kRunF32 : kRunBf16;
     a.scale = col_scale;
     a.scale_f32 = scale_dtype == ZERO1_DTYPE_F32;
     a.dw = dw; a.ld_dw = n > 1 ? ld_dw : K;
