@@ -34,6 +34,7 @@ _CFG = struct.Struct("=qqff8i")
 _FWD = struct.Struct("=11Q5q")
 _BWD = struct.Struct("=16Q8q")
 
+_Tensor = torch.Tensor
 _ready = None
 
 
@@ -52,7 +53,7 @@ def _lib():
     return _ready
 
 
-_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -77,7 +78,11 @@ def _usable(t: torch.Tensor, what: str) -> None:
 
 def _matrix(t: torch.Tensor, shape: tuple, dtype, what: str) -> tuple[int, int]:
     """(pointer, row stride) of a tensor of this shape with contiguous columns."""
-    _usable(t, what)
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == _get_device():
+        ld, step = t.stride()
+        if step == 1:
+            return t.data_ptr(), ld
+    _usable(t, what)  # the long way, for what is unusual or wrong
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -89,6 +94,9 @@ def _matrix(t: torch.Tensor, shape: tuple, dtype, what: str) -> tuple[int, int]:
 
 
 def _vector(t: torch.Tensor, numel: int, dtype, what: str) -> int:
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == (numel,) and t.stride() == (1,)
+            and t.get_device() == _get_device()):
+        return t.data_ptr()
     _usable(t, what)
     if t.dtype is not dtype:
         raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
@@ -256,15 +264,16 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _workspace(workspace, nbytes: int, device, stream) -> tuple[int | None, int, torch.Tensor | None]:
+def _workspace(workspace, nbytes: int, device, stream):
+    """(pointer, bytes, tensor) of the caller's workspace or a new one; the
+    tensor is kept until the call has been made."""
     if workspace is None:
-        workspace = _scratch(nbytes, device, stream) if nbytes else None
-    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        if not nbytes:
+            return None, 0, None
+        workspace = _scratch(nbytes, device, stream)
+        return workspace.data_ptr(), nbytes, workspace
+    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA uint8 tensor")
-    elif workspace.numel() < nbytes:
-        raise ValueError(f"workspace: has {workspace.numel()} bytes, needs {nbytes}")
-    if workspace is None:
-        return None, 0, None
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
