@@ -87,6 +87,12 @@ __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const F
 
 // ------------------------------------------------------- staged forward ----
 //
+// Measured on GB300 with both checkpoints, bf16: 8192 x 4096 58 us (5.75 TB/s of
+// the 10 bytes per element, 0.85 of the measured copy rate; the direct kernel
+// took 75), 32768 x 768 with an fp32 residual stream 54 us (0.83).  What is
+// lost is the first rows' latency and, with 16 warps per SM, the waits for
+// shuffles and shared memory (0.43 instructions per cycle and scheduler).
+//
 // KEPT: 1 both norms are there and both checkpoints wanted, 2 both norms and
 // no checkpoint, 0 any other mix, decided at run time.  FULL: the row has
 // exactly 8 C T columns.
@@ -196,6 +202,7 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
     }
 }
 
+// Every resident block, one row at a time.
 template <class TA, class TR, bool VEC>
 int launch_fwd(const Common &c, const Fwd &a, int sms, cudaStream_t st)
 {
