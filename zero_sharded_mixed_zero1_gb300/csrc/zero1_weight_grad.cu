@@ -57,7 +57,7 @@ constexpr int kWgThreads = 32 * (4 + 4 * kSets + 8);
 constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
 
 struct WgBars {
-    uint64_t bfull[kStages], afull[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
+    uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
 };
 constexpr int kStash = 32;  // packed pairs of results that a storing thread keeps in shared memory
@@ -419,8 +419,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     const uint32_t rank = cta_rank();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bar.bfull[s], 1);
-            mbar_init(&bar.afull[s], 8);   // four converting warps of each CTA
+            mbar_init(&bar.full[s], 9);    // the loads of B, four converting warps of each CTA
             mbar_init(&bar.empty[s], 1);
         }
         for (int s = 0; s < kCodeStages; ++s) {
@@ -455,8 +454,8 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                 unsigned char *b = smem + s * kBBytes;
                 if (elect_one()) {
                     // both CTAs' halves count on the leading CTA's barrier
-                    const uint32_t full = leader_addr(&bar.bfull[s]);
-                    if (rank == 0) mbar_expect_tx(&bar.bfull[s], 2 * kBBytes);
+                    const uint32_t full = leader_addr(&bar.full[s]);
+                    if (rank == 0) mbar_expect_tx(&bar.full[s], 2 * kBBytes);
                     tma_2d_pair(b, &map_dy, n, kb * kDeep, full);
                     tma_2d_pair(b + kBBytes / 2, &map_dy, n + 64, kb * kDeep, full);
                 }
@@ -466,7 +465,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
         // the last copies must land before the pair may exit
         if (rank == 0)
             for (uint32_t q = it > kStages ? it - kStages : 0; q < it; ++q)
-                warp_wait(&bar.bfull[q % kStages], (q / kStages) & 1);
+                warp_wait(&bar.full[q % kStages], (q / kStages) & 1);
     } else if (warp == 3) {
         uint32_t it = 0;
         bool ok = true;
@@ -500,15 +499,15 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                     const int start = kb, end = min(kb + a.run, w.kb1);
                     for (; kb < end; ++kb, ++it) {
                         const int s = it % kStages;
-                        const uint32_t ph = (it / kStages) & 1;
-                        if (!(ok = warp_wait(&bar.bfull[s], ph) && warp_wait(&bar.afull[s], ph))) break;
+                        // what the instructions take is ready before the branch, in uniform registers
+                        const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
+                        const uint32_t ta = tmem + kTmemA + s * kTmemAStage, more = kb > start;
+                        if (!(ok = warp_wait(&bar.full[s], (it / kStages) & 1))) break;
                         tc_after();
                         if (elect_one()) {
-                            const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
-                            const uint32_t ta = tmem + kTmemA + s * kTmemAStage;
 #pragma unroll
                             for (int j = 0; j < kDeep / 16; ++j)
-                                tc_mma(tmem, ta + 8 * j, b + j * (2048 >> 4), kIdesc, kb > start || j > 0);
+                                tc_mma(tmem, ta + 8 * j, b + j * (2048 >> 4), kIdesc, j ? 1u : more);
                             tc_commit(&bar.empty[s]);
                             if (kb + 1 == end) tc_commit(&bar.dfull);
                         }
@@ -579,7 +578,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bar.cempty[c]);
-                    arrive_leader(&bar.afull[s]);
+                    arrive_leader(&bar.full[s]);
                 }
             }
             it0 += n;
