@@ -50,7 +50,7 @@ constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
 constexpr int kDeep = 64;                  // rows of the contraction per stage
 constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time
 constexpr int kStages = 8;                 // of B in shared and A in tensor memory
-constexpr int kCodeStages = 8;             // of codes and scales in shared memory
+constexpr int kCodeStages = 6;             // of codes and scales in shared memory
 constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;  // of a CTA, per stage
 constexpr int kSets = 4;                   // of four converting warps
 constexpr int kWgThreads = 32 * (4 + 4 * kSets + 8);
@@ -60,7 +60,7 @@ struct WgBars {
     uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
 };
-constexpr int kStash = 32;  // packed pairs of results that a storing thread keeps in shared memory
+constexpr int kStash = 48;  // fp32 results, or packed pairs of bf16 ones, that a storing thread keeps in shared memory
 constexpr int kStashBytes = 8 * 32 * kStash * 4;
 constexpr int kWgSmem = 1024 + kStages * kBBytes + kCodeStages * (kXBytes + kDeep) + kStashBytes + (int)sizeof(WgBars);
 static_assert(kWgSmem <= 227 * 1024, "shared memory of a block");
@@ -371,38 +371,66 @@ __device__ __forceinline__ void add_to(float *p, float2 x)
 {
     asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x.x), "f"(x.y) : "memory");
 }
-// fp32 results, 32 lanes x 128 rows, two columns of a row per lane as above
+// 16 accumulator columns of fp32 results, two columns of a row per lane as above
 // (one column per lane, in the lanes' order, took twice the instructions and
-// more time).  rows: how many of the 128 are stored; cols: of this lane's two.
+// more time).  o: this lane's first row; rows: how many are stored from there;
+// cols: of this lane's two.
 template <bool ADD>
-__device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int cols, bool pairs, float scale, uint32_t acc,
-                                          uint64_t *dempty)
+__device__ __forceinline__ void store_f32_part(float *o, int64_t ld, int rows, int cols, bool easy, float scale, const uint32_t *v)
 {
     const bool up = threadIdx.x & 8;
-    const bool easy = pairs && cols == 2 && rows == kTileN / 2;
-    o += up ? ld : 0;
-#pragma unroll 1
-    for (int c = 0; c < kTileN / 2; c += 32) {
-        uint32_t v[32];
-        tc_load32(acc + c, v);
-        if (c + 32 == kTileN / 2) release_acc(dempty);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2, o += 2 * ld) {
-            const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-            const float2 x = up ? make_float2(got, v1) : make_float2(v0, got);
-            if (easy) {
-                if (ADD) add_to(o, x);
-                else *reinterpret_cast<float2 *>(o) = x;
-            } else if (c + j + up < rows) {
+    for (int j = 0; j < 16; j += 2, o += 2 * ld) {
+        const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
+        const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
+        const float2 x = up ? make_float2(got, v1) : make_float2(v0, got);
+        if (easy) {
+            if (ADD) add_to(o, x);
+            else *reinterpret_cast<float2 *>(o) = x;
+        } else if (j + up < rows) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (e >= cols) continue;
-                    if (ADD) add_to(o + e, e ? x.y : x.x);
-                    else o[e] = e ? x.y : x.x;
-                }
+            for (int e = 0; e < 2; ++e) {
+                if (e >= cols) continue;
+                if (ADD) add_to(o + e, e ? x.y : x.x);
+                else o[e] = e ? x.y : x.x;
             }
         }
+    }
+}
+
+// All 128 columns.  The first kStash wait in shared memory and the last 32 in
+// registers, so that the next MMAs wait for the stores of the others only.
+template <bool ADD>
+__device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int cols, bool pairs, float scale, uint32_t acc,
+                                          uint32_t *stash, uint64_t *dempty)
+{
+    constexpr int kLast = kTileN / 2 - 32;
+    const bool easy = pairs && cols == 2 && rows == kTileN / 2;
+    o += threadIdx.x & 8 ? ld : 0;
+#pragma unroll 1
+    for (int c = 0; c < kStash; c += 16) {
+        uint32_t v[16];
+        tc_load16(acc + c, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) stash[32 * (c + j)] = v[j];
+    }
+#pragma unroll 1
+    for (int c = kStash; c < kLast; c += 16) {
+        uint32_t v[16];
+        tc_load16(acc + c, v);
+        store_f32_part<ADD>(o + c * ld, ld, rows - c, cols, easy, scale, v);
+    }
+    uint32_t w[32];
+    tc_load32(acc + kLast, w);
+    release_acc(dempty);
+    store_f32_part<ADD>(o + kLast * ld, ld, rows - kLast, cols, easy, scale, w);
+    store_f32_part<ADD>(o + (kLast + 16) * ld, ld, rows - kLast - 16, cols, easy, scale, w + 16);
+#pragma unroll 1
+    for (int c = 0; c < kStash; c += 16) {
+        uint32_t v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = stash[32 * (c + j)];
+        store_f32_part<ADD>(o + c * ld, ld, rows - c, cols, easy, scale, v);
     }
 }
 
@@ -585,6 +613,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
         }
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
+        uint32_t *const stash = s_stash + (4 * half + q) * 32 * kStash + lane;
         uint32_t tile = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
@@ -604,10 +633,10 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                     const int rows = part ? kTileN / 2 : (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
                     const int cols = part ? 2 : (int)max((int64_t)0, min((int64_t)2, a.K - k));
                     const float scale = !part && a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
-                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
-                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
+                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, stash, &bar.dempty);
+                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, stash, &bar.dempty);
                 } else {
-                    store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
+                    store_bf16(a, acc, k0, n0, stash, &bar.dempty);
                 }
             }
         }
