@@ -143,7 +143,6 @@ __device__ __forceinline__ uint32_t max16(uint32_t a)
     for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
     return a;
 }
-__device__ __forceinline__ uint32_t max32(uint32_t a) { return __reduce_max_sync(0xffffffffu, a); }
 
 // ------------------------------------------------------------ fp32 pairs ---
 //

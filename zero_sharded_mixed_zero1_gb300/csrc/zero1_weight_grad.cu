@@ -25,19 +25,22 @@ namespace {
 // of the contraction where a CTA alone would load 40.  Products are exact in
 // fp32; sums are fp32 in the accumulator.
 //
-// Measured on GB300: 14336 x 4096 outputs over 8192 rows 550 us in a burst (1750
-// TFLOP/s, 0.89 of the measured cuBLAS rate for a plain bf16 product), 4096 x
-// 4096 168 us (1635).  The converting warps need about 260 of a stage's 512
-// cycles on the integer pipe; what is left is the start and end of each tile
-// and, over seconds, the power limit.  A first version with one CTA's worth of
-// synchronisation (loads of codes and dy in one ring, releases at cluster
-// scope, the timer read in every wait) took 1.5 ms on the larger size.
+// Measured on GB300: 14336 x 4096 outputs over 8192 rows 498 us in a burst (1930
+// TFLOP/s, 0.98 of the measured cuBLAS rate for a plain bf16 product), 4096 x
+// 4096 152 us (1815).  A stage takes about 575 cycles where its MMAs need 512,
+// the converting warps 260 on the integer pipe; what is left is the start and
+// end of each tile and, over seconds, the power limit.  Steps on the way: one
+// ring for codes and dy, releases at cluster scope and the timer read in every
+// wait 1.5 ms on the larger size; two barriers per stage for the issuing warp
+// instead of one 550 us; stores to memory before the accumulator is let go
+// 509 us.
 //
 // The tensor cores truncate where fp32 would round, an error that grows with
 // the number of additions: 2e-7 of a gradient's norm over 777 rows, 1.5e-6 over
 // 4096, 9e-6 over 16384.  For bf16 results that is nothing; for fp32 ones the
 // accumulator is emptied every 2048 rows and the runs are added in fp32 (6e-7
-// over 16384 rows; 4096 x 4096 over 8192 rows 211 us against 168).
+// over 16384 rows; 4096 x 4096 over 8192 rows 191 us against 163 in one run:
+// the MMAs stop for some 4500 cycles each time).
 //
 // Roles (28 warps): warp 0 loads dy and warp 3 the codes, warp 1 of the
 // leading CTA issues the MMAs, warps 4-19 convert (four sets of four take
@@ -755,7 +758,7 @@ struct Plan {
 // The pairs of CTAs take the tiles in rounds; what a last, partial round would
 // leave idle is used by splitting its tiles along the rows.  Of the splits
 // into 1 to 16 parts the one with the least estimated time is taken, in
-// stages of the contraction (0.35 us): the rounds, about 8 stages for each
+// stages of the contraction (0.28 us): the rounds, about 8 stages for each
 // item's start and end, and for a split the writing and joining of its parts
 // (0.5 MB each, about 0.3 stages) and one more launch (10 stages).
 void split_rest(Plan *p)
