@@ -25,22 +25,21 @@ namespace {
 // of the contraction where a CTA alone would load 40.  Products are exact in
 // fp32; sums are fp32 in the accumulator.
 //
-// Measured on GB300: 14336 x 4096 outputs over 8192 rows 498 us in a burst (1930
-// TFLOP/s, 0.98 of the measured cuBLAS rate for a plain bf16 product), 4096 x
-// 4096 152 us (1815).  A stage takes about 575 cycles where its MMAs need 512,
+// Measured on GB300: 14336 x 4096 outputs over 8192 rows 509 us in a burst (1890
+// TFLOP/s, 0.96 of the measured cuBLAS rate for a plain bf16 product), 4096 x
+// 4096 154 us (1790).  A stage takes about 575 cycles where its MMAs need 512,
 // the converting warps 260 on the integer pipe; what is left is the start and
 // end of each tile and, over seconds, the power limit.  Steps on the way: one
 // ring for codes and dy, releases at cluster scope and the timer read in every
 // wait 1.5 ms on the larger size; two barriers per stage for the issuing warp
-// instead of one 550 us; stores to memory before the accumulator is let go
-// 509 us.
+// instead of one 550 us.
 //
 // The tensor cores truncate where fp32 would round, an error that grows with
 // the number of additions: 2e-7 of a gradient's norm over 777 rows, 1.5e-6 over
 // 4096, 9e-6 over 16384.  For bf16 results that is nothing; for fp32 ones the
 // accumulator is emptied every 2048 rows and the runs are added in fp32 (6e-7
-// over 16384 rows; 4096 x 4096 over 8192 rows 191 us against 163 in one run:
-// the MMAs stop for some 4500 cycles each time).
+// over 16384 rows; 4096 x 4096 over 8192 rows 192 us against 163 in one run:
+// the MMAs stop for some 5000 cycles each time).
 //
 // Roles (28 warps): warp 0 loads dy and warp 3 the codes, warp 1 of the
 // leading CTA issues the MMAs, warps 4-19 convert (four sets of four take
@@ -53,9 +52,13 @@ constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
 constexpr int kDeep = 64;                  // rows of the contraction per stage
 constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time
 constexpr int kStages = 8;                 // of B in shared and A in tensor memory
-constexpr int kCodeStages = 6;             // of codes and scales in shared memory
+constexpr int kCodeStages = 8;             // of codes and scales in shared memory
 constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;  // of a CTA, per stage
 constexpr int kSets = 4;                   // of four converting warps
+// A set must meet every use of the places it takes: one that came to a place for
+// the first time in its second use would take the parity of the phase before
+// the first for the one it waits for.
+static_assert(kStages % kSets == 0 && kCodeStages % kSets == 0, "a place belongs to one set");
 constexpr int kWgThreads = 32 * (4 + 4 * kSets + 8);
 constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
 
@@ -63,7 +66,7 @@ struct WgBars {
     uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
 };
-constexpr int kStash = 48;  // fp32 results, or packed pairs of bf16 ones, that a storing thread keeps in shared memory
+constexpr int kStash = 32;  // packed pairs of results that a storing thread keeps in shared memory
 constexpr int kStashBytes = 8 * 32 * kStash * 4;
 constexpr int kWgSmem = 1024 + kStages * kBBytes + kCodeStages * (kXBytes + kDeep) + kStashBytes + (int)sizeof(WgBars);
 static_assert(kWgSmem <= 227 * 1024, "shared memory of a block");
@@ -374,66 +377,38 @@ __device__ __forceinline__ void add_to(float *p, float2 x)
 {
     asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x.x), "f"(x.y) : "memory");
 }
-// 16 accumulator columns of fp32 results, two columns of a row per lane as above
+// fp32 results, 32 lanes x 128 rows, two columns of a row per lane as above
 // (one column per lane, in the lanes' order, took twice the instructions and
-// more time).  o: this lane's first row; rows: how many are stored from there;
-// cols: of this lane's two.
-template <bool ADD>
-__device__ __forceinline__ void store_f32_part(float *o, int64_t ld, int rows, int cols, bool easy, float scale, const uint32_t *v)
-{
-    const bool up = threadIdx.x & 8;
-#pragma unroll
-    for (int j = 0; j < 16; j += 2, o += 2 * ld) {
-        const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
-        const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
-        const float2 x = up ? make_float2(got, v1) : make_float2(v0, got);
-        if (easy) {
-            if (ADD) add_to(o, x);
-            else *reinterpret_cast<float2 *>(o) = x;
-        } else if (j + up < rows) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (e >= cols) continue;
-                if (ADD) add_to(o + e, e ? x.y : x.x);
-                else o[e] = e ? x.y : x.x;
-            }
-        }
-    }
-}
-
-// All 128 columns.  The first kStash wait in shared memory and the last 32 in
-// registers, so that the next MMAs wait for the stores of the others only.
+// more time).  rows: how many of the 128 are stored; cols: of this lane's two.
 template <bool ADD>
 __device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int cols, bool pairs, float scale, uint32_t acc,
-                                          uint32_t *stash, uint64_t *dempty)
+                                          uint64_t *dempty)
 {
-    constexpr int kLast = kTileN / 2 - 32;
+    const bool up = threadIdx.x & 8;
     const bool easy = pairs && cols == 2 && rows == kTileN / 2;
-    o += threadIdx.x & 8 ? ld : 0;
+    o += up ? ld : 0;
 #pragma unroll 1
-    for (int c = 0; c < kStash; c += 16) {
-        uint32_t v[16];
-        tc_load16(acc + c, v);
+    for (int c = 0; c < kTileN / 2; c += 32) {
+        uint32_t v[32];
+        tc_load32(acc + c, v);
+        if (c + 32 == kTileN / 2) release_acc(dempty);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) stash[32 * (c + j)] = v[j];
-    }
-#pragma unroll 1
-    for (int c = kStash; c < kLast; c += 16) {
-        uint32_t v[16];
-        tc_load16(acc + c, v);
-        store_f32_part<ADD>(o + c * ld, ld, rows - c, cols, easy, scale, v);
-    }
-    uint32_t w[32];
-    tc_load32(acc + kLast, w);
-    release_acc(dempty);
-    store_f32_part<ADD>(o + kLast * ld, ld, rows - kLast, cols, easy, scale, w);
-    store_f32_part<ADD>(o + (kLast + 16) * ld, ld, rows - kLast - 16, cols, easy, scale, w + 16);
-#pragma unroll 1
-    for (int c = 0; c < kStash; c += 16) {
-        uint32_t v[16];
+        for (int j = 0; j < 32; j += 2, o += 2 * ld) {
+            const float v0 = __uint_as_float(v[j]) * scale, v1 = __uint_as_float(v[j + 1]) * scale;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v0 : v1, 8);
+            const float2 x = up ? make_float2(got, v1) : make_float2(v0, got);
+            if (easy) {
+                if (ADD) add_to(o, x);
+                else *reinterpret_cast<float2 *>(o) = x;
+            } else if (c + j + up < rows) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = stash[32 * (c + j)];
-        store_f32_part<ADD>(o + c * ld, ld, rows - c, cols, easy, scale, v);
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= cols) continue;
+                    if (ADD) add_to(o + e, e ? x.y : x.x);
+                    else o[e] = e ? x.y : x.x;
+                }
+            }
+        }
     }
 }
 
@@ -616,7 +591,6 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
         }
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
-        uint32_t *const stash = s_stash + (4 * half + q) * 32 * kStash + lane;
         uint32_t tile = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
@@ -636,10 +610,10 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                     const int rows = part ? kTileN / 2 : (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
                     const int cols = part ? 2 : (int)max((int64_t)0, min((int64_t)2, a.K - k));
                     const float scale = !part && a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
-                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, stash, &bar.dempty);
-                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, stash, &bar.dempty);
+                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
+                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
                 } else {
-                    store_bf16(a, acc, k0, n0, stash, &bar.dempty);
+                    store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
                 }
             }
         }
