@@ -66,7 +66,8 @@ struct WgBars {
     uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
 };
-constexpr int kStash = 32;  // packed pairs of results that a storing thread keeps in shared memory
+constexpr int kStash = 32;  // packed pairs of bf16 results, or fp32 ones, that a storing thread keeps in shared memory
+constexpr int kBoxRows = 16, kPlaces = kStash / kBoxRows;  // of the boxes that a part's sums leave in
 constexpr int kStashBytes = 8 * 32 * kStash * 4;
 constexpr int kWgSmem = 1024 + kStages * kBBytes + kCodeStages * (kXBytes + kDeep) + kStashBytes + (int)sizeof(WgBars);
 static_assert(kWgSmem <= 227 * 1024, "shared memory of a block");
@@ -412,8 +413,58 @@ __device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int co
     }
 }
 
+// A box from shared memory, added to what is there or written, and a group of its own.
+__device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bool add, const uint32_t *place)
+{
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                     "r"(x), "r"(y), "r"(smem_u32(place))
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                     "r"(y), "r"(smem_u32(place))
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Sums of a split tile's part, 32 lanes x 128 rows, as boxes of 32 columns x
+// kBoxRows rows that are copied or added from the warp's two places in shared
+// memory: no trade between lanes and a quarter of the instructions.  (Whole
+// tiles are stored from registers as above, which lets go of the accumulator
+// sooner.)  Only this warp writes here, and a run's boxes are added after those
+// of the run before.
+__device__ __forceinline__ void store_part(const CUtensorMap *map, int x, int y, bool add, uint32_t acc, uint32_t *places,
+                                           uint64_t *dempty)
+{
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+#pragma unroll 1
+    for (int c = 0; c < kTileN / 2; c += 2 * kBoxRows) {
+        uint32_t v[2 * kBoxRows];
+        tc_load32(acc + c, v);
+        if (c + 2 * kBoxRows == kTileN / 2) release_acc(dempty);
+#pragma unroll
+        for (int h = 0; h < 2 * kBoxRows; h += kBoxRows) {
+            if (elect_one()) {  // the run before is written, or the place's last box has been read
+                if (c + h == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                else asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPlaces - 1) : "memory");
+            }
+            __syncwarp();
+            uint32_t *place = places + at * 32 * kBoxRows;
+#pragma unroll
+            for (int j = 0; j < kBoxRows; ++j) place[32 * j + own_column(lane)] = v[h + j];
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (elect_one()) box_out(map, x, y + c + h, add, place);
+            __syncwarp();
+            at = at + 1 == kPlaces ? 0 : at + 1;
+        }
+    }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
-k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x, const Wg a)
+k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
+              const __grid_constant__ CUtensorMap map_part, const Wg a)
 {
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -591,6 +642,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
         }
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
+        uint32_t *const places = s_stash + (4 * half + q) * 32 * kStash, *const stash = places + lane;
         uint32_t tile = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
@@ -601,22 +653,24 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                 if (!(ok = warp_wait(&bar.dfull, tile & 1))) break;
                 tc_after();
                 const bool add = kb > w.kb0;
-                if (w.part >= 0 || a.out_f32) {
-                    const bool part = w.part >= 0;
+                if (w.part >= 0) {
+                    store_part(&map_part, (int)(k0 - w.k0), w.part * kTileN + half * (kTileN / 2), add, acc, places, &bar.dempty);
+                } else if (a.out_f32) {
                     const int64_t own = k0 + own_column(lane), k = k0 + (lane & 16) + 2 * (lane & 7);
-                    const int64_t ld = part ? kTileK : a.ld_dw;
-                    float *o = part ? a.part + (int64_t)w.part * kTileN * kTileK + (n0 - w.n0) * kTileK + (k - w.k0)
-                                    : static_cast<float *>(a.dw) + n0 * a.ld_dw + k;
-                    const int rows = part ? kTileN / 2 : (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
-                    const int cols = part ? 2 : (int)max((int64_t)0, min((int64_t)2, a.K - k));
-                    const float scale = !part && a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
-                    if (add || (!part && a.accumulate)) store_f32<true>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
-                    else store_f32<false>(o, ld, rows, cols, part || a.pairs, scale, acc, &bar.dempty);
+                    float *o = static_cast<float *>(a.dw) + n0 * a.ld_dw + k;
+                    const int rows = (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
+                    const int cols = (int)max((int64_t)0, min((int64_t)2, a.K - k));
+                    const float scale = a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
+                    if (add || a.accumulate) store_f32<true>(o, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
+                    else store_f32<false>(o, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
                 } else {
-                    store_bf16(a, acc, k0, n0, s_stash + (4 * half + q) * 32 * kStash + lane, &bar.dempty);
+                    store_bf16(a, acc, k0, n0, stash, &bar.dempty);
                 }
             }
         }
+        // the boxes on their way are written before the grid counts as done
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     __syncwarp();
     __syncthreads();
@@ -701,17 +755,17 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// A [rows, cols] matrix in boxes of box_x columns and kDeep rows, 128-byte swizzled.
+// A [rows, cols] matrix in boxes of box_x columns and box_y rows.
 int make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *p, int64_t rows, int64_t cols, int64_t ld,
-             int box_x, const char *what)
+             int box_x, const char *what, int box_y = kDeep, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
-    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)kDeep}, one[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, one[2] = {1, 1};
     const EncodeTiled fn = encode_tiled();
     if (!fn) return z1_fail(ZERO1_ECUDA, "weight gradient: the driver has no tensor maps");
     const CUresult r = fn(m, type, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return z1_fail(ZERO1_ECUDA, "weight gradient: tensor map of %s: error %d", what, (int)r);
     return ZERO1_OK;
@@ -858,17 +912,19 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
             src = copy;
             ld = p.ld_copy;
         }
-        CUtensorMap mdy, mx;
+        CUtensorMap mdy, mx, mpart{};
         if ((rc = make_map(&mdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, src, T, n, ld, 64, "dy")) ||
             (rc = make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
-                           "the codes")))
+                           "the codes")) ||
+            (p.splits > 1 && (rc = make_map(&mpart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, p.copy_at / (kTileK * 4), kTileK,
+                                            kTileK, 32, "the parts", kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE))))
             return rc;
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = allow_smem(k_weight_grad, kWgSmem, done);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
         const int64_t items = p.whole + (int64_t)(p.tiles_k * p.tiles_n - p.whole) * p.splits;
         const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
-        const cudaError_t le = launch_after(k_weight_grad, dim3(grid), kWgThreads, kWgSmem, st, mdy, mx, a);
+        const cudaError_t le = launch_after(k_weight_grad, dim3(grid), kWgThreads, kWgSmem, st, mdy, mx, mpart, a);
         if (le != cudaSuccess) return pdl_fail(le, "weight gradient launch");
         z1_note_launch(reinterpret_cast<const void *>(k_weight_grad), grid, 1, kWgThreads, 0);
         if (p.splits == 1) return ZERO1_OK;
