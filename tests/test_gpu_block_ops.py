@@ -529,6 +529,25 @@ def test_weight_grad_without_rows(cuda_device):
     assert (dw == 0.0).all()
 
 
+@pytest.mark.parametrize("T,N,K,out", [(777, 771, 1000, F32), (16384, 512, 512, F32), (2048, 2000, 2000, BF16)])
+def test_weight_grad_repeats_bit_for_bit(cuda_device, T, N, K, out):
+    """Many calls in a row, with and without split tiles: no stage of a ring is
+    used before it has arrived, and no wait runs out."""
+    g = torch.Generator(device=cuda_device).manual_seed(T)
+    x = torch.randn((T, K), device=cuda_device, generator=g)
+    dy = torch.randn((T, N), device=cuda_device, generator=g).to(BF16)
+    k = z.new_checkpoint(T, K, cuda_device)
+    z.zero1_checkpoint_pack(x, k)
+    first, dw = (torch.empty((N, K), dtype=out, device=cuda_device) for _ in range(2))
+    z.zero1_weight_grad(dy, k, first)
+    for _ in range(20):
+        dw.zero_()
+        for _ in range(50):
+            z.zero1_weight_grad(dy, k, dw)
+        assert torch.equal(dw, first)
+    assert z.zero1_device_status() == 0
+
+
 def test_weight_grad_is_reproducible(cuda_device):
     x, dy, _ = weight_grad_problem(3000, 130, 260, 9)
     k = z.new_checkpoint(3000, 260, cuda_device)
