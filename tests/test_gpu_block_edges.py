@@ -1,0 +1,56 @@
+"""The block norms at the edges of their buffers: what lies behind a vector or
+between a matrix's rows reaches no result."""
+import pytest
+import torch
+
+import test_gpu_block_ops as ops
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def among_nans(t, cuda, pad=0, off=0):
+    """ops.dev with NaN in place of every element around t: 16 behind it, `off`
+    before it, `pad` after each row."""
+    if t is None:
+        return None
+    rows, D = (1, t.shape[0]) if t.dim() == 1 else t.shape
+    pad = 0 if t.dim() == 1 else pad
+    big = torch.full((off + rows * (D + pad) + 16,), float("nan"), dtype=t.dtype, device=cuda)
+    v = big[off:off + rows * (D + pad)].view(rows, D + pad)[:, :D]
+    v.copy_(t.view(rows, D))
+    return v[0] if t.dim() == 1 else v
+
+
+@pytest.fixture
+def surrounded(monkeypatch):
+    monkeypatch.setattr(ops, "dev", among_nans)
+
+
+@pytest.mark.parametrize("T,D", [(3, 1), (3, 7), (5, 250), (2, 513), (4, 1021), (3, 2003), (2, 4093), (2, 8190), (2, 9001)])
+@pytest.mark.parametrize("act,res", ops.TYPES)
+@pytest.mark.parametrize("gate", [None, "channel", "full"])
+@pytest.mark.parametrize("param", [BF16, F32])
+def test_nothing_behind_a_vector_is_read(cuda_device, surrounded, T, D, act, res, gate, param):
+    p = ops.Problem(T, D, act, res, True, True, gate, "sigmoid" if T % 2 else "linear", param=param, seed=20)
+    ops.check_forward(p, ops.run_forward(p, cuda_device))
+    for ckpt in (False, True):
+        ops.check_backward(p, *ops.run_backward(p, cuda_device, ckpt))
+
+
+@pytest.mark.parametrize("post,pre", [(True, False), (False, True)])
+def test_nothing_behind_a_vector_is_read_with_a_norm_left_out(cuda_device, surrounded, post, pre):
+    for D in (250, 1021, 2003):
+        p = ops.Problem(4, D, BF16, BF16, post, pre, "channel", "linear", seed=21)
+        ops.check_forward(p, ops.run_forward(p, cuda_device))
+        for ckpt in (False, True):
+            ops.check_backward(p, *ops.run_backward(p, cuda_device, ckpt))
+
+
+@pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 1), (5, 0), (0, 3)])
+@pytest.mark.parametrize("D", [1024, 1021])
+def test_nothing_between_rows_is_read(cuda_device, surrounded, pad, off, D):
+    for gate in ("channel", "token", "full"):
+        p = ops.Problem(9, D, BF16, F32, True, True, gate, "sigmoid", seed=22)
+        ops.check_forward(p, ops.run_forward(p, cuda_device, pad, off, woff=off))
+        ops.check_backward(p, *ops.run_backward(p, cuda_device, False, pad, off, goff=off))

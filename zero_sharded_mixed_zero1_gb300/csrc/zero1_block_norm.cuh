@@ -125,7 +125,8 @@ __device__ __forceinline__ void store_chunk(T *row, int col, int D, const float 
 }
 
 // Eight weights or gate values of run-time type (1 beyond the row's end, so
-// that nothing there turns into a NaN).
+// that nothing there turns into a NaN).  vec: in 128-bit loads, if all eight lie
+// below column D or all beyond.
 template <bool VEC>
 __device__ __forceinline__ void param8(const void *p, int f32, int vec, int64_t base, int col, int D, float f[8])
 {
@@ -255,16 +256,20 @@ constexpr int kSmemPerSm = 227 * 1024;  // of which each block also takes 1 KB, 
 
 // Keeps a [D] vector in shared memory as fp32 values, through the logistic
 // function if asked: the first four values of each eight, then the last four,
-// so that a warp's 16-byte reads touch every bank once.
+// so that a warp's 16-byte reads touch every bank once.  The eight values that
+// reach past column D are read one by one (D need be no multiple of 8): what
+// lies behind a vector is not the caller's, and an Inf or NaN kept from there
+// would reach the row's sums as 0 * NaN.
 template <int T, int C>
 __device__ __forceinline__ void keep_vector(unsigned char *kept, const void *src, int f32, int D, int act)
 {
     if (!src) return;
-    const bool vec = ((uintptr_t)src & 15) == 0;
+    const bool aligned = ((uintptr_t)src & 15) == 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
+        const int col = threadIdx.x * 8 + i * T * 8;
         float f[8];
-        param8<true>(src, f32, vec, 0, threadIdx.x * 8 + i * T * 8, D, f);
+        param8<true>(src, f32, aligned && col + 8 <= D, 0, col, D, f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] = act ? sigmoid(f[k]) : f[k];
         float4 *q = reinterpret_cast<float4 *>(kept) + i * T + threadIdx.x;
