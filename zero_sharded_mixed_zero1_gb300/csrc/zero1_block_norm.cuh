@@ -160,8 +160,10 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-// The sum over a row, the same in every thread.  Consecutive calls alternate
-// between two `red` buffers, so one barrier per call is enough.
+// The sum over a row, the same in every thread.  One barrier per call: between
+// two calls with the same `red` buffer every warp passes another call's
+// barrier, so the kernels alternate by sum and by row (a row may have one sum
+// only).
 __device__ __forceinline__ float row_sum(float x, float *red)
 {
     const int lane = threadIdx.x & 31;

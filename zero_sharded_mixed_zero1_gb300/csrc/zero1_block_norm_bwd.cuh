@@ -20,7 +20,7 @@ template <class TA, class TR, bool VEC, bool SACC>
 __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Common c, const Bwd a)
 {
     constexpr int C = 2, V = 8 * C;
-    __shared__ float red[2][32];
+    __shared__ float red[2][2][32];  // by the row's parity and sum
     extern __shared__ float sacc[];  // SACC: [3][V][threads]
     const int tid = threadIdx.x, nthr = blockDim.x;
     float acc[SACC ? 1 : 3][C][8];
@@ -39,7 +39,8 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
         else acc[s][i][k] += x;
     };
 
-    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x, flip ^= 1) {
         Chunk<TA, VEC> hq[C], yq[C];
         Chunk<TR, VEC> dq[C], rq[C];
         uint2 y8[C], r8[C];
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
                     s1 = fmaf(d[i][k], rh[i][k], s1);
                 }
             }
-            s1 = row_sum(s1, red[0]) * c.inv_d;
+            s1 = row_sum(s1, red[flip][0]) * c.inv_d;
         }
         float s2 = 0.f;
         float yh[C][8];
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
             }
         }
         const bool tok = a.need_gate && c.gate_kind == ZERO1_GATE_TOKEN;
-        if (post || tok) s2 = row_sum(s2, red[1]);
+        if (post || tok) s2 = row_sum(s2, red[flip][1]);
         if (tok && tid == 0) {
             const float dg = c.sigmoid ? s2 * gt * (1.f - gt) : s2;
             if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;

@@ -18,9 +18,10 @@ template <class TA, class TR, bool VEC>
 __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const Fwd a)
 {
     constexpr int C = 2;
-    __shared__ float red[2][32];
+    __shared__ float red[2][2][32];  // by the row's parity and sum
     const int tid = threadIdx.x, nthr = blockDim.x;
-    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
+    int flip = 0;
+    for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x, flip ^= 1) {
         Chunk<TA, VEC> yq[C];
         Chunk<TR, VEC> xq[C];
         const TA *y = static_cast<const TA *>(a.y) + row * a.ld_y;
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const F
         }
         float rs = 1.f;
         if (c.w_post) {
-            rs = rstd_of(row_sum(ss, red[0]), c);
+            rs = rstd_of(row_sum(ss, red[flip][0]), c);
             if (tid == 0) a.rstd_post[row] = rs;
         }
         ss = 0.f;
@@ -68,7 +69,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const F
             for (int k = 0; k < 8; ++k) ss = fmaf(f[i][k], f[i][k], ss);
         }
         if (!c.w_pre) continue;
-        rs = rstd_of(row_sum(ss, red[1]), c);
+        rs = rstd_of(row_sum(ss, red[flip][1]), c);
         if (tid == 0) a.rstd_pre[row] = rs;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
