@@ -255,8 +255,9 @@ def zero1_block_norm_forward(cfg: BlockNorm, y, x, r, h=None, rstd_post=None, rs
     _check_rc(_lib().zero1_block_norm_forward(c, io, _launch_stream(stream)))
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """Scratch memory of the stream that will use it."""
+def _scratch(nbytes: int, stream) -> torch.Tensor:
+    """Scratch memory on the current device, of the stream that will use it."""
+    device = torch.device("cuda", _get_device())
     if stream is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     st = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=device)
@@ -264,16 +265,22 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _workspace(workspace, nbytes: int, device, stream):
+def _workspace(workspace, nbytes: int, stream):
     """(pointer, bytes, tensor) of the caller's workspace or a new one; the
-    tensor is kept until the call has been made."""
+    tensor is kept until the call has been made, and its memory then goes back
+    to the stream that uses it.  Always device memory, wherever the call's
+    tensors are: host memory would be freed while the kernels still write it."""
     if workspace is None:
         if not nbytes:
             return None, 0, None
-        workspace = _scratch(nbytes, device, stream)
+        workspace = _scratch(nbytes, stream)
         return workspace.data_ptr(), nbytes, workspace
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a torch.Tensor")
     if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous CUDA uint8 tensor")
+    if workspace.get_device() != _get_device():
+        raise ValueError(f"workspace: on {workspace.device}, the current device is cuda:{_get_device()}")
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
@@ -334,7 +341,7 @@ def zero1_block_norm_backward(cfg: BlockNorm, dh, dr, y, r, rstd_post, rstd_pre,
         need = _i64()
         _check_rc(lib.zero1_block_norm_workspace(c, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, dy.device, stream)
+    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
     _check_rc(lib.zero1_block_norm_backward(c, io, ws, nbytes, _launch_stream(stream)))
 
 
@@ -370,6 +377,6 @@ def zero1_weight_grad(dy, x8: Checkpoint8, dw, *, col_scale=None, accumulate: bo
         need = _i64()
         _check_rc(lib.zero1_weight_grad_workspace(rows, n, cols, pdy, ld, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, dy.device, stream)
+    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
     _check_rc(lib.zero1_weight_grad(pdy, ld, n, k, pc, ccode, pw, lw, code, 1 if accumulate else 0, ws, nbytes,
                                     _launch_stream(stream)))

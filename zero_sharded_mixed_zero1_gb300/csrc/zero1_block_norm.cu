@@ -274,6 +274,7 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
             return z1_fail(ZERO1_EINVAL, "%s: workspace of %lld bytes, needs %lld", call,
                            (long long)(workspace ? workspace_bytes : 0), (long long)need);
         if ((uintptr_t)workspace & 15) return z1_fail(ZERO1_EALIGN, "%s: the workspace is not 16-byte aligned", call);
+        if (in_host_memory(workspace)) return z1_fail(ZERO1_EINVAL, "%s: the workspace must be device memory", call);
     }
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -885,6 +885,8 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     }
     if (T > 0 && (in_host_memory(dy) || in_host_memory(x8->codes) || in_host_memory(x8->exps)))
         return z1_fail(ZERO1_EINVAL, "%s: dy and x8 must be device memory", call);
+    if (in_host_memory(dw) || (col_scale && in_host_memory(col_scale)) || (p.bytes > 0 && in_host_memory(workspace)))
+        return z1_fail(ZERO1_EINVAL, "%s: dw, col_scale and the workspace must be device memory", call);
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Wg a{};
