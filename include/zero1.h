@@ -651,7 +651,7 @@ int zero1_block_norm_forward(const zero1_block_norm_t *cfg, const zero1_block_no
  * The saved activations come either as y (act_dtype) and r (res_dtype) or as
  * the checkpoints y8 and r8 of the forward call, each on its own.  Without the
  * norm after the block y (or y8, then a checkpoint of y itself) is needed for
- * dgate only.  dw_post, dw_pre and dgate may be views into a replica's flat
+ * dgate only, and not looked at without it.  dw_post, dw_pre and dgate may be views into a replica's flat
  * gradient buffer at any element offset; any of them may be NULL when it is
  * not wanted.  dx may be dr and dy may be dh (same pointer, type and stride).
  * workspace: device, 16-byte aligned, zero1_block_norm_workspace bytes

@@ -3,6 +3,8 @@ between a matrix's rows reaches no result."""
 import pytest
 import torch
 
+import zero_sharded_mixed_zero1_gb300 as z
+import block_reference as ref
 import test_gpu_block_ops as ops
 
 pytestmark = pytest.mark.gpu
@@ -54,3 +56,28 @@ def test_nothing_between_rows_is_read(cuda_device, surrounded, pad, off, D):
         p = ops.Problem(9, D, BF16, F32, True, True, gate, "sigmoid", seed=22)
         ops.check_forward(p, ops.run_forward(p, cuda_device, pad, off, woff=off))
         ops.check_backward(p, *ops.run_backward(p, cuda_device, False, pad, off, goff=off))
+
+
+@pytest.mark.parametrize("D", [640, 1021, 9000])
+@pytest.mark.parametrize("gate", [None, "channel", "token"])
+def test_a_saved_block_output_that_is_not_needed_is_not_read(cuda_device, D, gate):
+    """Without the norm after the block, y serves dgate only: a checkpoint that
+    is no use (codes at an odd address, scales that stand for NaN) changes
+    nothing, and neither does a tensor over the outputs."""
+    p = ops.Problem(40, D, BF16, BF16, False, True, gate, "sigmoid", seed=23)
+    T, dev = p.T, cuda_device
+    f = p.forward64()
+    r, rstd = f["r"].to(BF16).to(dev), f["rstd_pre"].float().to(dev)
+    w, g, dh, dr = p.w_pre.to(dev), None if gate is None else p.gate.to(dev), p.dh.to(dev), p.dr.to(dev)
+    wide = ref.up(D)
+    odd = torch.zeros(T * wide + 1, dtype=torch.uint8, device=dev)[1:].view(T, wide)
+    useless = z.Checkpoint8(T, D, odd, torch.full((wide // 128, 128), 255, dtype=torch.uint8, device=dev))
+    results = []
+    for y in (None, useless, "dy"):
+        dy, dx, dw = torch.empty_like(dh), torch.empty_like(dr), torch.empty(D, device=dev)
+        z.zero1_block_norm_backward(p.cfg, dh, dr, dy if isinstance(y, str) else y, r, None, rstd, dy, dx, w_pre=w, gate=g,
+                                    dw_pre=dw)
+        results.append((dy, dx, dw))
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+    assert all(torch.isfinite(t.float()).all() for t in results[0])

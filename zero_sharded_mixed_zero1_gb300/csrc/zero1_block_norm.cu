@@ -221,13 +221,17 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
     const int ea = esize(cfg->act_dtype), er = esize(cfg->res_dtype), ep = esize(cfg->param_dtype),
               eg = esize(cfg->gate_dtype), ew = esize(cfg->grad_dtype);
     const int edg = cfg->gate_kind == ZERO1_GATE_FULL ? eg : ew;
+    // What the call does not need is not looked at: neither checked nor read.
+    const bool need_y = post || io->dgate;
+    const void *y = need_y ? io->y : nullptr;
+    const zero1_checkpoint8_t *y8 = need_y && T > 0 ? io->y8 : nullptr, *r8 = T > 0 ? io->r8 : nullptr;
     const Mat in[] = {mat(io->dr, T, D, io->ld_dr, er, "dr"), mat(io->dh, T, D, io->ld_dh, ea, "dh"),
-                      mat(io->y, T, D, io->ld_y, ea, "y"), mat(io->r, T, D, io->ld_r, er, "r"),
+                      mat(y, T, D, io->ld_y, ea, "y"), mat(io->r, T, D, io->ld_r, er, "r"),
                       mat(io->w_post, 1, D, 0, ep, "w_post"), mat(io->w_pre, 1, D, 0, ep, "w_pre"),
                       gate_mat(cfg, io->gate, io->ld_gate, eg, "gate"),
                       mat(io->rstd_post, 1, T, 0, 4, "rstd_post"), mat(io->rstd_pre, 1, T, 0, 4, "rstd_pre"),
-                      codes_mat(io->y8, "the codes of y8"), exps_mat(io->y8, "the exps of y8"),
-                      codes_mat(io->r8, "the codes of r8"), exps_mat(io->r8, "the exps of r8")};
+                      codes_mat(y8, "the codes of y8"), exps_mat(y8, "the exps of y8"),
+                      codes_mat(r8, "the codes of r8"), exps_mat(r8, "the exps of r8")};
     Mat work{workspace, 1, workspace_bytes, workspace_bytes, "the workspace"};
     const Mat out[] = {mat(io->dx, T, D, io->ld_dx, er, "dx"), mat(io->dy, T, D, io->ld_dy, ea, "dy"),
                        mat(io->dw_post, 1, D, 0, ew, "dw_post"), mat(io->dw_pre, 1, D, 0, ew, "dw_pre"),
@@ -237,7 +241,6 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
     if (!pre && (io->dw_pre || io->rstd_pre || io->dh || io->r || io->r8))
         return z1_fail(ZERO1_EINVAL, "%s: dw_pre, rstd_pre, dh, r or r8 without w_pre", call);
     if (io->dgate && cfg->gate_kind == ZERO1_GATE_NONE) return z1_fail(ZERO1_EINVAL, "%s: dgate without a gate", call);
-    const bool need_y = post || io->dgate;
     if (T > 0) {
         if ((rc = check_mat(out[0], er, true, call)) || (rc = check_mat(out[1], ea, true, call)) ||
             (io->dr && (rc = check_mat(in[0], er, false, call))) || (io->gate && (rc = check_mat(in[6], eg, false, call))))
@@ -246,15 +249,15 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
             if ((rc = check_mat(in[1], ea, false, call)) || (rc = check_natural(io->w_pre, ep, "w_pre")) ||
                 (rc = check_mat(in[8], 4, false, call)))
                 return rc;
-            if ((io->r != nullptr) == (io->r8 != nullptr))
+            if ((io->r != nullptr) == (r8 != nullptr))
                 return z1_fail(ZERO1_EINVAL, "%s: exactly one of r and r8 is needed", call);
-            if (io->r8 ? (rc = check_saved(cfg, io->r8, call, "r8")) : (rc = check_mat(in[3], er, false, call))) return rc;
+            if (r8 ? (rc = check_saved(cfg, r8, call, "r8")) : (rc = check_mat(in[3], er, false, call))) return rc;
         }
         if (post && ((rc = check_natural(io->w_post, ep, "w_post")) || (rc = check_mat(in[7], 4, false, call)))) return rc;
         if (io->y && io->y8) return z1_fail(ZERO1_EINVAL, "%s: both y and y8", call);
         if (need_y) {
-            if (!io->y && !io->y8) return z1_fail(ZERO1_EINVAL, "%s: y or y8 is needed", call);
-            if (io->y8 ? (rc = check_saved(cfg, io->y8, call, "y8")) : (rc = check_mat(in[2], ea, false, call))) return rc;
+            if (!y && !y8) return z1_fail(ZERO1_EINVAL, "%s: y or y8 is needed", call);
+            if (y8 ? (rc = check_saved(cfg, y8, call, "y8")) : (rc = check_mat(in[2], ea, false, call))) return rc;
         }
         if (!pre && !io->dr) return z1_fail(ZERO1_EINVAL, "%s: neither dh nor dr", call);
     }
@@ -279,9 +282,9 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
 
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (T > 0) {
-        const Common c = common_of(cfg, io->w_post, io->w_pre, io->gate, io->ld_gate, io->y8, io->r8);
+        const Common c = common_of(cfg, io->w_post, io->w_pre, io->gate, io->ld_gate, y8, r8);
         Bwd a{};
-        a.dh = io->dh; a.dr = io->dr; a.y = need_y ? io->y : nullptr; a.r = io->r;
+        a.dh = io->dh; a.dr = io->dr; a.y = y; a.r = io->r;
         a.rstd_post = io->rstd_post; a.rstd_pre = io->rstd_pre;
         a.dy = io->dy; a.dx = io->dx; a.dgate = io->dgate;
         a.ld_dh = io->ld_dh; a.ld_dr = io->ld_dr; a.ld_y = io->ld_y; a.ld_r = io->ld_r;
