@@ -560,7 +560,7 @@ int zero1_checksum(const void *data, int64_t nbytes, uint64_t *out, zero1_stream
  *    and sums are fp32 (fused multiply-adds allowed here, unlike the optimizer
  *    step); each output is rounded once, when it is stored.
  *  - rows may be 0: forward calls do nothing, gradients that are sums over
- *    rows get +0 (or stay, when accumulated into).
+ *    rows get +0 (or stay, when accumulated into); no input is looked at.
  *  - Results do not depend on timing: no floating-point atomics, fixed
  *    summation orders.
  * ------------------------------------------------------------------------- */

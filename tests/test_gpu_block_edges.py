@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import zero_sharded_mixed_zero1_gb300 as z
+from zero_sharded_mixed_zero1_gb300 import block as zb
 import block_reference as ref
 import test_gpu_block_ops as ops
 
@@ -81,3 +82,28 @@ def test_a_saved_block_output_that_is_not_needed_is_not_read(cuda_device, D, gat
     for other in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(results[0], other))
     assert all(torch.isfinite(t.float()).all() for t in results[0])
+
+
+@pytest.mark.parametrize("value", [1.0, float("nan"), float("inf")])
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_sums_over_no_rows_do_not_look_at_the_gate(cuda_device, value, kind):
+    """Sums over no rows are +0, or stay, whatever a sigmoid gate holds, and at
+    an address that its type does not allow."""
+    D = 200
+    w = torch.ones(D, dtype=BF16, device=cuda_device)
+    gate = torch.full((D,), value, dtype=kind, device=cuda_device)
+    e, s = torch.empty((0, D), dtype=BF16, device=cuda_device), torch.empty(0, device=cuda_device)
+    cfg = z.BlockNorm(gate_act="sigmoid")
+    for accumulate, want in ((False, 0.0), (True, 3.0)):
+        dw = [torch.full((D,), 3.0, dtype=F32, device=cuda_device) for _ in range(3)]
+        z.zero1_block_norm_backward(cfg, e, e, e, e, s, s, e, e, w_post=w, w_pre=w, gate=gate, dw_post=dw[0], dw_pre=dw[1],
+                                    dgate=dw[2], accumulate=accumulate)
+        assert all((t == want).all() for t in dw)
+        if not accumulate:
+            assert all(not torch.signbit(t).any() for t in dw)
+    dgate = torch.full((D,), 3.0, dtype=F32, device=cuda_device)
+    c = zb._CFG.pack(0, D, 1e-6, 1.0, 0, 0, 0, 1, 1, 1, 1, 0)   # fp32 gate and gradients, per channel, sigmoid
+    odd = torch.full((D + 1,), value, dtype=F32, device=cuda_device)
+    io = zb._BWD.pack(*([0] * 6), odd.data_ptr() + 1, *([0] * 8), dgate.data_ptr(), *([0] * 8))
+    assert zb._lib().zero1_block_norm_backward(c, io, None, 0, zb._launch_stream(None)) == 0
+    assert (dgate == 0.0).all()

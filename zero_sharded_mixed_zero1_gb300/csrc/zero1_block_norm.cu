@@ -309,7 +309,8 @@ extern "C" int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const ze
     f.out[0] = io->dw_post;
     f.out[1] = io->dw_pre;
     f.out[2] = chan ? io->dgate : nullptr;
-    f.gate = chan && cfg->gate_act == ZERO1_GATE_SIGMOID ? io->gate : nullptr;
+    // (without rows the gate is not checked, nor does it matter: the sums are +0)
+    f.gate = T > 0 && chan && cfg->gate_act == ZERO1_GATE_SIGMOID ? io->gate : nullptr;
     f.gf32 = cfg->gate_dtype == ZERO1_DTYPE_F32;
     const cudaError_t e = launch_after(k_block_norm_finish, dim3((unsigned)((D + 31) / 32), 3), 256, 0, st, f);
     if (e != cudaSuccess) return pdl_fail(e, "block norm backward: column sums");
