@@ -368,9 +368,13 @@ struct Mat {
     const char *what;
 };
 
+// `n` elements in bytes, INT64_MAX or -1 where they do not fit (check_mat then
+// refuses the matrix: a stride that wrapped round would pass for a short one).
+int64_t in_bytes(int64_t n, int es) { return n < 0 ? -1 : n > INT64_MAX / es ? INT64_MAX : n * es; }
+
 Mat mat(const void *p, int64_t rows, int64_t cols, int64_t ld, int es, const char *what)
 {
-    return Mat{p, rows, cols * es, (rows > 1 ? ld : cols) * es, what};
+    return Mat{p, rows, in_bytes(cols, es), in_bytes(rows > 1 ? ld : cols, es), what};
 }
 
 // Whether two matrices share a byte.  Of equal pitch they may be interleaved
@@ -395,7 +399,8 @@ int check_mat(const Mat &m, int es, bool out, const char *call)
     if (m.rows == 0) return ZERO1_OK;
     if (!m.p) return z1_fail(ZERO1_EINVAL, "%s: %s is NULL", call, m.what);
     if (m.pitch < 0 || (out && m.pitch < m.width))
-        return z1_fail(ZERO1_EINVAL, "%s: %s: row stride of %lld elements", call, m.what, (long long)(m.pitch / es));
+        return z1_fail(ZERO1_EINVAL, m.pitch < 0 ? "%s: %s: negative row stride" : "%s: %s: row stride of %lld elements", call,
+                       m.what, (long long)(m.pitch / es));
     if (m.rows > 1 && m.pitch > INT64_MAX / m.rows)
         return z1_fail(ZERO1_ERANGE, "%s: %s: size overflows", call, m.what);
     return check_natural(m.p, es, m.what);
