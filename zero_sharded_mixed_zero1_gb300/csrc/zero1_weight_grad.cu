@@ -5,8 +5,11 @@
 
 #include "zero1_async.cuh"
 #include "zero1_block.cuh"
+#include "zero1_weight_grad_plan.h"
 
 namespace {
+
+using namespace z1wg;
 
 // dw[n, k] = c[k] * sum_t dy[t, n] * x8[t, k].
 //
@@ -48,9 +51,6 @@ namespace {
 // into registers and half into shared memory, so that the next tile's MMAs do
 // not wait for the stores to memory.
 
-constexpr int kTileK = 256, kTileN = 256;  // of the pair of CTAs
-constexpr int kDeep = 64;                  // rows of the contraction per stage
-constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time
 constexpr int kStages = 8;                 // of B in shared and A in tensor memory
 constexpr int kCodeStages = 8;             // of codes and scales in shared memory
 constexpr int kBBytes = kDeep * kTileN / 2 * 2, kXBytes = kDeep * kQBlock;  // of a CTA, per stage
@@ -683,7 +683,8 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
 
 // Adds a split tile's parts in order and finishes the gradient there; with no
 // parts at all (no rows) the gradient of every tile is 0.  A block takes 8 rows
-// of a tile, a thread 8 columns.
+// of a tile, a thread 8 columns.  a.whole: the launch's first tile, a.part: its
+// first part.
 __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
 {
     wait_prior_grid();
@@ -774,43 +775,6 @@ int make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *p, in
 bool rows_aligned(const void *dy, int64_t ld, int64_t rows)
 {
     return (((uintptr_t)dy) & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld > 0));
-}
-
-// How a call is cut up: its tiles, which of them are split along the rows, and
-// where the partial sums and the aligned copy lie in the workspace.
-struct Plan {
-    int tiles_k, tiles_n, kblocks, clusters, whole, splits, per_split;
-    int64_t ld_copy, copy_at, bytes;
-};
-
-// The pairs of CTAs take the tiles in rounds; what a last, partial round would
-// leave idle is used by splitting its tiles along the rows.  Of the splits
-// into 1 to 16 parts the one with the least estimated time is taken, in
-// stages of the contraction (0.28 us): the rounds, about 8 stages for each
-// item's start and end, and for a split the writing and joining of its parts
-// (0.5 MB each, about 0.3 stages) and one more launch (10 stages).
-void split_rest(Plan *p)
-{
-    const int tiles = p->tiles_k * p->tiles_n;
-    // (a bf16 tile done whole is stored once, so its rows fit one run)
-    const bool all = p->kblocks > kRunBf16;
-    p->whole = all ? 0 : tiles / p->clusters * p->clusters;
-    const int rest = tiles - p->whole;
-    p->splits = 1;
-    p->per_split = p->kblocks;
-    if (rest == 0 || p->kblocks == 0) return;
-    double best = all ? 1e30 : p->kblocks + 8;
-    for (int s = 2; s <= 16 && s * 4 <= p->kblocks; ++s) {
-        const int per = (p->kblocks + s - 1) / s, parts = (p->kblocks + per - 1) / per;
-        const int rounds = (rest * parts + p->clusters - 1) / p->clusters;
-        const double cost = (double)rounds * (per + 8) + 0.3 * rest * parts + 10;
-        if (cost < best) {
-            best = cost;
-            p->splits = parts;
-            p->per_split = per;
-        }
-    }
-    if (p->splits == 1) p->whole = tiles;
 }
 
 int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p)
@@ -933,14 +897,15 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     } else {
         a.whole = a.splits = 0;
     }
-    // (no rows: every tile is finished here, in runs that fit the grid)
+    // (no rows: every tile is finished here, without parts)
     for (int t = a.whole, tiles = p.tiles_k * p.tiles_n; t < tiles;) {
-        const int run = tiles - t < 65535 ? tiles - t : 65535;
+        const JoinRun run = join_run(a.whole, tiles, a.splits, t, 65535);
         Wg j = a;
-        j.whole = t;
-        const cudaError_t e = launch_after(k_weight_grad_join, dim3(kTileN / 8, (unsigned)run), 256, 0, st, j);
+        j.whole = run.tile;
+        j.part = a.part + run.part;
+        const cudaError_t e = launch_after(k_weight_grad_join, dim3(kTileN / 8, (unsigned)run.tiles), 256, 0, st, j);
         if (e != cudaSuccess) return pdl_fail(e, "weight gradient: joining the parts");
-        t += run;
+        t += run.tiles;
     }
     return ZERO1_OK;
 }
