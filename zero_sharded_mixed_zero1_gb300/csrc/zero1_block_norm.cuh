@@ -142,10 +142,19 @@ __device__ __forceinline__ void param8(const void *p, int f32, int vec, int64_t 
             return;
         }
     } else {
+        // (the type is looked at once, so that the eight loads are under way together)
+        if (f32) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int c = col + kStep<VEC> * k;
-            f[k] = c < D ? ld_param(p, f32, base + c) : 1.f;
+            for (int k = 0; k < 8; ++k) {
+                const int c = col + kStep<VEC> * k;
+                f[k] = c < D ? __ldg(static_cast<const float *>(p) + base + c) : 1.f;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = col + kStep<VEC> * k;
+                f[k] = c < D ? bf_one(__ldg(static_cast<const uint16_t *>(p) + base + c)) : 1.f;
+            }
         }
         return;
     }
