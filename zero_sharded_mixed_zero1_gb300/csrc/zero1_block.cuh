@@ -219,17 +219,6 @@ __device__ __forceinline__ float dot8(const V8 &a, const V8 &b)
     const float2 s = split(add2(x, y));
     return s.x + s.y;
 }
-template <class F>
-__device__ __forceinline__ V8 map8(const V8 &a, F &&f)
-{
-    V8 r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 v = split(a.p[k]);
-        r.p[k] = pair(f(v.x), f(v.y));
-    }
-    return r;
-}
 
 __device__ __forceinline__ V8 from_bf16(const uint4 q)
 {

@@ -38,10 +38,7 @@ __global__ void __launch_bounds__(256) k_block_norm_finish(const Finish f)
     if (slice || col >= f.D) return;
 #pragma unroll
     for (int q = 1; q < 8; ++q) x += sum[q][lane];
-    if (s == 2 && f.gate) {
-        const float g = sigmoid(ld_param(f.gate, f.gf32, col));
-        x *= g * (1.f - g);
-    }
+    if (s == 2 && f.gate) x *= Logistic<>(ld_param(f.gate, f.gf32, col)).slope;
     if (f.f32) {
         float *o = static_cast<float *>(f.out[s]) + col;
         *o = f.accumulate ? *o + x : x;

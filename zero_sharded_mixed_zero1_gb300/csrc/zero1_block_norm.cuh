@@ -182,27 +182,112 @@ __device__ __forceinline__ float row_sum(float x, float *red)
     return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.f);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// exp(-a) for a >= 0 to 2.5 ulps (and through the subnormal numbers, NaN for
+// NaN; USUAL: a is at most 87, where the result is a normal number): 2^t by the
+// hardware's 2-ulp instruction, t = -a log2(e) rounded, times 1 + r ln 2 for the
+// rest r of that product, which a fused multiply-add gives exactly and log2(e)'s
+// own lower part completes.  Without r the error grows with a: 100 ulps at 80.
+template <bool USUAL = false>
+__device__ __forceinline__ float exp_minus(float a)
+{
+    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147182f;
+    if (!USUAL) asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(200.f));  // an infinity would have no rest
+    const float t = __fmul_rn(-a, kLog2e);
+    const float r = __fmaf_rn(-a, kLog2eLow, __fmaf_rn(-a, kLog2e, -t));
+    float e;
+    if (USUAL) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    else asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return __fmaf_rn(e, __fmul_rn(r, kLn2), e);
+}
+
+// s = 1 / (1 + exp(-x)) and its slope s (1 - s), both from e = exp(-|x|) and 1 +
+// e, which is between 1 and 2: s = 1 / (1 + e) or e / (1 + e), slope = e / (1 +
+// e)^2, within 16 half ulps at every x.  1 - s would lose every bit where s
+// rounds to 1.
+template <bool USUAL = false>
+struct Logistic {
+    float s, slope;
+    __device__ __forceinline__ explicit Logistic(float x)
+    {
+        const float e = exp_minus<USUAL>(fabsf(x));
+        float q;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));  // 1 ulp
+        const float t = e * q;
+        s = x >= 0.f ? q : t;
+        slope = t * q;
+    }
+};
+__device__ __forceinline__ float sigmoid(float x) { return Logistic<>(x).s; }
 __device__ __forceinline__ float rstd_of(float ss, const Common &c) { return rsqrtf(fmaf(ss, c.inv_d, c.eps)); }
 
-// The gate's factor for a chunk (channel and full gates; else g is left).
-template <bool VEC>
-__device__ __forceinline__ void gate8(const Common &c, int64_t row, int col, float g[8])
+// Eight gates to their factors or slopes (or both).  Eight of usual size,
+// almost always all of them, take the shorter form (16384 x 8192 with a full
+// gate: backward 294 us against 298 without it, forward 263 against 266; 292 and
+// 257 with __expf and 1 - s).
+__device__ __forceinline__ bool usual8(float a, float b, float c, float d, float e, float f, float g, float h)
 {
-    if (c.gate_kind == ZERO1_GATE_CHANNEL) param8<VEC>(c.gate, c.gf32, c.pvec, 0, col, c.D, g);
-    else if (c.gate_kind == ZERO1_GATE_FULL) param8<VEC>(c.gate, c.gf32, c.gvec, row * c.ld_gate, col, c.D, g);
-    else return;
-    if (c.sigmoid) {
+    return max_abs(max_abs(a, b, c), max_abs(d, e, f), max_abs(g, h, 0.f)) <= 87.f;
+}
+template <bool USUAL>
+__device__ __forceinline__ void logistic8_of(V8 &g, V8 &slope)
+{
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = sigmoid(g[k]);
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = split(g.p[k]);
+        const Logistic<USUAL> a(v.x), b(v.y);
+        g.p[k] = pair(a.s, b.s);
+        slope.p[k] = pair(a.slope, b.slope);
+    }
+}
+__device__ __forceinline__ void logistic8(V8 &g, V8 &slope)
+{
+    const float2 a = split(g.p[0]), b = split(g.p[1]), c = split(g.p[2]), d = split(g.p[3]);
+    if (usual8(a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y)) logistic8_of<true>(g, slope);
+    else logistic8_of<false>(g, slope);
+}
+template <bool SLOPE>
+__device__ __forceinline__ void logistic8(float g[8])
+{
+    if (usual8(g[0], g[1], g[2], g[3], g[4], g[5], g[6], g[7])) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = SLOPE ? Logistic<true>(g[k]).slope : Logistic<true>(g[k]).s;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = SLOPE ? Logistic<>(g[k]).slope : Logistic<>(g[k]).s;
     }
 }
 
-__device__ __forceinline__ float token_gate(const Common &c, int64_t row)
+// The gates of a chunk (channel and full gates; else g is left).
+template <bool VEC>
+__device__ __forceinline__ void raw_gate8(const Common &c, int64_t row, int col, float g[8])
 {
+    if (c.gate_kind == ZERO1_GATE_CHANNEL) param8<VEC>(c.gate, c.gf32, c.pvec, 0, col, c.D, g);
+    else if (c.gate_kind == ZERO1_GATE_FULL) param8<VEC>(c.gate, c.gf32, c.gvec, row * c.ld_gate, col, c.D, g);
+}
+
+// Their factors.
+template <bool VEC>
+__device__ __forceinline__ void gate8(const Common &c, int64_t row, int col, float g[8])
+{
+    raw_gate8<VEC>(c, row, col, g);
+    if (c.sigmoid && c.gate_kind != ZERO1_GATE_TOKEN) logistic8<false>(g);
+}
+
+// A token's factor, and its slope.
+__device__ __forceinline__ float token_gate(const Common &c, int64_t row, float &slope)
+{
+    slope = 1.f;
     if (c.gate_kind != ZERO1_GATE_TOKEN) return 1.f;
     const float g = ld_param(c.gate, c.gf32, row * c.ld_gate);
-    return c.sigmoid ? sigmoid(g) : g;
+    if (!c.sigmoid) return g;
+    const Logistic<> l(g);
+    slope = l.slope;
+    return l.s;
+}
+__device__ __forceinline__ float token_gate(const Common &c, int64_t row)
+{
+    float slope;
+    return token_gate(c, row, slope);
 }
 
 // Write 8 values of a row into a checkpoint (all 32 lanes take part; values

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
             if (c.y8.codes) load_codes<VEC>(c.y8, row, col, c.D, y8[i], ey[i]);
             else if (a.y) yq[i].load(static_cast<const TA *>(a.y) + row * a.ld_y, col, c.D);
         }
-        const float gt = token_gate(c, row);
+        float gt_slope;
+        const float gt = token_gate(c, row, gt_slope);
         const float rs_pre = pre ? a.rstd_pre[row] : 0.f, rs_post = post ? a.rstd_post[row] : 1.f;
         float d[C][8], rh[C][8];
         float s1 = 0.f;
@@ -117,11 +118,18 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
                 const float ad = c.alpha * d[i][k];
                 const float p = ad * (w[k] * yh[i][k]);
                 if (a.need_gate && c.gate_kind == ZERO1_GATE_CHANNEL) add(2, i, k, p);
-                o[k] = p * (c.sigmoid ? g[k] * (1.f - g[k]) : 1.f);
+                o[k] = p;
                 d[i][k] = ad * g[k];
                 s2 = fmaf(g[k], p, s2);
             }
             if (a.need_gate && c.gate_kind == ZERO1_GATE_FULL) {
+                if (c.sigmoid) {  // (the slopes from the gates again: registers are short)
+                    float slope[8];
+                    raw_gate8<VEC>(c, row, col, slope);
+                    logistic8<true>(slope);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] *= slope[k];
+                }
                 if (VEC && a.dgvec) {
                     if (c.gf32) store_chunk<float, true>(static_cast<float *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
                     else store_chunk<uint16_t, true>(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Comm
         const bool tok = a.need_gate && c.gate_kind == ZERO1_GATE_TOKEN;
         if (post || tok) s2 = row_sum(s2, red[flip][1]);
         if (tok && tid == 0) {
-            const float dg = c.sigmoid ? s2 * gt * (1.f - gt) : s2;
+            const float dg = s2 * gt_slope;
             if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;
             else static_cast<uint16_t *>(a.dgate)[row * a.ld_dgate] = to_bf16(dg);
         }
@@ -304,8 +312,8 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
 
     int st = 0, flip = 0;
     for (int64_t row = blockIdx.x; row < c.rows; row += gridDim.x) {
-        float gt = 1.f;
-        if (GATE == 0 && c.gate_kind == ZERO1_GATE_TOKEN) gt = token_gate(c, row);
+        float gt = 1.f, gt_slope = 1.f;
+        if (GATE == 0 && c.gate_kind == ZERO1_GATE_TOKEN) gt = token_gate(c, row, gt_slope);
         // the stage that this warp has read a row ago is filled again
         __syncwarp();
         fetch(row + (int64_t)(stages - 1) * gridDim.x, ring + (st == 0 ? stages - 1 : st - 1) * stage_bytes);
@@ -353,20 +361,20 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
                 t += dot8(x, u);  // times a: the gradient of a token's gate
                 d[i] = mul8(x, c.alpha * gt);
             } else {
-                V8 gc;
+                V8 gc, slope;
                 if (GATE == 1) {
                     gc = kept8<T, C>(kept + 2 * kVector, i);
                 } else {
                     gc = c.gf32 ? Ld::take(b + S::gate, i, static_cast<const float *>(c.gate) + row * c.ld_gate)
                                 : Ld::take(b + S::gate, i, static_cast<const uint16_t *>(c.gate) + row * c.ld_gate);
-                    if (c.sigmoid) gc = map8(gc, [](float v) { return sigmoid(v); });
+                    if (c.sigmoid) logistic8(gc, slope);
                 }
                 const V8 ax = mul8(x, c.alpha), p = mul8(ax, u);
                 if (GATE == 1) acc_gate[GATE == 1 ? i : 0] = add8(acc_gate[GATE == 1 ? i : 0], p);
                 t += dot8(gc, p);
                 d[i] = mul8(ax, gc);
                 if (GATE == 2 && a.need_gate) {
-                    const V8 o = c.sigmoid ? mul8(p, map8(gc, [](float v) { return v * (1.f - v); })) : p;
+                    const V8 o = c.sigmoid ? mul8(p, slope) : p;
                     if (c.gf32) Ld::put(static_cast<float *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
                     else Ld::put(static_cast<uint16_t *>(a.dgate) + row * a.ld_dgate, col, c.D, o);
                 }
@@ -377,7 +385,7 @@ k_block_norm_bwd_staged(const Common c, const Bwd a, const int stages, const int
         if (GATE == 0) {
             t *= c.alpha;
             if (tok && tid == 0) {
-                const float dg = c.sigmoid ? t * gt * (1.f - gt) : t;
+                const float dg = t * gt_slope;
                 if (c.wf32) static_cast<float *>(a.dgate)[row * a.ld_dgate] = dg;
                 else static_cast<uint16_t *>(a.dgate)[row * a.ld_dgate] = to_bf16(dg);
             }

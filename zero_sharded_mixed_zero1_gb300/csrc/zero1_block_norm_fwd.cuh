@@ -180,7 +180,10 @@ k_block_norm_fwd_staged(const Common c, const Fwd a, const int stages, const int
             } else if (GATE == 2) {
                 V8 g = c.gf32 ? Ld::take(b + at_gate, i, static_cast<const float *>(c.gate) + row * c.ld_gate)
                               : Ld::take(b + at_gate, i, static_cast<const uint16_t *>(c.gate) + row * c.ld_gate);
-                if (c.sigmoid) g = map8(g, [](float x) { return sigmoid(x); });
+                if (c.sigmoid) {
+                    V8 slope;
+                    logistic8(g, slope);
+                }
                 v[i] = mul8(v[i], g);
             }
             v[i] = fma8(v[i], c.alpha * gt, Ld::take(b + at_x, i, static_cast<const TR *>(a.x) + row * a.ld_x));
