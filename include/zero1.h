@@ -680,7 +680,10 @@ int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const zero1_block_n
  * workspace: device, 128-byte aligned, zero1_weight_grad_workspace bytes for
  * the same rows, n, k, dy and ld_dy (fp32 partial sums where the rows are
  * split over blocks; an aligned copy of dy when its rows are not on 16-byte
- * boundaries). */
+ * boundaries).  The kernel's waits are bounded (1 s each): should one run out,
+ * which takes a fault or a GPU that is held up for that long, dw is wrong
+ * although the call has returned ZERO1_OK, and bit 0 of the device status
+ * (zero1_device_status) says so. */
 int zero1_weight_grad_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy, int64_t *bytes);
 int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const zero1_checkpoint8_t *x8, const void *col_scale,
                       int32_t scale_dtype, void *dw, int64_t ld_dw, int32_t out_dtype, int32_t accumulate,

@@ -16,6 +16,18 @@ DRIVER = r"""
 using namespace z1wg;
 int main(int argc, char **argv)
 {
+    if (argc == 2) {  // every state that a use of B's place can be left in
+        printf("[");
+        for (unsigned mine = 0; mine < 2; ++mine)
+            for (unsigned other = 0; other < 2; ++other)
+                for (unsigned late = 0; late <= 8; ++late) {
+                    const Drain d = drain_of(5, 5 + mine, 5 + other, late);
+                    printf("%s[%u, %u, %u, %u, %u, %u]", mine + other + late ? ", " : "", mine, other, late, d.arrivals,
+                           d.announce, d.write_off);
+                }
+        printf("]");
+        return 0;
+    }
     const long tiles_k = atol(argv[1]), tiles_n = atol(argv[2]), kblocks = atol(argv[3]), limit = atol(argv[4]);
     Plan p{};
     p.tiles_k = (int)tiles_k; p.tiles_n = (int)tiles_n; p.kblocks = (int)kblocks; p.clusters = 76;
@@ -68,3 +80,30 @@ def test_each_joined_tile_gets_its_own_parts(plan, tiles_k, tiles_n, kblocks, li
             seen[first + k] = part + k * p["splits"] * 65536          # what block k of the launch reads
     assert sorted(seen) == list(range(p["whole"], p["tiles"]))
     assert all(at == (t - p["whole"]) * p["splits"] * 65536 for t, at in seen.items())
+
+
+def test_what_is_made_up_waits_for_the_loads_under_way(plan):
+    """A barrier of nine arrivals and two halves of bytes (the leading CTA's load
+    announces both and is one arrival; eight converting warps) after the pair has
+    given up: the use becomes complete exactly when every half that was loaded
+    has landed, whenever that is, and no half lands on a completed use."""
+    states = plan("drain")
+    assert len(states) == 36
+    for mine, other, late, arrivals, announce, write_off in states:
+        if not mine and not other:
+            continue                                       # past the last use: not asked for
+        for before in range(mine + other + 1):             # halves that land before the barrier is made up
+            pending, bytes_due = 9 - mine - (8 - late), 2 * mine - before
+            done = pending == 0 and bytes_due == 0
+            assert not done or (before == mine + other and not (arrivals or announce or write_off))
+            under_way = mine + other - before
+            bytes_due += announce
+            bytes_due -= write_off
+            assert arrivals <= pending                     # never one arrival too many
+            assert not (pending == 0 and bytes_due == 0 and under_way)
+            pending -= arrivals
+            assert pending == 0
+            while under_way:
+                assert bytes_due != 0                      # not complete yet
+                bytes_due, under_way = bytes_due - 1, under_way - 1
+            assert bytes_due == 0

@@ -3,7 +3,8 @@
 //
 // Every wait is bounded (kWaitNs of %globaltimer); a wait that runs out
 // records an error in its source's g_zero1_status, which zero1_device_status
-// reports, and the kernel drains and returns instead of hanging.
+// reports, and the kernel waits (again with a limit) for its own copies in
+// flight and returns instead of hanging.  The call's results are then wrong.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -35,6 +36,18 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *b, uint32_t bytes)
 __device__ __forceinline__ void mbar_arrive(uint64_t *b)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
+// Bytes announced, bytes written off as if they had come, then arrivals.
+__device__ __forceinline__ void mbar_make_up(uint64_t *b, uint32_t arrivals, uint32_t announce, uint32_t write_off)
+{
+    if (announce)
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(announce) : "memory");
+    if (write_off)
+        asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(write_off)
+                     : "memory");
+    if (arrivals)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(arrivals) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try(uint64_t *b, uint32_t parity)

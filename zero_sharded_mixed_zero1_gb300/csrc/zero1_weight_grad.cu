@@ -65,6 +65,9 @@ constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
 struct WgBars {
     uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
     uint32_t tmem;
+    uint32_t failed;                  // a wait of either CTA ran out
+    uint32_t loads, mmas, fills;      // uses of B's places loaded, stages and accumulator fills issued
+    uint32_t converted[4 * kSets];    // the first use that a converting warp has not arrived at
 };
 constexpr int kStash = 32;  // packed pairs of bf16 results, or fp32 ones, that a storing thread keeps in shared memory
 constexpr int kBoxRows = 16, kPlaces = kStash / kBoxRows;  // of the boxes that a part's sums leave in
@@ -193,10 +196,28 @@ __device__ __forceinline__ void arrive_leader(uint64_t *bar)
         : "memory");
 }
 
-// A bounded wait of a whole warp.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
+// The same place in the shared memory of the pair's CTA `rank`.
+__device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank)
 {
-    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity));
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t read_rank(const uint32_t *p, uint32_t rank)
+{
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at_rank(p, rank)) : "memory");
+    return x;
+}
+
+// A bounded wait of a whole warp; one that runs out is noted in both CTAs.
+__device__ __forceinline__ bool warp_wait(WgBars &b, uint64_t *bar, uint32_t parity)
+{
+    if (__all_sync(0xffffffffu, mbar_wait_long(bar, parity))) return true;
+    if ((threadIdx.x & 31) < 2)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(&b.failed, threadIdx.x & 31)), "r"(1u) : "memory");
+    __syncwarp();
+    return false;
 }
 
 // The leading CTA's copy of a barrier, as a cluster address.
@@ -485,6 +506,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
         }
         mbar_init(&bar.dfull, 1);
         mbar_init(&bar.dempty, 16);  // eight storing warps of each CTA
+        bar.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tc_alloc(&bar.tmem);
@@ -507,7 +529,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             const int n = w.n0 + (int)rank * (kTileN / 2);
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = it % kStages;
-                if (it >= kStages && !(ok = warp_wait(&bar.empty[s], (it / kStages - 1) & 1))) break;
+                if (it >= kStages && !(ok = warp_wait(bar, &bar.empty[s], (it / kStages - 1) & 1))) break;
                 unsigned char *b = smem + s * kBBytes;
                 if (elect_one()) {
                     // both CTAs' halves count on the leading CTA's barrier
@@ -519,10 +541,11 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                 __syncwarp();
             }
         }
-        // the last copies must land before the pair may exit
+        // the last copies must land before the pair may exit (both CTAs have as many)
         if (rank == 0)
-            for (uint32_t q = it > kStages ? it - kStages : 0; q < it; ++q)
-                warp_wait(&bar.full[q % kStages], (q / kStages) & 1);
+            for (uint32_t q = it > kStages ? it - kStages : 0; q < it && ok; ++q)
+                ok = warp_wait(bar, &bar.full[q % kStages], (q / kStages) & 1);
+        if (lane == 0) bar.loads = it;
     } else if (warp == 3) {
         uint32_t it = 0;
         bool ok = true;
@@ -533,7 +556,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             const int k = w.k0 + (int)rank * kQBlock;
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int s = it % kCodeStages;
-                if (it >= kCodeStages && !(ok = warp_wait(&bar.cempty[s], (it / kCodeStages - 1) & 1))) break;
+                if (it >= kCodeStages && !(ok = warp_wait(bar, &bar.cempty[s], (it / kCodeStages - 1) & 1))) break;
                 if (elect_one()) {
                     mbar_expect_tx(&bar.cfull[s], kXBytes + kDeep);
                     tma_2d(s_codes + s * kXBytes, &map_x, k, kb * kDeep, &bar.cfull[s]);
@@ -542,24 +565,25 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                 __syncwarp();
             }
         }
+        // (only the copies themselves are waited for here)
         for (uint32_t q = it > kCodeStages ? it - kCodeStages : 0; q < it; ++q)
-            warp_wait(&bar.cfull[q % kCodeStages], (q / kCodeStages) & 1);
+            warp_wait(bar, &bar.cfull[q % kCodeStages], (q / kCodeStages) & 1);
     } else if (warp == 1) {
         if (rank == 0) {
-            uint32_t it = 0, tile = 0;  // stages and accumulator fills so far
+            uint32_t it = 0, tile = 0, fills = 0;  // stages, accumulator fills begun and done so far
             bool ok = true;
             const uint64_t b0 = b_desc(smem_u32(smem));
             for (int i = first; i < items && ok; i += step) {
                 const Item w = item_of(a, i);
                 for (int kb = w.kb0; kb < w.kb1 && ok; ++tile) {
-                    if (tile > 0 && !(ok = warp_wait(&bar.dempty, (tile - 1) & 1))) break;
+                    if (tile > 0 && !(ok = warp_wait(bar, &bar.dempty, (tile - 1) & 1))) break;
                     const int start = kb, end = min(kb + a.run, w.kb1);
                     for (; kb < end; ++kb, ++it) {
                         const int s = it % kStages;
                         // what the instructions take is ready before the branch, in uniform registers
                         const uint64_t b = b0 + (uint64_t)(s * (kBBytes >> 4));
                         const uint32_t ta = tmem + kTmemA + s * kTmemAStage, more = kb > start;
-                        if (!(ok = warp_wait(&bar.full[s], (it / kStages) & 1))) break;
+                        if (!(ok = warp_wait(bar, &bar.full[s], (it / kStages) & 1))) break;
                         tc_after();
                         if (elect_one()) {
 #pragma unroll
@@ -570,14 +594,19 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                         }
                         __syncwarp();
                     }
+                    fills += ok;
                 }
             }
             // the MMAs must have finished with both CTAs' memory before the exit
-            if (it > 0) warp_wait(&bar.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1);
+            if (it > 0) warp_wait(bar, &bar.empty[(it - 1) % kStages], ((it - 1) / kStages) & 1);
+            if (lane == 0) {
+                bar.mmas = it;
+                bar.fills = fills;
+            }
         }
     } else if (warp >= 4 && warp < 4 + 4 * kSets) {
         const uint32_t set = (warp - 4) / 4, q = warp % 4;
-        uint32_t it0 = 0;  // stages before this item
+        uint32_t it0 = 0, stopped = 0;  // stages before this item; where a wait ran out
         bool ok = true;
         // this thread's share of a stage: ldmatrix rows `lane` and 32 + lane, columns 32 q .. 32 q + 31
         const uint32_t x_row = smem_u32(s_codes) + lane * 128, x_swz = lane & 7;
@@ -587,7 +616,8 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             const uint32_t n = w.kb1 - w.kb0;
             for (uint32_t j = (set - it0) % kSets; j < n; j += kSets) {
                 const uint32_t it = it0 + j, s = it % kStages, c = it % kCodeStages;
-                if (!(ok = warp_wait(&bar.cfull[c], (it / kCodeStages) & 1))) break;
+                stopped = it;
+                if (!(ok = warp_wait(bar, &bar.cfull[c], (it / kCodeStages) & 1))) break;
                 // Scales of rows 2 lane and 2 lane + 1 as a bf16 pair, passed to
                 // the lanes that convert those rows.  Almost always every scale
                 // of the stage is at most 2^7 and every row is there: then one
@@ -600,7 +630,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
                     mine = factor1(e & 255, left >= 1) | factor1(e >> 8, left >= 2) << 16;
                     more = factor2(e & 255) | factor2(e >> 8) << 16;
                 }
-                if (it >= kStages && !(ok = warp_wait(&bar.empty[s], (it / kStages - 1) & 1))) break;
+                if (it >= kStages && !(ok = warp_wait(bar, &bar.empty[s], (it / kStages - 1) & 1))) break;
                 tc_after();
                 const uint32_t x = x_row + c * kXBytes, at = a_addr + s * kTmemAStage;
 #pragma unroll
@@ -640,6 +670,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             }
             it0 += n;
         }
+        if (lane == 0) bar.converted[warp - 4] = ok ? it0 : stopped;
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
         uint32_t *const places = s_stash + (4 * half + q) * 32 * kStash, *const stash = places + lane;
@@ -650,7 +681,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + half * (kTileN / 2);
             const int64_t k0 = w.k0 + (int64_t)rank * kQBlock + 32 * q, n0 = w.n0 + half * (kTileN / 2);
             for (int kb = w.kb0; kb < w.kb1; kb += a.run, ++tile) {
-                if (!(ok = warp_wait(&bar.dfull, tile & 1))) break;
+                if (!(ok = warp_wait(bar, &bar.dfull, tile & 1))) break;
                 tc_after();
                 const bool add = kb > w.kb0;
                 if (w.part >= 0) {
@@ -675,6 +706,30 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     __syncwarp();
     __syncthreads();
     cluster_sync();
+    // From here on neither CTA starts anything.  If no wait ran out, all that was
+    // started has finished (the waits above).  If one did, what is under way to
+    // either CTA's shared memory, or reads it, is waited for before the pair's
+    // memory is given back: the loads of B, by making up what their barriers
+    // lack, and the MMAs with the arrivals that follow them.
+    if (bar.failed) {
+        if (warp == 0 && rank == 0) {
+            const uint32_t mine = bar.loads, other = read_rank(&bar.loads, 1), n = max(mine, other);
+            for (uint32_t q = n > kStages ? n - kStages : 0; q < n; ++q) {
+                const uint32_t *c = &bar.converted[q % kSets * 4 + lane % 4];  // lanes 0-3 here, 4-7 there
+                const uint32_t late = __popc(__ballot_sync(0xffffffffu, lane < 8 && read_rank(c, lane / 4 & 1) <= q));
+                const Drain d = drain_of(q, mine, other, late);
+                if (lane == 0) mbar_make_up(&bar.full[q % kStages], d.arrivals, d.announce * kBBytes, d.write_off * kBBytes);
+                __syncwarp();
+                warp_wait(bar, &bar.full[q % kStages], (q / kStages) & 1);
+            }
+        } else if (warp == 1) {
+            const uint32_t m = read_rank(&bar.mmas, 0), f = read_rank(&bar.fills, 0);
+            if (m > 0) warp_wait(bar, &bar.empty[(m - 1) % kStages], ((m - 1) / kStages) & 1);
+            if (f > 0) warp_wait(bar, &bar.dfull, (f - 1) & 1);
+        }
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 2) {
         tc_after();
         tc_free(tmem);

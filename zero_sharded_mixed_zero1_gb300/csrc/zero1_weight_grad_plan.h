@@ -4,6 +4,12 @@
 
 #include <stdint.h>
 
+#ifdef __CUDACC__
+#define Z1_HOST_DEVICE __host__ __device__
+#else
+#define Z1_HOST_DEVICE
+#endif
+
 namespace z1wg {
 
 constexpr int kTileK = 256, kTileN = 256;     // of a pair of CTAs
@@ -58,6 +64,22 @@ struct JoinRun {
 inline JoinRun join_run(int whole, int tiles, int splits, int tile, int limit)
 {
     return JoinRun{tile, tiles - tile < limit ? tiles - tile : limit, (int64_t)(tile - whole) * splits * kTileN * kTileK};
+}
+
+// What the barrier of one use of a place for B still lacks once a pair of CTAs
+// has given up.  A use is complete after one arrival that announces both CTAs'
+// halves (the leading CTA's, with its own load), the converting warps' eight,
+// and the bytes of both halves.  q: the use; mine, other: how many uses the
+// leading CTA and the other one have loaded; late: converting warps that have
+// not arrived.  With these arrivals made and these halves announced or written
+// off, the use completes when the loads under way have landed, and not before.
+struct Drain {
+    uint32_t arrivals, announce, write_off;
+};
+
+Z1_HOST_DEVICE inline Drain drain_of(uint32_t q, uint32_t mine, uint32_t other, uint32_t late)
+{
+    return Drain{late + (q < mine ? 0u : 1u), q >= mine && q < other ? 1u : 0u, q < mine && q >= other ? 1u : 0u};
 }
 
 }  // namespace z1wg
