@@ -561,8 +561,9 @@ int zero1_checksum(const void *data, int64_t nbytes, uint64_t *out, zero1_stream
  *    step); each output is rounded once, when it is stored.
  *  - rows may be 0: forward calls do nothing, gradients that are sums over
  *    rows get +0 (or stay, when accumulated into); no input is looked at.
- *  - Results do not depend on timing: no floating-point atomics, fixed
- *    summation orders.
+ *  - Results do not depend on timing: summation orders are fixed, and the only
+ *    reductions to memory are each to one address from one thread, one after
+ *    the other.
  * ------------------------------------------------------------------------- */
 
 /* An 8-bit checkpoint of a [rows, cols] activation: e4m3 codes and one
@@ -675,12 +676,16 @@ int zero1_block_norm_backward(const zero1_block_norm_t *cfg, const zero1_block_n
  * checkpoint of rh and col_scale = w_pre this is the gradient for X = h, which
  * then need not be kept; dw: device [n, k] of out_dtype, for instance a view
  * into a replica's flat gradient buffer at any element offset; accumulate != 0
- * adds to it (rounded once).  The checkpoint's values are exact in bf16; the
- * products are summed in fp32 on the tensor cores.  Device memory only.
+ * adds the scaled fp32 sum to it, with one rounding.  The checkpoint's values
+ * (which hold no NaN code: a block that stands for NaN has E = 255) are exact in
+ * bf16; the products are summed in fp32 on the tensor cores, whose additions
+ * truncate.  An fp32 dw is summed in runs of 2048 rows that are added in fp32,
+ * where a run's magnitudes below 2^-126 may count as 0; a bf16 dw in runs of up to
+ * 131072 rows.  Device memory only.
  * workspace: device, 128-byte aligned, zero1_weight_grad_workspace bytes for
  * the same rows, n, k, dy and ld_dy (fp32 partial sums where the rows are
- * split over blocks; an aligned copy of dy when its rows are not on 16-byte
- * boundaries).  The kernel's waits are bounded (1 s each): should one run out,
+ * split over blocks or, in whole tiles, take several runs; an aligned copy of dy
+ * when its rows are not on 16-byte boundaries).  The kernel's waits are bounded (1 s each): should one run out,
  * which takes a fault or a GPU that is held up for that long, dw is wrong
  * although the call has returned ZERO1_OK, and bit 0 of the device status
  * (zero1_device_status) says so. */

@@ -88,7 +88,9 @@ struct Wg {
     void *dw;
     int64_t ld_dw;
     int out_f32, accumulate, pairs;  // pairs: two outputs of a row per store
+    int boxes;                       // fp32 results may go to dw in boxes
     float *part;                     // [split tile][part][kTileN][kTileK]
+    float *held;                     // [CTA][storing warp][kTileN / 2][32 lanes]
 };
 
 // ------------------------------------------------------------- tcgen05 -----
@@ -391,14 +393,17 @@ __device__ __forceinline__ void store_bf16(const Wg &a, uint32_t acc, int64_t k0
     }
 }
 
-// Adds to what this thread stored before, or to the caller's gradient.  Only
-// this thread ever adds there, one addition after the other, so the order of
-// the sum is fixed; a reduction leaves no value to wait for.
+// Adds to what this thread stored before.  Only this thread ever adds there, one
+// addition after the other, so the order of the sum is fixed; a reduction leaves
+// no value to wait for.  It takes subnormal values for 0 (measured; copies to
+// the same place in boxes, which do not, took 211 us for 188 at 4096 x 4096 over
+// 8192 rows), so it serves this call's own sums only, never the caller's.
 __device__ __forceinline__ void add_to(float *p, float x) { asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(x) : "memory"); }
 __device__ __forceinline__ void add_to(float *p, float2 x)
 {
     asm volatile("red.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x.x), "f"(x.y) : "memory");
 }
+
 // fp32 results, 32 lanes x 128 rows, two columns of a row per lane as above
 // (one column per lane, in the lanes' order, took twice the instructions and
 // more time).  rows: how many of the 128 are stored; cols: of this lane's two.
@@ -434,7 +439,63 @@ __device__ __forceinline__ void store_f32(float *o, int64_t ld, int rows, int co
     }
 }
 
-// A box from shared memory, added to what is there or written, and a group of its own.
+// What is added to the caller's gradient is the whole sum, rounded once: the
+// sums of the runs before an item's last one are held in the workspace, 128
+// values per thread of its own, 32 lanes side by side.
+constexpr int kHeld = 16;  // values that are on their way at one time
+
+__device__ __forceinline__ void hold_run(float *held, bool begin, uint32_t acc, uint64_t *dempty)
+{
+#pragma unroll 1
+    for (int c = 0; c < kTileN / 2; c += 32) {
+        uint32_t v[32];
+        tc_load32(acc + c, v);
+        if (c + 32 == kTileN / 2) release_acc(dempty);
+#pragma unroll
+        for (int j = 0; j < 32; ++j, held += 32) {
+            if (begin) *held = __uint_as_float(v[j]);
+            else add_to(held, __uint_as_float(v[j]));
+        }
+    }
+}
+
+struct Held {
+    const float *p;  // NULL: nothing is held
+    // Adds rows c .. c + 15.  (Loading them earlier took registers that the rest
+    // of the kernel then spilled.)
+    __device__ __forceinline__ void join(int c, uint32_t v[kHeld]) const
+    {
+        float h[kHeld];
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) h[j] = __ldcg(p + (c + j) * 32);
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) v[j] = __float_as_uint(h[j] + __uint_as_float(v[j]));
+    }
+};
+
+// fp32 results added to the caller's where boxes cannot take them (dw off 16-byte
+// boundaries), an element at a time.
+__device__ __forceinline__ void add_f32_any(float *o, int64_t ld, int rows, bool in, float scale, const Held &held, uint32_t acc,
+                                            uint64_t *dempty)
+{
+#pragma unroll 1
+    for (int c = 0; c < kTileN / 2; c += kHeld) {
+        uint32_t v[kHeld];
+        tc_load16(acc + c, v);
+        if (c + kHeld == kTileN / 2) release_acc(dempty);
+        if (held.p) held.join(c, v);
+        float old[kHeld];
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) old[j] = in && c + j < rows ? o[j * ld] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+            if (in && c + j < rows) o[j * ld] = fmaf(__uint_as_float(v[j]), scale, old[j]);
+        o += kHeld * ld;
+    }
+}
+
+// A box from shared memory, added to what is there or written, and a group of
+// its own.  (These reductions keep subnormal values, measured.)
 __device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bool add, const uint32_t *place)
 {
     if (add)
@@ -448,44 +509,45 @@ __device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bo
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// Sums of a split tile's part, 32 lanes x 128 rows, as boxes of 32 columns x
-// kBoxRows rows that are copied or added from the warp's two places in shared
-// memory: no trade between lanes and a quarter of the instructions.  (Whole
-// tiles are stored from registers as above, which lets go of the accumulator
-// sooner.)  Only this warp writes here, and a run's boxes are added after those
-// of the run before.
-__device__ __forceinline__ void store_part(const CUtensorMap *map, int x, int y, bool add, uint32_t acc, uint32_t *places,
-                                           uint64_t *dempty)
+// 32 lanes x 128 rows as boxes of 32 columns x kBoxRows rows, copied or added
+// from the warp's two places in shared memory: no trade between lanes, a
+// quarter of the instructions, and nothing to wait for.  rows: how many of the
+// 128 are wanted (a box may hang over dw's edge and is clipped there).
+__device__ __forceinline__ void store_boxes(const CUtensorMap *map, int x, int y, int rows, bool add, float scale,
+                                            const Held &held, uint32_t acc, uint32_t *places, uint64_t *dempty)
 {
+    static_assert(kBoxRows == kHeld, "a box takes what is on its way");
     const int lane = threadIdx.x & 31;
     int at = 0;
 #pragma unroll 1
-    for (int c = 0; c < kTileN / 2; c += 2 * kBoxRows) {
-        uint32_t v[2 * kBoxRows];
-        tc_load32(acc + c, v);
-        if (c + 2 * kBoxRows == kTileN / 2) release_acc(dempty);
+    for (int c = 0; c < kTileN / 2; c += kBoxRows) {
+        uint32_t v[kBoxRows];
+        tc_load16(acc + c, v);
+        if (c + kBoxRows == kTileN / 2) release_acc(dempty);
+        if (held.p) held.join(c, v);
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPlaces - 1) : "memory");  // the place is free
+        __syncwarp();
+        uint32_t *place = places + at * 32 * kBoxRows;
 #pragma unroll
-        for (int h = 0; h < 2 * kBoxRows; h += kBoxRows) {
-            if (elect_one()) {  // the run before is written, or the place's last box has been read
-                if (c + h == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                else asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPlaces - 1) : "memory");
-            }
-            __syncwarp();
-            uint32_t *place = places + at * 32 * kBoxRows;
-#pragma unroll
-            for (int j = 0; j < kBoxRows; ++j) place[32 * j + own_column(lane)] = v[h + j];
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (elect_one()) box_out(map, x, y + c + h, add, place);
-            __syncwarp();
-            at = at + 1 == kPlaces ? 0 : at + 1;
-        }
+        for (int j = 0; j < kBoxRows; ++j) place[32 * j + own_column(lane)] = __float_as_uint(__uint_as_float(v[j]) * scale);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (c < rows && elect_one()) box_out(map, x, y + c, add, place);
+        __syncwarp();
+        at = at + 1 == kPlaces ? 0 : at + 1;
     }
+}
+
+// All boxes that this warp has sent are written.
+__device__ __forceinline__ void boxes_written()
+{
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
 k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_x,
-              const __grid_constant__ CUtensorMap map_part, const Wg a)
+              const __grid_constant__ CUtensorMap map_part, const __grid_constant__ CUtensorMap map_dw, const Wg a)
 {
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -674,6 +736,7 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
     } else if (warp >= 4 + 4 * kSets) {
         const int q = warp % 4, half = (warp - 4 - 4 * kSets) / 4;
         uint32_t *const places = s_stash + (4 * half + q) * 32 * kStash, *const stash = places + lane;
+        float *const sums = a.held + ((int64_t)blockIdx.x * 8 + 4 * half + q) * (kTileN / 2) * 32 + lane;
         uint32_t tile = 0;
         bool ok = true;
         for (int i = first; i < items && ok; i += step) {
@@ -683,25 +746,38 @@ k_weight_grad(const __grid_constant__ CUtensorMap map_dy, const __grid_constant_
             for (int kb = w.kb0; kb < w.kb1; kb += a.run, ++tile) {
                 if (!(ok = warp_wait(bar, &bar.dfull, tile & 1))) break;
                 tc_after();
-                const bool add = kb > w.kb0;
-                if (w.part >= 0) {
-                    store_part(&map_part, (int)(k0 - w.k0), w.part * kTileN + half * (kTileN / 2), add, acc, places, &bar.dempty);
-                } else if (a.out_f32) {
-                    const int64_t own = k0 + own_column(lane), k = k0 + (lane & 16) + 2 * (lane & 7);
-                    float *o = static_cast<float *>(a.dw) + n0 * a.ld_dw + k;
-                    const int rows = (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
-                    const int cols = (int)max((int64_t)0, min((int64_t)2, a.K - k));
-                    const float scale = a.scale && own < a.K ? ld_param(a.scale, a.scale_f32, own) : 1.f;
-                    if (add || a.accumulate) store_f32<true>(o, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
-                    else store_f32<false>(o, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
-                } else {
+                const bool begin = kb == w.kb0, end = kb + a.run >= w.kb1;
+                if (w.part < 0 && !a.out_f32) {  // (takes one run)
                     store_bf16(a, acc, k0, n0, stash, &bar.dempty);
+                    continue;
                 }
+                const int64_t k = k0 + own_column(lane), two = k0 + (lane & 16) + 2 * (lane & 7);
+                const int rows = (int)max((int64_t)0, min((int64_t)(kTileN / 2), a.N - n0));
+                const float scale = w.part < 0 && a.scale && k < a.K ? ld_param(a.scale, a.scale_f32, k) : 1.f;
+                float *const o = static_cast<float *>(a.dw) + n0 * a.ld_dw;
+                if (w.part < 0 && !a.accumulate && !(a.boxes && begin && end)) {
+                    const int cols = (int)max((int64_t)0, min((int64_t)2, a.K - two));
+                    if (begin) store_f32<false>(o + two, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
+                    else store_f32<true>(o + two, a.ld_dw, rows, cols, a.pairs, scale, acc, &bar.dempty);
+                    continue;
+                }
+                if (w.part < 0 && !end) {
+                    hold_run(sums, begin, acc, &bar.dempty);
+                    continue;
+                }
+                const Held held{w.part < 0 && !begin ? sums : nullptr};
+                if (w.part < 0 && !a.boxes) {
+                    add_f32_any(o + k, a.ld_dw, rows, k < a.K, scale, held, acc, &bar.dempty);
+                    continue;
+                }
+                const bool part = w.part >= 0;
+                if (part && !begin) boxes_written();  // the run before
+                store_boxes(part ? &map_part : &map_dw, (int)(part ? k0 - w.k0 : k0),
+                            part ? w.part * kTileN + half * (kTileN / 2) : (int)n0, part ? kTileN / 2 : k0 < a.K ? rows : 0,
+                            part ? !begin : a.accumulate, scale, held, acc, places, &bar.dempty);
             }
         }
-        // the boxes on their way are written before the grid counts as done
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
+        boxes_written();  // before the grid counts as done
     }
     __syncwarp();
     __syncthreads();
@@ -760,23 +836,25 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
     }
     const int64_t kk = (int64_t)k0 + k;
     const int width = kk + 8 <= a.K ? 8 : (int)(a.K - kk);
-    if (a.scale)
+    float scale[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= j < width ? ld_param(a.scale, a.scale_f32, kk + j) : 0.f;
+    for (int j = 0; j < 8; ++j) scale[j] = a.scale && j < width ? ld_param(a.scale, a.scale_f32, kk + j) : 1.f;
     const int64_t at = (int64_t)(n0 + n) * a.ld_dw + kk;
     if (a.out_f32) {
         float *o = static_cast<float *>(a.dw) + at;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j < width) o[j] = a.accumulate ? o[j] + x[j] : x[j];
+            if (j < width) o[j] = a.accumulate ? fmaf(x[j], scale[j], o[j]) : x[j] * scale[j];
     } else {
         uint16_t *o = static_cast<uint16_t *>(a.dw) + at;
         if (!a.accumulate && width == 8 && ((uintptr_t)o & 15) == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= scale[j];
             store8(o, x);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < width) o[j] = to_bf16(a.accumulate ? bf_one(o[j]) + x[j] : x[j]);
+                if (j < width) o[j] = to_bf16(a.accumulate ? fmaf(x[j], scale[j], bf_one(o[j])) : x[j] * scale[j]);
         }
     }
 }
@@ -846,8 +924,8 @@ int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p
     p->tiles_n = (int)tn;
     p->kblocks = (int)kb;
     split_rest(p);
-    const int64_t parts = p->splits > 1 ? (tk * tn - p->whole) * p->splits : 0;
-    p->copy_at = parts * kTileN * kTileK * 4;
+    p->held_at = p->splits > 1 ? (tk * tn - p->whole) * p->splits * kTileN * kTileK * 4 : 0;
+    p->copy_at = p->held_at + (holds_sums(*p) ? (int64_t)p->clusters * kTileN * kTileK * 4 : 0);
     p->ld_copy = round_up(N, 8);
     p->bytes = p->copy_at + (rows_aligned(dy, ld, T) ? 0 : round_up(T * p->ld_copy * 2, 128));
     return ZERO1_OK;
@@ -920,6 +998,7 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
     a.accumulate = accumulate != 0;
     a.pairs = ((uintptr_t)dw & (2 * eo - 1)) == 0 && a.ld_dw % 2 == 0;
     a.part = static_cast<float *>(workspace);
+    a.held = workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + p.held_at) : nullptr;
     if (T > 0) {
         a.exps = x8->exps;
         a.ld_exps = x8->ld_exps;
@@ -933,19 +1012,24 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
             src = copy;
             ld = p.ld_copy;
         }
-        CUtensorMap mdy, mx, mpart{};
+        // (a box is clipped at dw's edge by 16 bytes)
+        a.boxes = a.out_f32 && ((uintptr_t)dw & 15) == 0 && a.ld_dw % 4 == 0 && K % 4 == 0 &&
+                  a.ld_dw < (INT64_C(1) << 37);  // (a tensor map's strides are below 2^40 bytes)
+        CUtensorMap mdy, mx, mpart{}, mdw{};
         if ((rc = make_map(&mdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, src, T, n, ld, 64, "dy")) ||
             (rc = make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
                            "the codes")) ||
-            (p.splits > 1 && (rc = make_map(&mpart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, p.copy_at / (kTileK * 4), kTileK,
-                                            kTileK, 32, "the parts", kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE))))
+            (p.splits > 1 && (rc = make_map(&mpart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, p.held_at / (kTileK * 4), kTileK,
+                                            kTileK, 32, "the parts", kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE))) ||
+            (a.boxes && (rc = make_map(&mdw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dw, n, K, a.ld_dw, 32, "dw", kBoxRows,
+                                       CU_TENSOR_MAP_SWIZZLE_NONE))))
             return rc;
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = allow_smem(k_weight_grad, kWgSmem, done);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", call, cudaGetErrorString(e));
         const int64_t items = p.whole + (int64_t)(p.tiles_k * p.tiles_n - p.whole) * p.splits;
         const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
-        const cudaError_t le = launch_after(k_weight_grad, dim3(grid), kWgThreads, kWgSmem, st, mdy, mx, mpart, a);
+        const cudaError_t le = launch_after(k_weight_grad, dim3(grid), kWgThreads, kWgSmem, st, mdy, mx, mpart, mdw, a);
         if (le != cudaSuccess) return pdl_fail(le, "weight gradient launch");
         z1_note_launch(reinterpret_cast<const void *>(k_weight_grad), grid, 1, kWgThreads, 0);
         if (p.splits == 1) return ZERO1_OK;

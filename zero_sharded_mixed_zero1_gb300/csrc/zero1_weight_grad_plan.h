@@ -16,11 +16,12 @@ constexpr int kTileK = 256, kTileN = 256;     // of a pair of CTAs
 constexpr int kDeep = 64;                     // rows of the contraction per stage
 constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time
 
-// A call's tiles, which of them are split along the rows, and where the
-// partial sums and the aligned copy lie in the workspace.
+// A call's tiles and which of them are split along the rows.  The workspace
+// holds the split tiles' parts, the sums that whole tiles hold between runs (one
+// tile per pair of CTAs), and the aligned copy of dy.
 struct Plan {
     int tiles_k, tiles_n, kblocks, clusters, whole, splits, per_split;
-    int64_t ld_copy, copy_at, bytes;
+    int64_t ld_copy, held_at, copy_at, bytes;
 };
 
 // The pairs of CTAs take the tiles in rounds; what a last, partial round would
@@ -52,6 +53,9 @@ inline void split_rest(Plan *p)
     }
     if (p->splits == 1) p->whole = tiles;
 }
+
+// Whether a whole tile may take more than one run of the accumulator.
+inline bool holds_sums(const Plan &p) { return p.whole > 0 && p.kblocks > kRunF32; }
 
 // The tiles whose parts one launch of the joining kernel adds: from `tile` on,
 // their sums `part` values into the partial sums.  A grid holds at most
