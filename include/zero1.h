@@ -555,7 +555,8 @@ int zero1_checksum(const void *data, int64_t nbytes, uint64_t *out, zero1_stream
  *    one row to the next; columns are contiguous.  Outputs need ld >= columns;
  *    inputs may have any ld >= 0 (0: the same row again).  With one row ld is
  *    not used.  Rows of 16-byte aligned bases and strides, with columns a
- *    multiple of 8, take the 128-bit path; anything else runs per element.
+ *    multiple of 8, move in 128-bit accesses; any others in 4-byte words or
+ *    element by element.
  *  - dtype codes: ZERO1_DTYPE_BF16 or ZERO1_DTYPE_F32.  Arithmetic, statistics
  *    and sums are fp32 (fused multiply-adds allowed here, unlike the optimizer
  *    step); each output is rounded once, when it is stored.

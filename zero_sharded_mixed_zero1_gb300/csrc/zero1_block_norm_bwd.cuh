@@ -14,7 +14,7 @@ namespace {
 // block visits (in registers, or in shared memory where a row takes 1024
 // threads and registers are short); a second kernel adds the blocks' sums in
 // block order.  This direct kernel takes the rows that do not fit the ring of
-// the staged one below: above 8192 columns, and wide fp32 rows.
+// the staged one below (which ones: at the choice of kernel there).
 
 template <class TA, class TR, bool VEC, bool SACC>
 __global__ void __launch_bounds__(SACC ? 1024 : 512) k_block_norm_bwd(const Common c, const Bwd a)
@@ -449,7 +449,8 @@ int direct_bwd(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st)
 }
 
 // One resident wave of staged blocks (`grid`); false, with nothing launched, if
-// a row does not fit.
+// a row does not fit: two stages, which are sized for 8 C T columns and, but for
+// SAVED = 1, for tensors, beside two or three vectors of as many fp32 values.
 template <class TA, class TR, int T, int C, int GATE, int SAVED, bool FULL, bool AL>
 bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t st, int *rc)
 {
@@ -472,6 +473,24 @@ bool launch_bwd_staged(const Common &c, const Bwd &a, int64_t grid, cudaStream_t
     return true;
 }
 
+// The mixes in use are compiled apart (SAVED) for rows of exactly 8 C T columns,
+// 256 to 8192 in powers of two; any other row takes the run-time mix.  us on the
+// device, compiled apart and as a run-time mix, 33.6 million bf16 elements,
+// without a gate and with a channel gate:
+//   columns   from checkpoints         from tensors
+//   1024      66 / 83    69 / 87       74 / 84    75 / 88
+//   2048      67 / 72    69 / 198      76 / 73   154 / 154
+//   4096      67 / 73    71 / 104      73 / 72    74 / 105
+//   8192      75 / 71    68 / 210      70 / 73    72 / 167
+// The long times are rows that do not fit the ring and run on the direct kernel:
+//   - above 8192 columns, all (398 to 654);
+//   - at 1025 to 2048 and 4097 to 8192 columns: bf16 with a channel or full gate
+//     (5120: 293 from checkpoints, 221 from tensors; without a gate 90) but for
+//     the mixes compiled apart at 2048 (checkpoints) and 8192 columns; an fp32
+//     residual stream or fp32 activations (353 to 506) but for 2048 and 8192 columns
+//     from checkpoints with bf16 activations and without such a gate (83, 85); and
+//     rows off the 128-bit path;
+//   - up to 256 columns, fp32 activations off the 128-bit path with a full fp32 gate.
 template <class TA, class TR>
 bool backward_staged(const Common &c, const Bwd &a, bool vec, int64_t grid, cudaStream_t st, int *rc)
 {

@@ -12,7 +12,11 @@ namespace {
 // r, h and the checkpoints are written once: 10 bytes per bf16 element with
 // both checkpoints, 8 without.  HBM is the bound.  This direct kernel takes
 // the rows that do not fit the ring of the staged one below: above 8192
-// columns, and wide fp32 rows.
+// columns (94 to 111 us for 33.6 million bf16 elements with checkpoints, where
+// the ring takes 57 to 67 up to 4096 and at 8192), at 1025 to 2048 columns fp32
+// activations with a channel or full gate and an fp32 residual stream with a
+// full fp32 gate, and from 4097 on those of them that are off the 128-bit path
+// or have a full fp32 gate beside fp32 activations.
 
 template <class TA, class TR, bool VEC>
 __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const Fwd a)
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(1024) k_block_norm_fwd(const Common c, const F
 
 // ------------------------------------------------------- staged forward ----
 //
-// Measured on GB300 with both checkpoints, bf16: 8192 x 4096 58 us (5.75 TB/s of
+// Measured on GB300 with both checkpoints, bf16: 8192 x 4096 59 us (5.7 TB/s of
 // the 10 bytes per element, 0.85 of the measured copy rate; the direct kernel
 // took 75), 32768 x 768 with an fp32 residual stream 54 us (0.83).  What is
 // lost is the first rows' latency and, with 16 warps per SM, the waits for
@@ -246,6 +250,15 @@ bool launch_fwd_staged(const Common &c, const Fwd &a, int sms, cudaStream_t st, 
     return true;
 }
 
+// The mixes in use are compiled apart (KEPT) for rows of exactly 8 C T columns; any
+// other row takes the run-time mix.  us on the device, compiled apart and as a
+// run-time mix, 33.6 million bf16 elements, without a gate and with a channel
+// gate:
+//   columns   with checkpoints         without
+//   1024      56 / 69    60 / 69       44 / 51    45 / 52
+//   2048      60 / 56    60 / 58       48 / 48    48 / 46
+//   4096      57 / 58    58 / 62       46 / 46    45 / 44
+//   8192      63 / 61    67 / 65       43 / 43    48 / 48
 template <class TA, class TR>
 bool forward_staged(const Common &c, const Fwd &a, bool vec, int sms, cudaStream_t st, int *rc)
 {

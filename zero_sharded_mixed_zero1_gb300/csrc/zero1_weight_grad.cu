@@ -18,7 +18,7 @@ using namespace z1wg;
 // which is the layout the MMA reads for its B operand.  x8 becomes the A
 // operand: a code is 8 bits of a bf16 (sign, exponent, mantissa) 120 binades
 // too low, so shifting it into place and multiplying by 2^(e + 120) gives the
-// exact value; eight warps do that for 16-bit pairs of rows and write A into
+// exact value; sixteen warps do that for 16-bit pairs of rows and write A into
 // tensor memory, where it needs no second pass through shared memory.  A
 // checkpoint block is 128 columns, which is one CTA's share of the tile, so
 // each row has one scale per CTA.
@@ -29,8 +29,8 @@ using namespace z1wg;
 // fp32; sums are fp32 in the accumulator.
 //
 // Measured on GB300: 14336 x 4096 outputs over 8192 rows 509 us in a burst (1890
-// TFLOP/s, 0.96 of the measured cuBLAS rate for a plain bf16 product), 4096 x
-// 4096 154 us (1790).  A stage takes about 575 cycles where its MMAs need 512,
+// TFLOP/s, 0.96 of the measured cuBLAS rate for a plain bf16 product; 550 in a
+// long loop), 4096 x 4096 148 to 150 us (1840).  A stage takes about 575 cycles where its MMAs need 512,
 // the converting warps 260 on the integer pipe; what is left is the start and
 // end of each tile and, over seconds, the power limit.  Steps on the way: one
 // ring for codes and dy, releases at cluster scope and the timer read in every
@@ -41,7 +41,7 @@ using namespace z1wg;
 // the number of additions: 2e-7 of a gradient's norm over 777 rows, 1.5e-6 over
 // 4096, 9e-6 over 16384.  For bf16 results that is nothing; for fp32 ones the
 // accumulator is emptied every 2048 rows and the runs are added in fp32 (6e-7
-// over 16384 rows; 4096 x 4096 over 8192 rows 192 us against 163 in one run:
+// over 16384 rows; 4096 x 4096 over 8192 rows 191 to 200 us where bf16 takes 150:
 // the MMAs stop for some 5000 cycles each time).
 //
 // Roles (28 warps): warp 0 loads dy and warp 3 the codes, warp 1 of the
