@@ -74,6 +74,43 @@ __device__ __forceinline__ float ld_param(const void *p, int f32, int64_t i)
     return f32 ? __ldg(static_cast<const float *>(p) + i) : bf_one(__ldg(static_cast<const uint16_t *>(p) + i));
 }
 
+// ------------------------------------------------------ logistic function --
+
+// exp(-a) for a >= 0 to 2.5 ulps (and through the subnormal numbers, NaN for
+// NaN; USUAL: a is at most 87, where the result is a normal number): 2^t by the
+// hardware's 2-ulp instruction, t = -a log2(e) rounded, times 1 + r ln 2 for the
+// rest r of that product, which a fused multiply-add gives exactly and log2(e)'s
+// own lower part completes.  Without r the error grows with a: 100 ulps at 80.
+template <bool USUAL = false>
+__device__ __forceinline__ float exp_minus(float a)
+{
+    constexpr float kLog2e = 1.44269502f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147182f;
+    if (!USUAL) asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(200.f));  // an infinity would have no rest
+    const float t = __fmul_rn(-a, kLog2e);
+    const float r = __fmaf_rn(-a, kLog2eLow, __fmaf_rn(-a, kLog2e, -t));
+    float e;
+    if (USUAL) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    else asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(t));
+    return __fmaf_rn(e, __fmul_rn(r, kLn2), e);
+}
+
+// s = 1 / (1 + exp(-x)) and its slope s (1 - s), both from e = exp(-|x|) and 1 +
+// e, which is between 1 and 2: s = 1 / (1 + e) or e / (1 + e), slope = e / (1 +
+// e)^2, within 16 half ulps at every x.  1 - s would lose every bit where s
+// rounds to 1.
+template <bool USUAL = false>
+struct Logistic {
+    float s, slope;
+    __device__ __forceinline__ explicit Logistic(float x)
+    {
+        const float e = exp_minus<USUAL>(fabsf(x));
+        float q;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));  // 1 ulp
+        const float t = e * q;
+        s = x >= 0.f ? q : t;
+        slope = t * q;
+    }
+};
 // -------------------------------------------------- 8-bit checkpoint code --
 
 // Largest magnitude seen, as the bits of |x|: integer order is the order of

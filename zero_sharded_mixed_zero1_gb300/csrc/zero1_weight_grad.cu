@@ -1,10 +1,7 @@
 // zero1_weight_grad.cu - the weight gradient of a projection, taken straight
 // from the 8-bit checkpoint of its input, on the tensor cores.
 
-#include <cuda.h>
-
-#include "zero1_async.cuh"
-#include "zero1_block.cuh"
+#include "zero1_tensor.cuh"
 #include "zero1_weight_grad_plan.h"
 
 namespace {
@@ -60,7 +57,7 @@ constexpr int kSets = 4;                   // of four converting warps
 // the first for the one it waits for.
 static_assert(kStages % kSets == 0 && kCodeStages % kSets == 0, "a place belongs to one set");
 constexpr int kWgThreads = 32 * (4 + 4 * kSets + 8);
-constexpr uint32_t kTmemCols = 512, kTmemA = 256, kTmemAStage = kDeep / 2;
+constexpr uint32_t kTmemA = 256, kTmemAStage = kDeep / 2;
 
 struct WgBars {
     uint64_t full[kStages], empty[kStages], cfull[kCodeStages], cempty[kCodeStages], dfull, dempty;
@@ -95,35 +92,12 @@ struct Wg {
 
 // ------------------------------------------------------------- tcgen05 -----
 
-__device__ __forceinline__ void tc_alloc(uint32_t *slot)
-{
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-}
-__device__ __forceinline__ void tc_free(uint32_t base)
-{
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(kTmemCols));
-}
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // D (both CTAs' tensor memory) (+)= A (tensor memory) * B (shared memory).
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add)
 {
     asm volatile(
         "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(add)
-        : "memory");
-}
-
-// Arrive on this barrier of both CTAs when the MMAs issued so far are done.
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
         : "memory");
 }
 
@@ -136,31 +110,6 @@ __device__ __forceinline__ void tc_store(uint32_t addr, const uint32_t r[8])
                  : "memory");
 }
 __device__ __forceinline__ void tc_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// 32 accumulator columns of this thread's lane.
-__device__ __forceinline__ void tc_load32(uint32_t addr, uint32_t r[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tc_load16(uint32_t addr, uint32_t r[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-        "[%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 
 // Descriptor of a B tile: 128-byte swizzle, 64 columns x kDeep rows per TMA
 // box (kDeep * 128 bytes from one 64-column group to the next), 8 rows per
@@ -175,79 +124,6 @@ __device__ __forceinline__ uint64_t b_desc(uint32_t addr)
 // memory, M = 256 (both CTAs), N = 256.
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(kTileN / 8) << 17) |
                             ((uint32_t)(kTileK / 16) << 24);
-
-// ------------------------------------------------------------- clusters ----
-
-__device__ __forceinline__ uint32_t cta_rank()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Arrive on the leading CTA's copy of a barrier.
-__device__ __forceinline__ void arrive_leader(uint64_t *bar)
-{
-    asm volatile(
-        "{ .reg .b32 a; mapa.shared::cluster.u32 a, %0, 0; mbarrier.arrive.shared::cluster.b64 _, [a]; }" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
-
-// The same place in the shared memory of the pair's CTA `rank`.
-__device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-__device__ __forceinline__ uint32_t read_rank(const uint32_t *p, uint32_t rank)
-{
-    uint32_t x;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at_rank(p, rank)) : "memory");
-    return x;
-}
-
-// A bounded wait of a whole warp; one that runs out is noted in both CTAs.
-__device__ __forceinline__ bool warp_wait(WgBars &b, uint64_t *bar, uint32_t parity)
-{
-    if (__all_sync(0xffffffffu, mbar_wait_long(bar, parity))) return true;
-    if ((threadIdx.x & 31) < 2)
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at_rank(&b.failed, threadIdx.x & 31)), "r"(1u) : "memory");
-    __syncwarp();
-    return false;
-}
-
-// The leading CTA's copy of a barrier, as a cluster address.
-__device__ __forceinline__ uint32_t leader_addr(uint64_t *bar)
-{
-    uint32_t a;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
-    return a;
-}
-
-// A box into this CTA's shared memory, counted on the leading CTA's barrier.
-__device__ __forceinline__ void tma_2d_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
 
 // ----------------------------------------------------------- conversion ----
 
@@ -494,21 +370,6 @@ __device__ __forceinline__ void add_f32_any(float *o, int64_t ld, int rows, bool
     }
 }
 
-// A box from shared memory, added to what is there or written, and a group of
-// its own.  (These reductions keep subnormal values, measured.)
-__device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bool add, const uint32_t *place)
-{
-    if (add)
-        asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
-                     "r"(x), "r"(y), "r"(smem_u32(place))
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
-                     "r"(y), "r"(smem_u32(place))
-                     : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 // 32 lanes x 128 rows as boxes of 32 columns x kBoxRows rows, copied or added
 // from the warp's two places in shared memory: no trade between lanes, a
 // quarter of the instructions, and nothing to wait for.  rows: how many of the
@@ -536,13 +397,6 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap *map, int x, int y
         __syncwarp();
         at = at + 1 == kPlaces ? 0 : at + 1;
     }
-}
-
-// All boxes that this warp has sent are written.
-__device__ __forceinline__ void boxes_written()
-{
-    if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgThreads, 1)
@@ -859,56 +713,7 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
     }
 }
 
-// Copies dy to rows that start on 16-byte boundaries, eight elements per thread.
-__global__ void __launch_bounds__(256)
-k_align_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t T, int64_t N, uint16_t *__restrict__ dst, int64_t ld_dst)
-{
-    for (int64_t c = ((int64_t)blockIdx.y * 32 + threadIdx.x % 32) * 8; c < N; c += (int64_t)gridDim.y * 256)
-        for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; t < T; t += (int64_t)gridDim.x * 8)
-            *reinterpret_cast<uint4 *>(dst + t * ld_dst + c) = load8_any(src + t * ld, c, N, t * ld == 0);
-}
-
 // --------------------------------------------------------------- launch ----
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
-// A [rows, cols] matrix in boxes of box_x columns and box_y rows.
-int make_map(CUtensorMap *m, CUtensorMapDataType type, int es, const void *p, int64_t rows, int64_t cols, int64_t ld,
-             int box_x, const char *what, int box_y = kDeep, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
-{
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
-    const cuuint32_t box[2] = {(cuuint32_t)box_x, (cuuint32_t)box_y}, one[2] = {1, 1};
-    const EncodeTiled fn = encode_tiled();
-    if (!fn) return z1_fail(ZERO1_ECUDA, "weight gradient: the driver has no tensor maps");
-    const CUresult r = fn(m, type, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return z1_fail(ZERO1_ECUDA, "weight gradient: tensor map of %s: error %d", what, (int)r);
-    return ZERO1_OK;
-}
-
-bool rows_aligned(const void *dy, int64_t ld, int64_t rows)
-{
-    return (((uintptr_t)dy) & 15) == 0 && (rows <= 1 || (ld % 8 == 0 && ld > 0));
-}
 
 int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p)
 {
@@ -1016,12 +821,12 @@ extern "C" int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const
         a.boxes = a.out_f32 && ((uintptr_t)dw & 15) == 0 && a.ld_dw % 4 == 0 && K % 4 == 0 &&
                   a.ld_dw < (INT64_C(1) << 37);  // (a tensor map's strides are below 2^40 bytes)
         CUtensorMap mdy, mx, mpart{}, mdw{};
-        if ((rc = make_map(&mdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, src, T, n, ld, 64, "dy")) ||
-            (rc = make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
-                           "the codes")) ||
-            (p.splits > 1 && (rc = make_map(&mpart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, p.held_at / (kTileK * 4), kTileK,
+        if ((rc = make_map(call, &mdy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, src, T, n, ld, 64, "dy", kDeep)) ||
+            (rc = make_map(call, &mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, x8->codes, T, round_up(K, kQBlock), x8->ld_codes, kQBlock,
+                           "the codes", kDeep)) ||
+            (p.splits > 1 && (rc = make_map(call, &mpart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, p.held_at / (kTileK * 4), kTileK,
                                             kTileK, 32, "the parts", kBoxRows, CU_TENSOR_MAP_SWIZZLE_NONE))) ||
-            (a.boxes && (rc = make_map(&mdw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dw, n, K, a.ld_dw, 32, "dw", kBoxRows,
+            (a.boxes && (rc = make_map(call, &mdw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, dw, n, K, a.ld_dw, 32, "dw", kBoxRows,
                                        CU_TENSOR_MAP_SWIZZLE_NONE))))
             return rc;
         static std::atomic<uint64_t> done{0};
