@@ -695,6 +695,67 @@ int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const zero1_chec
                       int32_t scale_dtype, void *dw, int64_t ld_dw, int32_t out_dtype, int32_t accumulate,
                       void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block.  For rows h [rows, d_model] and weights w_gate,
+ * w_up [d_ff, d_model], all bf16:
+ *   g = h w_gate^T,  u = h w_up^T,  a = act(g) * u          [rows, d_ff]
+ * with act(g) = g s(k(g)), s the logistic function and k(g) = g
+ * (ZERO1_FFN_SILU) or 2 sqrt(2 / pi) (g + 0.044715 g^3) (ZERO1_FFN_GELU, the
+ * tanh form).  The down projection of a is a plain product and not part of this.
+ *  forward:     reads h, w_gate, w_up; writes a.  Both projections, the activation
+ *               and the product are one kernel; g and u are not kept.
+ *  backward:    reads da (the gradient of a) and h, w_gate, w_up again; writes
+ *               dg = da * u * act'(g) and du = da * act(g), and a if it is not NULL
+ *               (the down projection's weight gradient takes it, so that a need
+ *               not be kept either).  dg may be da (same pointer and stride).
+ *  input_grad:  reads dg, du, w_gate, w_up; writes dh = dg w_gate + du w_up, one
+ *               contraction over both, rounded once.
+ * The weights' gradients are dg^T h and du^T h: zero1_weight_grad from an 8-bit
+ * checkpoint of h's norm, or zero1_weight_grad_bf16 from h itself.
+ * Sums are fp32 on the tensor cores, whose additions truncate, in runs of at most
+ * 131072 terms (d_model is at most that: ERANGE); the activation takes g and u
+ * unrounded.  An Inf or NaN in a row of h reaches that row of the results.
+ * Buffers that a call does not name are not looked at.  Device memory only.
+ * Outputs must not overlap one another or an input.
+ * workspace: device, 128-byte aligned, at least zero1_gated_ffn_workspace bytes for
+ * the same arguments and call (scratch: partial sums where the contraction is
+ * split over blocks, and aligned copies of the inputs whose rows are not on 16-byte
+ * boundaries or whose width in the contraction is no multiple of 8).
+ * The kernels' waits are bounded (1 s each): should one run out, results are wrong
+ * although the call has returned ZERO1_OK, and bit 0 of the device status
+ * (zero1_device_status) says so. */
+#define ZERO1_FFN_SILU 0
+#define ZERO1_FFN_GELU 1
+#define ZERO1_FFN_FORWARD 0
+#define ZERO1_FFN_BACKWARD 1
+#define ZERO1_FFN_INPUT_GRAD 2
+typedef struct zero1_gated_ffn {
+    int64_t rows, d_model, d_ff;
+    const void *h, *w_gate, *w_up, *da;
+    void *a, *dg, *du, *dh; /* dg, du: read by input_grad */
+    int64_t ld_h, ld_w_gate, ld_w_up, ld_da, ld_a, ld_dg, ld_du, ld_dh;
+    int32_t act; /* ZERO1_FFN_SILU or ZERO1_FFN_GELU */
+} zero1_gated_ffn_t;
+int zero1_gated_ffn_workspace(const zero1_gated_ffn_t *ffn, int32_t call, int64_t *bytes);
+int zero1_gated_ffn_forward(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
+int zero1_gated_ffn_backward(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
+int zero1_gated_ffn_input_grad(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
+
+/* The weight gradient of a projection p = x W^T from bf16 activations:
+ *   dw[n, k] (+)= sum_t dy[t, n] * x[t, k]
+ * dy: device bf16 [rows, n]; x: device bf16 [rows, k]; dw: device [n, k] of
+ * out_dtype, for instance a view into a replica's flat gradient buffer at any
+ * element offset; accumulate != 0 adds the fp32 sum to it, with one rounding.  The
+ * sums are fp32 on the tensor cores, in runs of 2048 rows that are added in fp32
+ * for an fp32 dw, of 131072 rows for a bf16 one.  Without rows dw gets +0 (or stays,
+ * when accumulated into).  Device memory only; dw must not overlap dy or x.  workspace and
+ * waits as above (zero1_weight_grad_bf16_workspace bytes). */
+int zero1_weight_grad_bf16_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy, const void *x,
+                                     int64_t ld_x, int32_t out_dtype, int64_t *bytes);
+int zero1_weight_grad_bf16(const void *dy, int64_t ld_dy, int64_t n, const void *x, int64_t ld_x, int64_t k, int64_t rows,
+                           void *dw, int64_t ld_dw, int32_t out_dtype, int32_t accumulate, void *workspace,
+                           int64_t workspace_bytes, zero1_stream_t stream);
+
 /* Text of a status code. */
 const char *zero1_strerror(int code);
 

@@ -62,3 +62,11 @@ from .block import (  # noqa: E402,F401
     zero1_weight_grad,
     zero1_weight_grad_workspace,
 )
+from .ffn import (  # noqa: E402,F401
+    zero1_gated_ffn_backward,
+    zero1_gated_ffn_forward,
+    zero1_gated_ffn_input_grad,
+    zero1_gated_ffn_workspace,
+    zero1_weight_grad_bf16,
+    zero1_weight_grad_bf16_workspace,
+)

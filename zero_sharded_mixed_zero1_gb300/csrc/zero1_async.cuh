@@ -10,9 +10,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-// The status word of the weight-gradient kernel's source (a cudaError_t as int),
-// part of what zero1_device_status reports.
+// The status words of the tensor-core kernels' sources (a cudaError_t as int),
+// parts of what zero1_device_status reports.
 int z1_weight_grad_status(uint32_t *status, int32_t clear);
+int z1_gated_ffn_status(uint32_t *status, int32_t clear);
 
 namespace {
 

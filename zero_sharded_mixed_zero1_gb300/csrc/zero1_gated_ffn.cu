@@ -1,0 +1,1030 @@
+// zero1_gated_ffn.cu - the gated feed-forward block on the tensor cores: both
+// projections with the activation and the product in one kernel, its backward
+// pass with the pre-activations computed again, the gradient of its input, and
+// weight gradients from bf16 activations.
+
+#include "zero1_gemm_plan.h"
+#include "zero1_tensor.cuh"
+
+namespace {
+
+using namespace z1mm;
+
+// Four products share one kernel (T rows, D the block's width, F its inner one):
+//   kForward    g = h Wg^T, u = h Wu^T;  a = act(g) u
+//   kBackward   the same g and u;  dg = da u act'(g), du = da act(g), a if wanted
+//   kInputGrad  dh = dg Wg + du Wu, one contraction over 2 F
+//   kWeightGrad dw (+)= dy^T x, contracted over T
+// Two CTAs share a tile of 256 rows x 256 columns (or 128, where that fills the
+// pairs better): each loads 128 rows of A and half of B's columns by TMA into a
+// ring of swizzled shared memory, one thread issues the MMAs of the pair, and the
+// accumulator is kept twice in tensor memory, so that a tile is stored while the
+// next one is summed.  For the first two products B's two halves are rows of Wg
+// and of Wu: a thread that stores finds the g and the u of an element in its own
+// lane of tensor memory.  Operands lie in shared memory as they do in device
+// memory, along the contraction (h, Wg, Wu, dg) or across it (the weights of
+// kInputGrad, both operands of kWeightGrad); the MMA reads either.
+//
+// Roles (12 warps): warp 0 loads, warp 1 of the leading CTA issues the MMAs,
+// warp 2 keeps the tensor memory, warps 4-11 store, each 32 rows and half of the
+// tile's columns.
+
+constexpr int kForward = 0, kBackward = 1, kInputGrad = 2, kWeightGrad = 3;
+
+constexpr int kThreads = 32 * 12, kStoring = 8;  // storing warps
+constexpr int kABytes = 128 * kDeep * 2;
+constexpr int kRingBytes = 6 * (kABytes + 128 * kDeep * 2);
+template <int TN>
+constexpr int kStageBytes = kABytes + TN / 2 * kDeep * 2;
+template <int TN>
+constexpr int kStages = kRingBytes / kStageBytes<TN>;
+
+constexpr int kPlaceBytes = 32 * 64;  // 32 rows of 64 bytes, swizzled, on their way out
+constexpr int kPlaces = 2;            // of each storing warp
+
+struct Bars {
+    uint64_t full[8], empty[8], dfull[2], dempty[2];
+    uint32_t tmem;
+    uint32_t failed;       // a wait of either CTA ran out
+    uint32_t loads, mmas;  // stages loaded and issued
+    uint32_t fills;        // accumulator fills issued
+};
+constexpr int kSmem = 1024 + kRingBytes + kStoring * kPlaces * kPlaceBytes + (int)sizeof(Bars);
+static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+static_assert(kStages<256> == 6 && kStages<128> == 8, "stages");
+
+struct Out {
+    void *p;
+    int64_t ld;
+    int boxes;  // stored in boxes by TMA
+};
+
+struct Mm {
+    int64_t M, N;                     // results: rows, columns (of a, or of the gradient)
+    int tiles_m, tiles_n, kblocks;    // kblocks: stages of the whole contraction
+    int second;                       // the stage from which kInputGrad reads du and Wu
+    int whole, splits, per_split, run;
+    int gelu;
+    const uint16_t *da;
+    int64_t ld_da;
+    int da_vec;                       // da in 128-bit loads
+    Out out[3];                       // kForward: a; kBackward: dg, du, a; the others: their gradient
+    int out_f32, accumulate;
+    float *part;                      // [split tile][part][slot][column][32 lanes]
+    float *held;                      // [CTA][storing warp][column][32 lanes]
+};
+
+__host__ __device__ constexpr bool dual(int kind) { return kind <= kBackward; }
+
+// ------------------------------------------------------------- operands ----
+
+// Shared-memory descriptor of an operand, 128-byte swizzle, 8 rows per
+// 1024-byte group.  Along the contraction: rows of 64 elements.  Across it: TMA
+// boxes of 64 elements x kDeep rows of the contraction, one behind the other.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool across)
+{
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(across ? (kDeep * 128) >> 4 : 1) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// From 16 elements of the contraction to the next.
+template <bool ACROSS>
+constexpr int kDescStep = (ACROSS ? 16 * 128 : 32) >> 4;
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(add)
+                 : "memory");
+}
+
+// fp32 accumulator, bf16 operands, M = 256 (both CTAs).
+template <int TN, bool A_ACROSS, bool B_ACROSS>
+constexpr uint32_t kInstr = (1u << 4) | (1u << 7) | (1u << 10) | ((A_ACROSS ? 1u : 0u) << 15) | ((B_ACROSS ? 1u : 0u) << 16) |
+                            ((uint32_t)(TN / 8) << 17) | ((uint32_t)(kTileM / 16) << 24);
+
+// ---------------------------------------------------------------- items ----
+
+struct Item {
+    int m, n, kb0, kb1, part;  // tile's row and column number; part: its place among the parts, -1 for a whole tile
+};
+
+// Tiles run in bands of eight along the rows, so that the pairs of CTAs at work
+// at one time share few rows of both operands (they meet in L2).
+__device__ __forceinline__ void tile_of(const Mm &a, int t, int &m, int &n)
+{
+    constexpr int kBand = 8;
+    const int per = kBand * a.tiles_n, band = t / per, in = t % per;
+    const int height = min(kBand, a.tiles_m - band * kBand);
+    m = band * kBand + in % height;
+    n = in / height;
+}
+
+// The whole tiles come first, then all first parts of the others, all second
+// ones and so on, so that neighbours in time share operands.
+__device__ __forceinline__ Item item_of(const Mm &a, int i)
+{
+    Item o;
+    o.part = -1;
+    o.kb0 = 0;
+    o.kb1 = a.kblocks;
+    int t = i;
+    if (i >= a.whole) {
+        const int rest = a.tiles_m * a.tiles_n - a.whole, p = (i - a.whole) / rest;
+        t = a.whole + (i - a.whole) % rest;
+        o.kb0 = p * a.per_split;
+        o.kb1 = min(o.kb0 + a.per_split, a.kblocks);
+        o.part = (t - a.whole) * a.splits + p;
+    }
+    tile_of(a, t, o.m, o.n);
+    return o;
+}
+
+__device__ __forceinline__ int items_of(const Mm &a) { return a.whole + (a.tiles_m * a.tiles_n - a.whole) * a.splits; }
+
+// ----------------------------------------------------------- activation ----
+
+// f = act(g) = g s(k(g)) and df = act'(g) = s + g s (1 - s) k'(g), s the logistic
+// function: silu has k(g) = g, the tanh form of gelu 2 sqrt(2 / pi) (g + 0.044715 g^3).
+struct Activated {
+    float f, df;
+    __device__ __forceinline__ Activated(float g, int gelu)
+    {
+        constexpr float kA = 1.5957691216f, kB = 0.0713548163f;  // 2 sqrt(2 / pi), 0.044715 of it
+        float k = g, dk = 1.f;
+        if (gelu) {
+            const float q = __fmul_rn(g, g);
+            k = __fmul_rn(g, __fmaf_rn(kB, q, kA));
+            dk = __fmaf_rn(3.f * kB, q, kA);
+        }
+        const Logistic<> l(k);
+        f = __fmul_rn(g, l.s);
+        df = __fmaf_rn(__fmul_rn(g, dk), l.slope, l.s);
+    }
+};
+
+// ------------------------------------------------------------- results -----
+
+// 16 bytes of a place: 64-byte rows, 16-byte pieces exchanged as TMA's 64-byte
+// swizzle does, which also keeps these stores off each other's banks.
+__device__ __forceinline__ unsigned char *piece(unsigned char *place, int row, int k)
+{
+    return place + row * 64 + ((k ^ ((row >> 1) & 3)) << 4);
+}
+
+// 32 rows x 64 bytes of results from a place: a box, or, off 16-byte boundaries
+// or to be added to, an element at a time.  rows, cols: how many of them lie
+// inside the matrix.
+struct Leaving {
+    unsigned char *places;  // of this warp
+    int at;
+
+    // Waits until the next place may be written.
+    __device__ __forceinline__ unsigned char *next()
+    {
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPlaces - 1) : "memory");
+        __syncwarp();
+        unsigned char *p = places + at * kPlaceBytes;
+        at = at + 1 == kPlaces ? 0 : at + 1;
+        return p;
+    }
+    // Every use of a place is a group, an empty one where nothing of it lies inside
+    // the matrix: next() counts them.
+    __device__ __forceinline__ void empty_group()
+    {
+        __syncwarp();
+        if (elect_one()) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        __syncwarp();
+    }
+    __device__ __forceinline__ void box(const CUtensorMap *map, int64_t row, int64_t col, bool inside, const unsigned char *place)
+    {
+        if (!inside) return empty_group();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (elect_one()) box_out(map, (int)col, (int)row, false, reinterpret_cast<const uint32_t *>(place));
+        __syncwarp();
+    }
+    template <class T>
+    __device__ __forceinline__ void elements(T *o, int64_t ld, int rows, int cols, bool add, unsigned char *place)
+    {
+        constexpr int kCols = 64 / (int)sizeof(T);  // one lane to an element of a row
+        const int lane = threadIdx.x & 31, c = lane % kCols;
+        __syncwarp();
+        if (c < cols) {
+#pragma unroll 4
+            for (int r = lane / kCols; r < rows; r += 32 / kCols) {
+                const T x = *reinterpret_cast<const T *>(piece(place, r, c * (int)sizeof(T) / 16) + c * sizeof(T) % 16);
+                T *q = o + r * ld + c;
+                if constexpr (sizeof(T) == 4) *q = add ? *q + x : x;
+                else *q = x;
+            }
+        }
+        empty_group();
+    }
+    // fp32 sums stored as bf16, or added to bf16 results, rounded once.
+    __device__ __forceinline__ void round_to(uint16_t *o, int64_t ld, int rows, int cols, bool add, unsigned char *place)
+    {
+        const int lane = threadIdx.x & 31, c = lane % 16;
+        __syncwarp();
+        if (c < cols) {
+#pragma unroll 4
+            for (int r = lane / 16; r < rows; r += 2) {
+                uint16_t *q = o + r * ld + c;
+                const float x = *reinterpret_cast<const float *>(piece(place, r, c / 4) + c % 4 * 4);
+                *q = to_bf16(add ? bf_one(*q) + x : x);
+            }
+        }
+        empty_group();
+    }
+};
+
+// 32 bf16 results of this thread's row, packed in pairs, from column `col` on.
+__device__ __forceinline__ void leave_bf16(Leaving &l, const Out &o, const CUtensorMap *map, int64_t row0, int64_t col, int rows,
+                                           int64_t N, const uint32_t x[16])
+{
+    unsigned char *place = l.next();
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4 *>(piece(place, lane, k)) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+    const int cols = (int)max((int64_t)0, min((int64_t)32, N - col));
+    if (o.boxes) {
+        l.box(map, row0, col, rows > 0 && cols > 0, place);
+    } else {
+        l.elements(static_cast<uint16_t *>(o.p) + row0 * o.ld + col, o.ld, rows, cols, false, place);
+    }
+}
+
+// 16 fp32 sums of this thread's row: stored, or added to what is there, as fp32
+// or rounded to bf16.
+__device__ __forceinline__ void leave_f32(Leaving &l, const Mm &a, const CUtensorMap *map, int64_t row0, int64_t col, int rows,
+                                          const float x[16])
+{
+    const Out &o = a.out[0];
+    unsigned char *place = l.next();
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<float4 *>(piece(place, lane, k)) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+    const int cols = (int)max((int64_t)0, min((int64_t)16, a.N - col));
+    if (!a.out_f32)
+        l.round_to(static_cast<uint16_t *>(o.p) + row0 * o.ld + col, o.ld, rows, cols, a.accumulate != 0, place);
+    else if (a.accumulate || !o.boxes)
+        l.elements(static_cast<float *>(o.p) + row0 * o.ld + col, o.ld, rows, cols, a.accumulate != 0, place);
+    else l.box(map, row0, col, rows > 0 && cols > 0, place);
+}
+
+// The accumulator has been read: it may be filled again.
+__device__ __forceinline__ void release(uint64_t *dempty)
+{
+    tc_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) arrive_leader(dempty);
+}
+
+// Sums that wait in the workspace, 32 lanes side by side: stored, or added to.
+// No other thread touches them.
+__device__ __forceinline__ void hold(float *p, bool begin, int columns, uint32_t acc, uint64_t *dempty)
+{
+#pragma unroll 1
+    for (int c = 0; c < columns; c += 16) {
+        uint32_t v[16];
+        tc_load16(acc + c, v);
+        if (c + 16 == columns) release(dempty);
+        float old[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) old[j] = begin ? 0.f : __ldcg(p + (c + j) * 32);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) __stcg(p + (c + j) * 32, old[j] + __uint_as_float(v[j]));
+    }
+}
+
+// Eight bf16 values of da at a row and column, zeros outside.
+__device__ __forceinline__ uint4 load_da(const Mm &a, int64_t row, int64_t col)
+{
+    if (row >= a.M || col >= a.N) return make_uint4(0, 0, 0, 0);
+    const uint16_t *p = a.da + row * a.ld_da + col;
+    if (a.da_vec && col + 8 <= a.N) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = col + 2 * k < a.N ? p[2 * k] : 0, hi = col + 2 * k + 1 < a.N ? p[2 * k + 1] : 0;
+        w[k] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ----------------------------------------------------------------- kernel --
+
+struct Maps {
+    CUtensorMap a0, a1, b0, b1, out0, out1, out2;
+};
+
+template <int KIND, int TN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
+{
+    constexpr bool kDual = dual(KIND), kAAcross = KIND == kWeightGrad, kBAcross = KIND >= kInputGrad;
+    constexpr int S = kStages<TN>, kBytes = kStageBytes<TN>;
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    unsigned char *s_places = smem + kRingBytes;
+    Bars &bar = *reinterpret_cast<Bars *>(s_places + kStoring * kPlaces * kPlaceBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&bar.full[s], 1);
+            mbar_init(&bar.empty[s], 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&bar.dfull[k], 1);
+            mbar_init(&bar.dempty[k], 2 * kStoring);
+        }
+        bar.failed = bar.loads = bar.mmas = bar.fills = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tc_alloc(&bar.tmem);
+    tc_before();
+    __syncthreads();
+    cluster_sync();
+    tc_after();
+    wait_prior_grid();  // up to here this kernel may run beside the one before it
+    const uint32_t tmem = bar.tmem;
+    const int items = items_of(a);
+    const int first = blockIdx.x / 2, step = gridDim.x / 2;
+
+    if (warp == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        for (int i = first; i < items && ok; i += step) {
+            const Item w = item_of(a, i);
+            const int m = w.m * kTileM + (int)rank * 128;
+            const int n = kDual ? w.n * (TN / 2) : w.n * TN + (int)rank * (TN / 2);
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+                const uint32_t s = it % S;
+                if (it >= S && !(ok = warp_wait(bar, &bar.empty[s], (it / S - 1) & 1))) break;
+                unsigned char *pa = smem + s * kBytes, *pb = pa + kABytes;
+                const bool late = KIND == kInputGrad && kb >= a.second;
+                const int k = (late ? kb - a.second : kb) * kDeep;
+                const CUtensorMap *ma = late ? &maps.a1 : &maps.a0;
+                const CUtensorMap *mb = late || (kDual && rank) ? &maps.b1 : &maps.b0;
+                if (elect_one()) {
+                    // both CTAs' loads count on the leading CTA's barrier
+                    const uint32_t full = leader_addr(&bar.full[s]);
+                    if (rank == 0) mbar_expect_tx(&bar.full[s], 2 * kBytes);
+                    if (kAAcross) {
+                        tma_2d_pair(pa, ma, m, k, full);
+                        tma_2d_pair(pa + kABytes / 2, ma, m + 64, k, full);
+                    } else {
+                        tma_2d_pair(pa, ma, k, m, full);
+                    }
+                    if (kBAcross) {
+                        tma_2d_pair(pb, mb, n, k, full);
+                        if (TN == 256) tma_2d_pair(pb + 64 * kDeep * 2, mb, n + 64, k, full);
+                    } else {
+                        tma_2d_pair(pb, mb, k, n, full);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // the last copies must land before the pair may exit (both CTAs have as many)
+        if (rank == 0)
+            for (uint32_t q = it > S ? it - S : 0; q < it && ok; ++q)
+                ok = warp_wait(bar, &bar.full[q % S], (q / S) & 1);
+        if (lane == 0) bar.loads = it;
+    } else if (warp == 1) {
+        if (rank == 0) {
+            uint32_t it = 0, fill = 0, fills = 0;
+            bool ok = true;
+            const uint64_t a0 = operand_desc(smem_u32(smem), kAAcross), b0 = operand_desc(smem_u32(smem) + kABytes, kBAcross);
+            for (int i = first; i < items && ok; i += step) {
+                const Item w = item_of(a, i);
+                for (int kb = w.kb0; kb < w.kb1 && ok; ++fill) {
+                    const uint32_t buf = fill & 1;
+                    if (fill >= 2 && !(ok = warp_wait(bar, &bar.dempty[buf], ((fill >> 1) - 1) & 1))) break;
+                    const int start = kb, end = min(kb + a.run, w.kb1);
+                    for (; kb < end; ++kb, ++it) {
+                        const uint32_t s = it % S;
+                        const uint64_t da = a0 + (uint64_t)(s * (kBytes >> 4)), db = b0 + (uint64_t)(s * (kBytes >> 4));
+                        const uint32_t more = kb > start, acc = tmem + buf * TN;
+                        if (!(ok = warp_wait(bar, &bar.full[s], (it / S) & 1))) break;
+                        tc_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int j = 0; j < kDeep / 16; ++j)
+                                mma_pair(acc, da + j * kDescStep<kAAcross>, db + j * kDescStep<kBAcross>,
+                                         kInstr<TN, kAAcross, kBAcross>, j ? 1u : more);
+                            tc_commit(&bar.empty[s]);
+                            if (kb + 1 == end) tc_commit(&bar.dfull[buf]);
+                        }
+                        __syncwarp();
+                    }
+                    fills += ok;
+                }
+            }
+            // the MMAs must have finished with both CTAs' memory before the exit
+            if (it > 0) warp_wait(bar, &bar.empty[(it - 1) % S], ((it - 1) / S) & 1);
+            if (lane == 0) {
+                bar.mmas = it;
+                bar.fills = fills;
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp % 4, half = (warp - 4) / 4, slot = (int)rank * 8 + half * 4 + q;
+        constexpr int kCols = TN / 2, W = TN / 4;  // accumulator columns of a warp; results' columns where it has g and u
+        Leaving leaving{s_places + (warp - 4) * kPlaces * kPlaceBytes, 0};
+        float *const held = a.held + ((int64_t)(blockIdx.x / 2) * 16 + slot) * kCols * 32 + lane;
+        uint32_t fill = 0;
+        bool ok = true;
+        for (int i = first; i < items && ok; i += step) {
+            const Item w = item_of(a, i);
+            const int64_t row0 = (int64_t)w.m * kTileM + (int)rank * 128 + 32 * q;
+            const int rows = (int)max((int64_t)0, min((int64_t)32, a.M - row0));
+            float *const part = a.part + ((int64_t)w.part * 16 + slot) * kCols * 32 + lane;
+            if (kDual) {
+                const int64_t col0 = (int64_t)w.n * (TN / 2) + half * W;
+                uint4 da[KIND == kBackward ? W / 8 : 1];
+                if (KIND == kBackward && w.part < 0) {  // on their way while the products are summed
+#pragma unroll
+                    for (int k = 0; k < W / 8; ++k) da[KIND == kBackward ? k : 0] = load_da(a, row0 + lane, col0 + 8 * k);
+                }
+                if (!(ok = warp_wait(bar, &bar.dfull[fill & 1], (fill >> 1) & 1))) break;
+                tc_after();
+                uint64_t *dempty = &bar.dempty[fill & 1];
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (fill & 1) * TN + half * W;
+                ++fill;
+                if (w.part >= 0) {
+                    // (of a part, g's columns come first, then u's; the last call releases the accumulator)
+                    uint32_t v[16];
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 16) {
+                        tc_load16(acc + (c < W ? c : c - W + TN / 2), v);
+                        if (c + 16 == kCols) release(dempty);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) __stcg(part + (c + j) * 32, __uint_as_float(v[j]));
+                    }
+                    continue;
+                }
+#pragma unroll
+                for (int c = 0; c < W; c += 32) {
+                    uint32_t x[3][16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t g[16], u[16];
+                        tc_load16(acc + c + e, g);
+                        tc_load16(acc + TN / 2 + c + e, u);
+                        if (c + e + 16 == W) release(dempty);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const Activated f0(__uint_as_float(g[j]), a.gelu), f1(__uint_as_float(g[j + 1]), a.gelu);
+                            const float u0 = __uint_as_float(u[j]), u1 = __uint_as_float(u[j + 1]);
+                            const int at = (e + j) / 2;
+                            if (KIND == kForward) {
+                                x[0][at] = pack_bf16x2(__fmul_rn(f0.f, u0), __fmul_rn(f1.f, u1));
+                            } else {
+                                const uint4 d4 = da[KIND == kBackward ? (c + e + j) / 8 : 0];
+                                const uint32_t d = (j / 2) % 4 == 0 ? d4.x : (j / 2) % 4 == 1 ? d4.y : (j / 2) % 4 == 2 ? d4.z : d4.w;
+                                const float d0 = bf_lo(d), d1 = bf_hi(d);
+                                x[0][at] = pack_bf16x2(__fmul_rn(__fmul_rn(d0, u0), f0.df), __fmul_rn(__fmul_rn(d1, u1), f1.df));
+                                x[1][at] = pack_bf16x2(__fmul_rn(d0, f0.f), __fmul_rn(d1, f1.f));
+                                x[2][at] = pack_bf16x2(__fmul_rn(f0.f, u0), __fmul_rn(f1.f, u1));
+                            }
+                        }
+                    }
+                    leave_bf16(leaving, a.out[0], &maps.out0, row0, col0 + c, rows, a.N, x[0]);
+                    if (KIND == kBackward) {
+                        leave_bf16(leaving, a.out[1], &maps.out1, row0, col0 + c, rows, a.N, x[1]);
+                        if (a.out[2].p) leave_bf16(leaving, a.out[2], &maps.out2, row0, col0 + c, rows, a.N, x[2]);
+                    }
+                }
+                continue;
+            }
+            const int64_t col0 = (int64_t)w.n * TN + half * kCols;
+            for (int kb = w.kb0; kb < w.kb1; kb += a.run) {
+                if (!(ok = warp_wait(bar, &bar.dfull[fill & 1], (fill >> 1) & 1))) break;
+                tc_after();
+                uint64_t *dempty = &bar.dempty[fill & 1];
+                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (fill & 1) * TN + half * kCols;
+                ++fill;
+                const bool begin = kb == w.kb0, end = kb + a.run >= w.kb1;
+                if (w.part >= 0 || !end) {
+                    hold(w.part >= 0 ? part : held, begin, kCols, acc, dempty);
+                    continue;
+                }
+                if (!a.out_f32 && !a.accumulate && begin) {
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        uint32_t v[32], x[16];
+                        tc_load32(acc + c, v);
+                        if (c + 32 == kCols) release(dempty);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) x[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                        leave_bf16(leaving, a.out[0], &maps.out0, row0, col0 + c, rows, a.N, x);
+                    }
+                    continue;
+                }
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 16) {
+                    uint32_t v[16];
+                    float x[16];
+                    tc_load16(acc + c, v);
+                    if (c + 16 == kCols) release(dempty);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = begin ? 0.f : __ldcg(held + (c + j) * 32);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]);
+                    leave_f32(leaving, a, &maps.out0, row0, col0 + c, rows, x);
+                }
+            }
+        }
+        boxes_written();  // before the grid counts as done
+    }
+    __syncwarp();
+    __syncthreads();
+    cluster_sync();
+    // From here on neither CTA starts anything.  If no wait ran out, all that was
+    // started has finished (the waits above).  If one did, what is under way to
+    // either CTA's shared memory, or reads it, is waited for before the pair's
+    // memory is given back: the loads, by making up what their barriers lack, and
+    // the MMAs with the arrivals that follow them.
+    if (bar.failed) {
+        if (warp == 0 && rank == 0) {
+            const uint32_t mine = bar.loads, other = read_rank(&bar.loads, 1), n = max(mine, other);
+            for (uint32_t q = n > S ? n - S : 0; q < n; ++q) {
+                // a use is complete after the leading CTA's arrival and both CTAs' bytes
+                const bool announced = q < mine, there = q < other;
+                if (lane == 0)
+                    mbar_make_up(&bar.full[q % S], announced ? 0u : 1u, !announced && there ? kBytes : 0u,
+                                 announced && !there ? kBytes : 0u);
+                __syncwarp();
+                warp_wait(bar, &bar.full[q % S], (q / S) & 1);
+            }
+        } else if (warp == 1) {
+            const uint32_t m = read_rank(&bar.mmas, 0), f = read_rank(&bar.fills, 0);
+            if (m > 0) warp_wait(bar, &bar.empty[(m - 1) % S], ((m - 1) / S) & 1);
+            if (f > 0) warp_wait(bar, &bar.dfull[(f - 1) & 1], ((f - 1) >> 1) & 1);
+        }
+        __syncthreads();
+        cluster_sync();
+    }
+    if (warp == 2) {
+        tc_after();
+        tc_free(tmem);
+    }
+}
+
+// Adds a split tile's parts in order and finishes its results; with no parts at
+// all (nothing to contract) the sums are 0.  A block takes 32 rows x 32 columns of
+// a tile: sums with lanes along the rows, as they were written, results with lanes
+// along the columns.
+template <int KIND, int TN>
+__global__ void __launch_bounds__(256) k_gated_ffn_join(const Mm a)
+{
+    constexpr bool kDual = dual(KIND);
+    constexpr int kCols = TN / 2, W = kDual ? TN / 4 : TN / 2, kGroups = W / 32;  // results' columns of a warp
+    wait_prior_grid();
+    __shared__ float sum[kDual ? 2 : 1][32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int slot = blockIdx.x / kGroups, c0 = blockIdx.x % kGroups * 32;
+    const int rest = a.tiles_m * a.tiles_n - a.whole;
+    for (int t = blockIdx.y; t < rest; t += gridDim.y) {
+        int m, n;
+        tile_of(a, a.whole + t, m, n);
+        const int64_t row0 = (int64_t)m * kTileM + slot / 8 * 128 + slot % 4 * 32;
+        const int64_t col0 = (int64_t)n * (kDual ? TN / 2 : TN) + slot / 4 % 2 * W + c0;
+        __syncthreads();  // what the tile before left has been read
+        if (row0 >= a.M || col0 >= a.N) continue;
+#pragma unroll
+        for (int k = 0; k < (kDual ? 8 : 4); ++k) {
+            const int set = k / 4, c = warp * 4 + k % 4;
+            const float *p = a.part + (((int64_t)t * a.splits * 16 + slot) * kCols + set * W + c0 + c) * 32 + lane;
+            float x = 0.f;
+#pragma unroll 4
+            for (int s = 0; s < a.splits; ++s) x += __ldcg(p + (int64_t)s * 16 * kCols * 32);
+            sum[set][c][lane] = x;
+        }
+        __syncthreads();
+        const int64_t col = col0 + lane;
+        if (col >= a.N) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int r = warp * 4 + k;
+            const int64_t row = row0 + r;
+            if (row >= a.M) continue;
+            if (kDual) {
+                const Activated f(sum[0][lane][r], a.gelu);
+                const float u = sum[kDual ? 1 : 0][lane][r];
+                const uint16_t y = to_bf16(__fmul_rn(f.f, u));
+                if (KIND == kForward) {
+                    static_cast<uint16_t *>(a.out[0].p)[row * a.out[0].ld + col] = y;
+                } else {
+                    const float d = bf_one(a.da[row * a.ld_da + col]);
+                    static_cast<uint16_t *>(a.out[0].p)[row * a.out[0].ld + col] = to_bf16(__fmul_rn(__fmul_rn(d, u), f.df));
+                    static_cast<uint16_t *>(a.out[1].p)[row * a.out[1].ld + col] = to_bf16(__fmul_rn(d, f.f));
+                    if (a.out[2].p) static_cast<uint16_t *>(a.out[2].p)[row * a.out[2].ld + col] = y;
+                }
+            } else {
+                const float x = sum[0][lane][r];
+                const int64_t at = row * a.out[0].ld + col;
+                if (a.out_f32) {
+                    float *o = static_cast<float *>(a.out[0].p) + at;
+                    *o = a.accumulate ? *o + x : x;
+                } else {
+                    uint16_t *o = static_cast<uint16_t *>(a.out[0].p) + at;
+                    *o = to_bf16(a.accumulate ? bf_one(*o) + x : x);
+                }
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- launch ----
+
+// An operand as a product takes it.
+struct Operand {
+    const void *p;
+    int64_t rows, cols, ld;
+    bool across;  // the contraction runs over the rows
+    const char *what;
+};
+
+// Rows that TMA can address as they are.  Along the contraction their width is a
+// multiple of eight elements too: what a box takes beyond the last column has to
+// be zero.
+bool usable(const Operand &o)
+{
+    return rows_aligned(o.p, o.ld, o.rows) && (o.across || o.cols % 8 == 0) && (o.rows <= 1 || o.ld < (INT64_C(1) << 38));
+}
+
+int64_t copy_bytes(const Operand &o) { return usable(o) ? 0 : round_up(o.rows * round_up(o.cols, 8) * 2, 128); }
+
+// One product: its plan, and the workspace's bytes with the operands' copies.
+struct Call {
+    const char *name;
+    int kind;
+    int64_t M, N, K;  // K: the contraction, of one of kInputGrad's two halves
+    Operand a[2], b[2];
+    int na, nb;
+    int run;
+    Plan plan;
+    int64_t bytes;
+};
+
+int plan_call(Call *c)
+{
+    if (c->M > INT32_MAX - 256 || c->N > INT32_MAX / 2 - 256 || c->K > INT32_MAX / 2 - 256)
+        return z1_fail(ZERO1_ERANGE, "%s: %lld x %lld x %lld: size not supported", c->name, (long long)c->M, (long long)c->N,
+                       (long long)c->K);
+    const int sms = sm_count();
+    if (sms == 0) return z1_fail(ZERO1_ECUDA, "%s: no CUDA device", c->name);
+    if (dual(c->kind) && c->K > (int64_t)kRunBf16 * kDeep)
+        return z1_fail(ZERO1_ERANGE, "%s: a width of %lld (at most %d)", c->name, (long long)c->K, kRunBf16 * kDeep);
+    const int64_t stages = (c->K + kDeep - 1) / kDeep * (c->kind == kInputGrad ? 2 : 1);
+    const int64_t N = dual(c->kind) ? 2 * c->N : c->N;
+    if ((c->M + 255) / 256 * ((N + 127) / 128) > (1 << 24))
+        return z1_fail(ZERO1_ERANGE, "%s: %lld x %lld results: size not supported", c->name, (long long)c->M, (long long)c->N);
+    c->plan = plan_of(c->M, N, (int)stages, sms / 2, c->run);
+    c->bytes = c->plan.bytes;
+    for (int k = 0; k < c->na; ++k) c->bytes += copy_bytes(c->a[k]);
+    for (int k = 0; k < c->nb; ++k) c->bytes += copy_bytes(c->b[k]);
+    return ZERO1_OK;
+}
+
+int check_workspace(const Call &c, const void *workspace, int64_t bytes, const Mat *mats, int n)
+{
+    if (c.bytes == 0) return ZERO1_OK;
+    if (!workspace || bytes < c.bytes)
+        return z1_fail(ZERO1_EINVAL, "%s: workspace of %lld bytes, needs %lld", c.name, (long long)(workspace ? bytes : 0),
+                       (long long)c.bytes);
+    if ((uintptr_t)workspace & 127) return z1_fail(ZERO1_EALIGN, "%s: the workspace is not 128-byte aligned", c.name);
+    const Mat w{workspace, 1, c.bytes, c.bytes, "the workspace"};
+    for (int k = 0; k < n; ++k)
+        if (mats_overlap(w, mats[k])) return z1_fail(ZERO1_EINVAL, "%s: the workspace and %s overlap", c.name, mats[k].what);
+    if (in_host_memory(workspace)) return z1_fail(ZERO1_EINVAL, "%s: the workspace must be device memory", c.name);
+    return ZERO1_OK;
+}
+
+int check_device(const char *call, const Mat *mats, int n)
+{
+    for (int k = 0; k < n; ++k)
+        if (mats[k].p && mats[k].rows > 0 && in_host_memory(mats[k].p))
+            return z1_fail(ZERO1_EINVAL, "%s: %s must be device memory", call, mats[k].what);
+    return ZERO1_OK;
+}
+
+// The map of an operand, of a copy of it in the workspace if need be.
+int operand_map(const Call &c, const Operand &o, int box_rows, char **scratch, CUtensorMap *map, cudaStream_t st)
+{
+    const void *p = o.p;
+    int64_t ld = o.rows > 1 ? o.ld : round_up(o.cols, 8), cols = o.cols;
+    if (!usable(o)) {
+        uint16_t *copy = reinterpret_cast<uint16_t *>(*scratch);
+        *scratch += copy_bytes(o);
+        const int64_t wide = round_up(o.cols, 8);
+        const dim3 grid((unsigned)(o.rows < 32768 ? (o.rows + 7) / 8 : 4096), (unsigned)(wide < 256 * 65535 ? (wide + 255) / 256 : 65535));
+        k_align_rows<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(o.p), o.rows > 1 ? o.ld : 0, o.rows, o.cols, copy, wide);
+        const int rc = launch_status("gated feed-forward: aligned copy");
+        if (rc != ZERO1_OK) return rc;
+        p = copy;
+        ld = cols = wide;
+    }
+    return make_map(c.name, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, o.rows, cols, ld, 64, o.what, box_rows);
+}
+
+int out_map(const Call &c, const Out &o, int64_t M, int64_t N, bool f32, CUtensorMap *map, const char *what)
+{
+    if (!o.p || !o.boxes) return ZERO1_OK;
+    return make_map(c.name, map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2, o.p, M, N,
+                    o.ld, f32 ? 16 : 32, what, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// A result matrix; boxes where its rows start on 16-byte boundaries and end on one
+// (a box is clipped by 16 bytes).
+Out out_of(const Mat &m, int es)
+{
+    Out o{const_cast<void *>(m.p), m.pitch / es, 0};
+    o.boxes = m.p && (((uintptr_t)m.p | (uintptr_t)m.pitch | (uintptr_t)m.width) & 15) == 0 && m.pitch < (INT64_C(1) << 39);
+    return o;
+}
+
+template <int KIND, int TN>
+int launch(const Call &c, Mm &a, void *workspace, cudaStream_t st)
+{
+    auto kernel = k_gated_ffn<KIND, TN>;
+    const Plan &p = c.plan;
+    a.M = c.M; a.N = c.N;
+    a.tiles_m = p.tiles_m; a.tiles_n = p.tiles_n; a.kblocks = p.kblocks;
+    a.second = p.kblocks / 2;
+    a.whole = p.whole; a.splits = p.splits; a.per_split = p.per_split;
+    a.run = c.run;
+    a.part = static_cast<float *>(workspace);
+    a.held = workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + p.held_at) : nullptr;
+    int rc;
+    if (p.kblocks > 0) {
+        Maps maps{};
+        char *scratch = static_cast<char *>(workspace) + p.bytes;
+        for (int k = 0; k < c.na; ++k)
+            if ((rc = operand_map(c, c.a[k], c.a[k].across ? kDeep : 128, &scratch, k ? &maps.a1 : &maps.a0, st))) return rc;
+        for (int k = 0; k < c.nb; ++k)
+            if ((rc = operand_map(c, c.b[k], c.b[k].across ? kDeep : TN / 2, &scratch, k ? &maps.b1 : &maps.b0, st))) return rc;
+        if ((rc = out_map(c, a.out[0], c.M, c.N, a.out_f32, &maps.out0, "the results")) ||
+            (rc = out_map(c, a.out[1], c.M, c.N, false, &maps.out1, "du")) ||
+            (rc = out_map(c, a.out[2], c.M, c.N, false, &maps.out2, "a")))
+            return rc;
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(kernel, kSmem, done);
+        if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "%s: %s", c.name, cudaGetErrorString(e));
+        const int64_t items = p.whole + ((int64_t)p.tiles_m * p.tiles_n - p.whole) * p.splits;
+        const int grid = 2 * (int)(items < p.clusters ? items : p.clusters);
+        const cudaError_t le = launch_after(kernel, dim3(grid), kThreads, kSmem, st, maps, a);
+        if (le != cudaSuccess) return pdl_fail(le, c.name);
+        z1_note_launch(reinterpret_cast<const void *>(kernel), grid, 1, kThreads, 0);
+        if (p.splits == 1) return ZERO1_OK;
+    } else {
+        a.whole = a.splits = 0;  // every tile is finished here, without parts
+    }
+    constexpr int kGroups = (dual(KIND) ? TN / 4 : TN / 2) / 32;
+    const int64_t rest = (int64_t)p.tiles_m * p.tiles_n - a.whole;
+    const cudaError_t e = launch_after(k_gated_ffn_join<KIND, TN>, dim3(16 * kGroups, (unsigned)(rest < 65535 ? rest : 65535)), 256, 0,
+                                       st, a);
+    if (e != cudaSuccess) return pdl_fail(e, c.name);
+    return ZERO1_OK;
+}
+
+template <int KIND>
+int launch_tile(const Call &c, Mm &a, void *workspace, zero1_stream_t stream)
+{
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return c.plan.tn == 256 ? launch<KIND, 256>(c, a, workspace, st) : launch<KIND, 128>(c, a, workspace, st);
+}
+
+// ------------------------------------------------- gated feed-forward ------
+
+// The matrices of a call; those that it does not use are absent.
+struct Ffn {
+    Mat h, w_gate, w_up, da, a, dg, du, dh;
+};
+
+Ffn mats_of(const zero1_gated_ffn_t *f)
+{
+    const int64_t T = f->rows, D = f->d_model, F = f->d_ff;
+    return Ffn{mat(f->h, T, D, f->ld_h, 2, "h"), mat(f->w_gate, F, D, f->ld_w_gate, 2, "w_gate"),
+               mat(f->w_up, F, D, f->ld_w_up, 2, "w_up"), mat(f->da, T, F, f->ld_da, 2, "da"), mat(f->a, T, F, f->ld_a, 2, "a"),
+               mat(f->dg, T, F, f->ld_dg, 2, "dg"), mat(f->du, T, F, f->ld_du, 2, "du"), mat(f->dh, T, D, f->ld_dh, 2, "dh")};
+}
+
+Operand operand(const Mat &m, int64_t cols, bool across) { return Operand{m.p, m.rows, cols, m.rows > 1 ? m.pitch / 2 : cols, across, m.what}; }
+
+int check_sizes(const zero1_gated_ffn_t *f, const char *call)
+{
+    if (!f) return z1_fail(ZERO1_EINVAL, "%s: the arguments are NULL", call);
+    if (f->rows < 0 || f->d_model < 1 || f->d_ff < 1)
+        return z1_fail(ZERO1_EINVAL, "%s: %lld rows, widths %lld and %lld", call, (long long)f->rows, (long long)f->d_model,
+                       (long long)f->d_ff);
+    if (f->act != ZERO1_FFN_SILU && f->act != ZERO1_FFN_GELU) return z1_fail(ZERO1_EINVAL, "%s: unknown activation %d", call, f->act);
+    if (f->rows > INT32_MAX / 2 || f->d_model > INT32_MAX / 4 || f->d_ff > INT32_MAX / 4)
+        return z1_fail(ZERO1_ERANGE, "%s: size not supported", call);
+    return ZERO1_OK;
+}
+
+const char *const kNames[] = {"gated feed-forward", "gated feed-forward backward", "gated feed-forward input gradient"};
+
+void fill_call(Call *c, const zero1_gated_ffn_t *f, int kind)
+{
+    const Ffn x = mats_of(f);
+    const int64_t D = f->d_model, F = f->d_ff;
+    *c = Call{};
+    c->name = kNames[kind];
+    c->kind = kind;
+    c->run = kRunBf16;
+    c->M = f->rows;
+    if (kind == kInputGrad) {
+        c->N = D; c->K = F;
+        c->a[0] = operand(x.dg, F, false); c->a[1] = operand(x.du, F, false);
+        c->b[0] = operand(x.w_gate, D, true); c->b[1] = operand(x.w_up, D, true);
+        c->na = c->nb = 2;
+    } else {
+        c->N = F; c->K = D;
+        c->a[0] = operand(x.h, D, false);
+        c->b[0] = operand(x.w_gate, D, false); c->b[1] = operand(x.w_up, D, false);
+        c->na = 1; c->nb = 2;
+    }
+}
+
+// EINVAL if an output shares memory with an input or another output; dg may be
+// da (the same pointer and stride).
+int check_ffn(const Call &c, const zero1_gated_ffn_t *f, Mat all[7], int *count)
+{
+    const Ffn x = mats_of(f);
+    Mat in[4], out[3];
+    int ni = 0, no = 0, rc;
+    in[ni++] = x.w_gate;
+    in[ni++] = x.w_up;
+    if (c.kind == kInputGrad) {
+        in[ni++] = x.dg;
+        in[ni++] = x.du;
+        out[no++] = x.dh;
+    } else {
+        in[ni++] = x.h;
+        if (c.kind == kBackward) {
+            in[ni++] = x.da;
+            out[no++] = x.dg;
+            out[no++] = x.du;
+        }
+        if (c.kind == kForward || x.a.p) out[no++] = x.a;
+    }
+    for (int k = 0; k < ni; ++k)
+        if ((rc = check_mat(in[k], 2, false, c.name)) != ZERO1_OK) return rc;
+    for (int k = 0; k < no; ++k)
+        if ((rc = check_mat(out[k], 2, true, c.name)) != ZERO1_OK) return rc;
+    for (int o = 0; o < no; ++o) {
+        for (int k = o + 1; k < no; ++k)
+            if (mats_overlap(out[o], out[k])) return z1_fail(ZERO1_EINVAL, "%s: %s and %s overlap", c.name, out[o].what, out[k].what);
+        for (int k = 0; k < ni; ++k) {
+            if (!mats_overlap(out[o], in[k])) continue;
+            if (c.kind == kBackward && o == 0 && k == 3 && out[o].p == in[k].p && out[o].pitch == in[k].pitch) continue;
+            return z1_fail(ZERO1_EINVAL, "%s: %s and %s overlap", c.name, out[o].what, in[k].what);
+        }
+    }
+    *count = 0;
+    for (int k = 0; k < ni; ++k) all[(*count)++] = in[k];
+    for (int k = 0; k < no; ++k) all[(*count)++] = out[k];
+    return ZERO1_OK;
+}
+
+// Checks and plans a call; nothing is left to do without rows (*idle).
+int begin_call(Call *c, const zero1_gated_ffn_t *f, int kind, void *workspace, int64_t bytes, bool *idle)
+{
+    int rc = check_sizes(f, kNames[kind]), n;
+    if (rc != ZERO1_OK) return rc;
+    *idle = f->rows == 0;
+    if (*idle) return ZERO1_OK;
+    Mat all[7];
+    fill_call(c, f, kind);
+    if ((rc = check_ffn(*c, f, all, &n)) || (rc = plan_call(c)) || (rc = check_workspace(*c, workspace, bytes, all, n))) return rc;
+    return check_device(c->name, all, n);
+}
+
+}  // namespace
+
+int z1_gated_ffn_status(uint32_t *status, int32_t clear) { return (int)async_status(status, clear); }
+
+extern "C" int zero1_gated_ffn_workspace(const zero1_gated_ffn_t *ffn, int32_t call, int64_t *bytes)
+{
+    const char *name = "gated feed-forward workspace";
+    if (!bytes) return z1_fail(ZERO1_EINVAL, "%s: bytes is NULL", name);
+    if (call < ZERO1_FFN_FORWARD || call > ZERO1_FFN_INPUT_GRAD) return z1_fail(ZERO1_EINVAL, "%s: unknown call %d", name, call);
+    int rc = check_sizes(ffn, name);
+    if (rc != ZERO1_OK) return rc;
+    *bytes = 0;
+    if (ffn->rows == 0) return ZERO1_OK;
+    Call c;
+    fill_call(&c, ffn, call);
+    if ((rc = plan_call(&c)) == ZERO1_OK) *bytes = c.bytes;
+    return rc;
+}
+
+extern "C" int zero1_gated_ffn_forward(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream)
+{
+    Z1Trace trace("zero1_gated_ffn_forward");
+    Call c;
+    bool idle;
+    const int rc = begin_call(&c, ffn, kForward, workspace, workspace_bytes, &idle);
+    if (rc != ZERO1_OK || idle) return rc;
+    Mm a{};
+    a.gelu = ffn->act == ZERO1_FFN_GELU;
+    a.out[0] = out_of(mats_of(ffn).a, 2);
+    return launch_tile<kForward>(c, a, workspace, stream);
+}
+
+extern "C" int zero1_gated_ffn_backward(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream)
+{
+    Z1Trace trace("zero1_gated_ffn_backward");
+    Call c;
+    bool idle;
+    const int rc = begin_call(&c, ffn, kBackward, workspace, workspace_bytes, &idle);
+    if (rc != ZERO1_OK || idle) return rc;
+    const Ffn x = mats_of(ffn);
+    Mm a{};
+    a.gelu = ffn->act == ZERO1_FFN_GELU;
+    a.da = static_cast<const uint16_t *>(ffn->da);
+    a.ld_da = x.da.rows > 1 ? ffn->ld_da : 0;
+    a.da_vec = vec_ok(x.da);
+    a.out[0] = out_of(x.dg, 2);
+    a.out[1] = out_of(x.du, 2);
+    a.out[2] = out_of(x.a, 2);
+    return launch_tile<kBackward>(c, a, workspace, stream);
+}
+
+extern "C" int zero1_gated_ffn_input_grad(const zero1_gated_ffn_t *ffn, void *workspace, int64_t workspace_bytes, zero1_stream_t stream)
+{
+    Z1Trace trace("zero1_gated_ffn_input_grad");
+    Call c;
+    bool idle;
+    const int rc = begin_call(&c, ffn, kInputGrad, workspace, workspace_bytes, &idle);
+    if (rc != ZERO1_OK || idle) return rc;
+    Mm a{};
+    a.out[0] = out_of(mats_of(ffn).dh, 2);
+    return launch_tile<kInputGrad>(c, a, workspace, stream);
+}
+
+// ------------------------------------------------------ weight gradient ----
+
+namespace {
+
+int weight_call(Call *c, int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy, const void *x, int64_t ld_x,
+                int32_t out_dtype, const char *call)
+{
+    if (rows < 0 || n < 1 || k < 1)
+        return z1_fail(ZERO1_EINVAL, "%s: %lld rows, %lld x %lld outputs", call, (long long)rows, (long long)n, (long long)k);
+    const int rc = check_dtype(out_dtype, call, "out_dtype");
+    if (rc != ZERO1_OK) return rc;
+    *c = Call{};
+    c->name = call;
+    c->kind = kWeightGrad;
+    c->M = n; c->N = k; c->K = rows;
+    c->a[0] = Operand{dy, rows, n, ld_dy, true, "dy"};
+    c->b[0] = Operand{x, rows, k, ld_x, true, "x"};
+    c->na = c->nb = rows > 0 ? 1 : 0;
+    c->run = out_dtype == ZERO1_DTYPE_F32 ? kRunF32 : kRunBf16;
+    return ZERO1_OK;
+}
+
+}  // namespace
+
+extern "C" int zero1_weight_grad_bf16_workspace(int64_t rows, int64_t n, int64_t k, const void *dy, int64_t ld_dy, const void *x,
+                                                int64_t ld_x, int32_t out_dtype, int64_t *bytes)
+{
+    const char *call = "bf16 weight gradient workspace";
+    if (!bytes) return z1_fail(ZERO1_EINVAL, "%s: bytes is NULL", call);
+    Call c;
+    int rc = weight_call(&c, rows, n, k, dy, ld_dy, x, ld_x, out_dtype, call);
+    if (rc == ZERO1_OK && (rc = plan_call(&c)) == ZERO1_OK) *bytes = c.bytes;
+    return rc;
+}
+
+extern "C" int zero1_weight_grad_bf16(const void *dy, int64_t ld_dy, int64_t n, const void *x, int64_t ld_x, int64_t k, int64_t rows,
+                                      void *dw, int64_t ld_dw, int32_t out_dtype, int32_t accumulate, void *workspace,
+                                      int64_t workspace_bytes, zero1_stream_t stream)
+{
+    Z1Trace trace("zero1_weight_grad_bf16");
+    const char *call = "bf16 weight gradient";
+    Call c;
+    int rc = weight_call(&c, rows, n, k, dy, ld_dy, x, ld_x, out_dtype, call);
+    if (rc != ZERO1_OK) return rc;
+    const int eo = esize(out_dtype);
+    const Mat all[] = {mat(dw, n, k, ld_dw, eo, "dw"), mat(dy, rows, n, ld_dy, 2, "dy"), mat(x, rows, k, ld_x, 2, "x")};
+    if ((rc = check_mat(all[0], eo, true, call)) || (rc = check_mat(all[1], 2, false, call)) || (rc = check_mat(all[2], 2, false, call)))
+        return rc;
+    for (int q = 1; q < 3; ++q)
+        if (mats_overlap(all[0], all[q])) return z1_fail(ZERO1_EINVAL, "%s: dw and %s overlap", call, all[q].what);
+    if ((rc = plan_call(&c)) || (rc = check_workspace(c, workspace, workspace_bytes, all, 3)) ||
+        (rc = check_device(call, all, 3)))
+        return rc;
+    Mm a{};
+    a.out[0] = out_of(all[0], eo);
+    a.out_f32 = out_dtype == ZERO1_DTYPE_F32;
+    a.accumulate = accumulate != 0;
+    return launch_tile<kWeightGrad>(c, a, workspace, stream);
+}

@@ -253,6 +253,8 @@ extern "C" int zero1_device_status(uint32_t *status, int32_t clear)
     cudaError_t e = async_status(status, clear);
     if (e == cudaSuccess) e = (cudaError_t)z1_weight_grad_status(&other, clear);
     *status |= other;
+    if (e == cudaSuccess) e = (cudaError_t)z1_gated_ffn_status(&other, clear);
+    *status |= other;
     if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "device status: %s", cudaGetErrorString(e));
     return ZERO1_OK;
 }
