@@ -696,6 +696,123 @@ int zero1_weight_grad(const void *dy, int64_t ld_dy, int64_t n, const zero1_chec
                       void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The global gradient norm and clipping (no counterpart in the pages):
+ *   norm = sqrt(sum of g^2 over all gradients)
+ *   c = min(1, max_norm / (norm + 1e-6)),   g <- g * c
+ * The norm travels as its square, a double in device memory, so that lists, shard
+ * ranges and ranks can be added up before anything is scaled.  Squares are summed
+ * eight at a time in fp32 and then, at the latest after sixteen such sums, in
+ * doubles; sums that would leave fp32's range are taken scaled.  The order is fixed
+ * by the sizes, the buffers' alignment and the GPU's number of SMs.  An Inf or a NaN among the gradients
+ * makes the sum Inf or NaN; so does no finite gradient by itself.
+ * Nothing synchronises the host, and the calls can be captured in a CUDA graph.
+ * ------------------------------------------------------------------------- */
+
+/* One tensor of a list: numel consecutive elements of dtype (0 elements: data is
+ * not looked at). */
+typedef struct zero1_tensor {
+    void *data;
+    int64_t numel;
+    int32_t dtype;
+    int32_t reserved;
+} zero1_tensor_t;
+
+/* *sumsq (device) = sum of squares of all elements of the `count` tensors (host
+ * array, read before the call returns), or, with accumulate, that sum added to it.
+ * norms: device, `count` floats, each tensor's own norm, or NULL.  Tensors may be of
+ * any element offset and may overlap one another.  workspace: device, 8-byte
+ * aligned, zero1_grad_sumsq_workspace bytes for the same list (scratch). */
+int zero1_grad_sumsq_workspace(const zero1_tensor_t *tensors, int32_t count, int64_t *bytes);
+int zero1_grad_sumsq(const zero1_tensor_t *tensors, int32_t count, double *sumsq, float *norms, int32_t accumulate,
+                     void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
+
+/* Every element times c, rounded once, into `outs` (tensors of the same sizes and
+ * types), or in place with outs NULL, where nothing is read or written if c is 1.  Where
+ * *sumsq is not finite, c is 1: the Inf or NaN stays and reaches the step's
+ * overflow flag.  norm: device, the norm, or NULL.  max_norm: finite, > 0.  An output
+ * may be its own input (same data), and shares no byte with any other tensor of the call. */
+int zero1_grad_clip(const zero1_tensor_t *tensors, const zero1_tensor_t *outs, int32_t count, const double *sumsq,
+                    float max_norm, float *norm, zero1_stream_t stream);
+
+/* The same for the step: *sumsq = sum of g^2 over the real elements of shards
+ * [shard_begin, shard_end), g = (rank-order fp32 sum of the M replicas) * 1/(B*S)
+ * as the fused step takes it (hp: B and S).  Ranks that own other shards add their
+ * sums before the step.  sums: device fp32, L elements, gets the unscaled sums
+ * (+0 on padding) for zero1_step_clipped, or NULL.  workspace: device, 8-byte
+ * aligned, zero1_shard_grad_sumsq_workspace bytes (scratch). */
+int zero1_shard_grad_sumsq_workspace(int64_t *bytes);
+int zero1_shard_grad_sumsq(const zero1_plan_t *plan, int32_t shard_begin, int32_t shard_end, const void *const *grads,
+                           const zero1_adamw_t *hp, double *sumsq, float *sums, int32_t accumulate, void *workspace,
+                           int64_t workspace_bytes, zero1_stream_t stream);
+
+/* The fused step with clipped gradients: zero1_reduce_scatter_adamw_allgather with
+ * g = (s * inv) * c, c from *sumsq, the total over all shards and ranks (one more
+ * rounding; with c = 1 bit for bit that step).  sums NULL: the gradients are read again, 2M + 26
+ * bytes per parameter; else the sums that zero1_shard_grad_sumsq kept, 30 bytes,
+ * and grads is not looked at.  master_out, m_out, v_out get the updated state: the
+ * state itself (in place) or other buffers, each its own way.  If *sumsq is not
+ * finite nothing is written but the norm, and 1 ORed into overflow_flag (device, or NULL).
+ * norm: device, the norm, or NULL.  max_norm: finite, > 0.  Buffers must not
+ * overlap, but for gradients one another and an output its own input. */
+int zero1_step_clipped(const zero1_plan_t *plan, int32_t shard_begin, int32_t shard_end, const void *const *grads,
+                       const float *sums, const float *master, const float *m, const float *v, float *master_out,
+                       float *m_out, float *v_out, void *params, const zero1_adamw_t *hp, const double *sumsq,
+                       float max_norm, float *norm, uint32_t *overflow_flag, zero1_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm with its residual.  For the residual stream x and a block's output
+ * y, row by row (D = cols, a = residual_scale):
+ *   r = x + a * y                                   [r = x without y]
+ *   mean = sum(r) / D,  rstd = 1 / sqrt(sum((r - mean)^2) / D + eps)
+ *   rh = (r - mean) * rstd
+ *   h = w * rh + b                                  [w NULL: 1, b NULL: 0]
+ * r enters its norm unrounded; the squares are summed about the mean.  y and r
+ * come together.  1 <= cols <= ZERO1_BLOCK_NORM_MAX_COLS (ERANGE above). */
+typedef struct zero1_layer_norm {
+    int64_t rows, cols;
+    float eps;            /* finite, > 0 */
+    float residual_scale; /* a, finite */
+    int32_t act_dtype;    /* y, h, dh, dy */
+    int32_t res_dtype;    /* x, r, dr, dx; fp32 whenever act_dtype is */
+    int32_t param_dtype;  /* w, b */
+    int32_t grad_dtype;   /* dw, db */
+    int32_t accumulate;   /* backward: add to dw and db instead of overwriting */
+} zero1_layer_norm_t;
+
+/* Forward.  r8, when not NULL, gets the checkpoint of rh in the same pass over the
+ * data: what the backward pass reads in place of r.  r may be x (same pointer,
+ * type and stride); other buffers must not overlap. */
+typedef struct zero1_layer_norm_forward {
+    const void *x, *y, *w, *b;
+    void *r, *h;
+    float *mean, *rstd; /* [rows] */
+    const zero1_checkpoint8_t *r8;
+    int64_t ld_x, ld_y, ld_r, ld_h;
+} zero1_layer_norm_forward_t;
+int zero1_layer_norm_forward(const zero1_layer_norm_t *cfg, const zero1_layer_norm_forward_t *io, zero1_stream_t stream);
+
+/* Backward, from the gradients dh of h and dr of r (dr NULL: none):
+ *   t = w dh,  d = dr + rstd * (t - mean(t) - rh * mean(t rh))
+ *   dx = d,  dy = a d
+ *   dw = sum over rows of dh * rh,  db = sum over rows of dh
+ * The saved rows come as r (res_dtype; the forward call's x where it had no y)
+ * or as the checkpoint r8.  dy, dw and db may each be NULL when not wanted; dw
+ * and db may be views into a replica's flat gradient buffer at any element
+ * offset.  dx may be dr and dy may be dh (same pointer, type and stride).
+ * workspace: device, 16-byte aligned, zero1_layer_norm_workspace bytes (scratch;
+ * not needed without dw and db). */
+typedef struct zero1_layer_norm_backward {
+    const void *dh, *dr, *r, *w;
+    const float *mean, *rstd;
+    const zero1_checkpoint8_t *r8;
+    void *dx, *dy, *dw, *db;
+    int64_t ld_dh, ld_dr, ld_r, ld_dx, ld_dy;
+} zero1_layer_norm_backward_t;
+int zero1_layer_norm_workspace(const zero1_layer_norm_t *cfg, int64_t *bytes);
+int zero1_layer_norm_backward(const zero1_layer_norm_t *cfg, const zero1_layer_norm_backward_t *io, void *workspace,
+                              int64_t workspace_bytes, zero1_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Gated feed-forward block.  For rows h [rows, d_model] and weights w_gate,
  * w_up [d_ff, d_model], all bf16:
  *   g = h w_gate^T,  u = h w_up^T,  a = act(g) * u          [rows, d_ff]

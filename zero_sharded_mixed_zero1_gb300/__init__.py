@@ -70,3 +70,16 @@ from .ffn import (  # noqa: E402,F401
     zero1_weight_grad_bf16,
     zero1_weight_grad_bf16_workspace,
 )
+from .layer_norm import (  # noqa: E402,F401
+    LayerNorm,
+    zero1_layer_norm_backward,
+    zero1_layer_norm_forward,
+    zero1_layer_norm_workspace,
+)
+from .clip import (  # noqa: E402,F401
+    zero1_grad_clip,
+    zero1_grad_sumsq,
+    zero1_grad_sumsq_workspace,
+    zero1_shard_grad_sumsq,
+    zero1_step_clipped,
+)

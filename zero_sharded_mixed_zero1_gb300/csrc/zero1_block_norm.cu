@@ -95,24 +95,6 @@ int check_saved(const zero1_block_norm_t *cfg, const zero1_checkpoint8_t *k, con
     return ZERO1_OK;
 }
 
-// EINVAL if an output overlaps another output or an input.  in_place[o] names
-// the input that output o may coincide with (-1: none).
-int check_overlaps(const Mat *out, const int *in_place, int nout, const Mat *in, int nin, const char *call)
-{
-    for (int o = 0; o < nout; ++o) {
-        for (int q = o + 1; q < nout; ++q)
-            if (mats_overlap(out[o], out[q]))
-                return z1_fail(ZERO1_EINVAL, "%s: %s and %s overlap", call, out[o].what, out[q].what);
-        for (int q = 0; q < nin; ++q) {
-            if (!mats_overlap(out[o], in[q])) continue;
-            if (in_place[o] == q && out[o].p == in[q].p && out[o].pitch == in[q].pitch && out[o].width == in[q].width)
-                continue;
-            return z1_fail(ZERO1_EINVAL, "%s: %s and %s overlap", call, out[o].what, in[q].what);
-        }
-    }
-    return ZERO1_OK;
-}
-
 Common common_of(const zero1_block_norm_t *cfg, const void *w_post, const void *w_pre, const void *gate, int64_t ld_gate,
                  const zero1_checkpoint8_t *y8, const zero1_checkpoint8_t *r8)
 {
