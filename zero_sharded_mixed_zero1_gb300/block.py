@@ -284,6 +284,26 @@ def _workspace(workspace, nbytes: int, stream):
     return workspace.data_ptr(), workspace.numel(), workspace
 
 
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+
+
+def _call_with(workspace, nbytes: int, stream, fn, *args) -> int:
+    """fn(*args, workspace, its bytes, stream): with the caller's workspace, or
+    with memory of the calling stream that goes back to it after the call, from
+    the allocator itself where that is there (a few microseconds less than a
+    tensor)."""
+    st = _launch_stream(stream)
+    if workspace is not None or not nbytes or _raw_alloc is None or _raw_delete is None:
+        ws, nbytes, keep = _workspace(workspace, nbytes, stream)
+        return fn(*args, ws, nbytes, st)
+    ws = _raw_alloc(nbytes, st)
+    try:
+        return fn(*args, ws, nbytes, st)
+    finally:
+        _raw_delete(ws)
+
+
 def zero1_block_norm_workspace(cfg: BlockNorm, rows: int, cols: int) -> int:
     """Bytes of scratch memory that zero1_block_norm_backward needs."""
     c = _cfg(cfg, (rows, cols), 0, 0, 0, 0, 0, 0, 0)

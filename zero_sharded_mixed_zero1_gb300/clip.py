@@ -12,8 +12,8 @@ import struct
 import torch
 
 from . import block as _block
-from ._lib import AdamW, Plan, _AdamWStruct, _check_rc, _dev, _ptrs, _range, _replicas
-from .block import _CODES, _get_device, _launch_stream, _usable, _workspace
+from ._lib import AdamW, Plan, _AdamWStruct, _check_rc, _dev, _range, _replicas
+from .block import _CODES, _call_with, _get_device, _launch_stream, _usable
 
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
 SHARD_WORKSPACE = 8 * 2048
@@ -36,23 +36,53 @@ def _lib():
     return _ready
 
 
+_Tensor = torch.Tensor
+_BF16, _F32, _F64 = torch.bfloat16, torch.float32, torch.float64
+
+
 def _table(tensors, what: str) -> bytes:
     """zero1_tensor_t of each tensor, packed."""
-    device, rows = _get_device(), []
-    for i, t in enumerate(tensors):
-        code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None or t.get_device() != device or not t.is_contiguous():
-            _usable(t, f"{what}[{i}]")  # the long way, for what is unusual or wrong
-            if code is None:
-                raise TypeError(f"{what}[{i}]: expected bfloat16 or float32, got {t.dtype}")
-            if not t.is_contiguous():
-                raise ValueError(f"{what}[{i}]: must be contiguous")
-        rows += (t.data_ptr(), t.numel(), code)
+    device = _get_device()
+    rows = []
+    for t in tensors:
+        if isinstance(t, _Tensor) and t.get_device() == device and t.is_contiguous():
+            dtype = t.dtype
+            if dtype is _BF16:
+                rows += (t.data_ptr(), t.numel(), 0)
+                continue
+            if dtype is _F32:
+                rows += (t.data_ptr(), t.numel(), 1)
+                continue
+        rows += _unusual(t, f"{what}[{len(rows) // 3}]")
     return struct.pack("=" + "Qqq" * (len(rows) // 3), *rows)
 
 
+def _unusual(t, what: str):
+    """The same for what is pinned, or wrong."""
+    _usable(t, what)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what}: expected bfloat16 or float32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr(), t.numel(), code
+
+
+def _ptr(t, dtype, numel: int, what: str) -> int:
+    """_dev, by the short way for a usual tensor."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    return _dev(t, dtype, numel, what)
+
+
 def _scalar(t, dtype, numel: int, what: str):
-    return None if t is None else _dev(t, dtype, numel, what)
+    return None if t is None else _ptr(t, dtype, numel, what)
+
+
+def _grads(plan: Plan, grads, nv: int):
+    """The replicas' gradient pointers, as a host array."""
+    _replicas(plan, grads, "grads")
+    return struct.pack(f"={plan.M}Q", *[_ptr(t, _BF16, nv, "a replica's gradient") for t in grads])
 
 
 def zero1_grad_sumsq(tensors, sumsq: torch.Tensor, *, norms: torch.Tensor | None = None, accumulate: bool = False,
@@ -67,10 +97,8 @@ def zero1_grad_sumsq(tensors, sumsq: torch.Tensor, *, norms: torch.Tensor | None
         need = _i64()
         _check_rc(lib.zero1_grad_sumsq_workspace(table, n, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
-    _check_rc(lib.zero1_grad_sumsq(table, n, _dev(sumsq, torch.float64, 1, "sumsq"),
-                                   _scalar(norms, torch.float32, n, "norms"), 1 if accumulate else 0, ws, nbytes,
-                                   _launch_stream(stream)))
+    _check_rc(_call_with(workspace, nbytes, stream, lib.zero1_grad_sumsq, table, n, _ptr(sumsq, _F64, 1, "sumsq"),
+                         _scalar(norms, _F32, n, "norms"), 1 if accumulate else 0))
 
 
 def zero1_grad_sumsq_workspace(tensors) -> int:
@@ -92,8 +120,8 @@ def zero1_grad_clip(tensors, sumsq: torch.Tensor, max_norm: float, *, outs=None,
         if len(outs) != n:
             raise ValueError(f"outs: expected {n} tensors, got {len(outs)}")
         out = _table(outs, "outs")
-    _check_rc(_lib().zero1_grad_clip(table, out, n, _dev(sumsq, torch.float64, 1, "sumsq"), max_norm,
-                                     _scalar(norm, torch.float32, 1, "norm"), _launch_stream(stream)))
+    _check_rc(_lib().zero1_grad_clip(table, out, n, _ptr(sumsq, _F64, 1, "sumsq"), max_norm,
+                                     _scalar(norm, _F32, 1, "norm"), _launch_stream(stream)))
 
 
 def zero1_shard_grad_sumsq(plan: Plan, shard_begin: int, shard_end: int, grads, hp: AdamW, sumsq: torch.Tensor, *,
@@ -102,13 +130,10 @@ def zero1_shard_grad_sumsq(plan: Plan, shard_begin: int, shard_end: int, grads, 
     """Sum of squares of the summed, unscaled gradients of shards [shard_begin,
     shard_end), written to sumsq (float64, one element) or added to it.  sums:
     fp32, L elements, keeps the replicas' sums for zero1_step_clipped."""
-    _replicas(plan, grads, "grads")
     _, L, nv = _range(plan, shard_begin, shard_end)
-    ws, nbytes, keep = _workspace(workspace, SHARD_WORKSPACE, stream)
-    _check_rc(_lib().zero1_shard_grad_sumsq(
-        ctypes.byref(plan), shard_begin, shard_end, _ptrs(grads, torch.bfloat16, nv, "grads"), ctypes.byref(hp.c_struct()),
-        _dev(sumsq, torch.float64, 1, "sumsq"), _scalar(sums, torch.float32, L, "sums"), 1 if accumulate else 0, ws, nbytes,
-        _launch_stream(stream)))
+    _check_rc(_call_with(workspace, SHARD_WORKSPACE, stream, _lib().zero1_shard_grad_sumsq, ctypes.byref(plan), shard_begin,
+                         shard_end, _grads(plan, grads, nv), ctypes.byref(hp.c_struct()), _ptr(sumsq, _F64, 1, "sumsq"),
+                         _scalar(sums, _F32, L, "sums"), 1 if accumulate else 0))
 
 
 def zero1_step_clipped(plan: Plan, shard_begin: int, shard_end: int, grads, master, m, v, params, hp: AdamW,
@@ -121,20 +146,17 @@ def zero1_step_clipped(plan: Plan, shard_begin: int, shard_end: int, grads, mast
     (master, m, v) go, by default in place.  norm: fp32, one element, gets the
     norm.  If sumsq is not finite, nothing else is written and overflow_flag set."""
     _, L, nv = _range(plan, shard_begin, shard_end)
-    g = None
-    if sums is None:
-        _replicas(plan, grads, "grads")
-        g = _ptrs(grads, torch.bfloat16, nv, "grads")
+    g = _grads(plan, grads, nv) if sums is None else None
     names = ("master", "m", "v")
-    state = [_dev(t, torch.float32, L, k) for t, k in zip((master, m, v), names)]
+    state = [_ptr(t, _F32, L, k) for t, k in zip((master, m, v), names)]
     if out is None:
         to = state
     else:
         if len(out) != 3:
             raise ValueError("out: expected three tensors (master, m, v)")
-        to = [_dev(t, torch.float32, L, f"out {k}") for t, k in zip(out, names)]
+        to = [_ptr(t, _F32, L, f"out {k}") for t, k in zip(out, names)]
     _check_rc(_lib().zero1_step_clipped(
-        ctypes.byref(plan), shard_begin, shard_end, g, _scalar(sums, torch.float32, L, "sums"), *state, *to,
-        _dev(params, torch.bfloat16, nv, "params"), ctypes.byref(hp.c_struct()), _dev(sumsq, torch.float64, 1, "sumsq"),
-        max_norm, _scalar(norm, torch.float32, 1, "norm"), _scalar(overflow_flag, torch.int32, 1, "overflow_flag"),
+        ctypes.byref(plan), shard_begin, shard_end, g, _scalar(sums, _F32, L, "sums"), *state, *to,
+        _ptr(params, _BF16, nv, "params"), ctypes.byref(hp.c_struct()), _ptr(sumsq, _F64, 1, "sumsq"),
+        max_norm, _scalar(norm, _F32, 1, "norm"), _scalar(overflow_flag, torch.int32, 1, "overflow_flag"),
         _launch_stream(stream)))

@@ -94,7 +94,9 @@ struct Clip {
 
 // ------------------------------------------------------ lists of tensors ---
 
-constexpr int kGroup = 512;     // tensors per launch (their table travels in the kernel's arguments)
+// Tensors per launch: their table travels in the kernel's arguments, of which a
+// launch copies all, so that short lists take a smaller one.
+constexpr int kGroup = 512, kShort = 48;
 constexpr int kListBlock = 256;
 constexpr int kUnroll = 4;      // vectors of 8 elements in flight per thread
 
@@ -106,14 +108,16 @@ struct Entry {
     int16_t f32;
     int16_t head;    // elements before the first 16-byte boundary; -1: out lies otherwise, one element at a time
 };
+template <int N>
 struct Table {
-    Entry e[kGroup];
     int count, chunks;
     int64_t chunk;  // vectors
+    Entry e[N];
 };
-static_assert(sizeof(Table) + 64 <= 32764, "kernel arguments");
+static_assert(sizeof(Table<kGroup>) + 64 <= 32764, "kernel arguments");
 
-__device__ __forceinline__ int entry_of(const Table &t, int chunk)
+template <int N>
+__device__ __forceinline__ int entry_of(const Table<N> &t, int chunk)
 {
     int lo = 0, hi = t.count - 1;  // the last entry whose first chunk is at most this (empty tensors have none)
     while (lo < hi) {
@@ -169,9 +173,11 @@ __device__ __forceinline__ void sum_chunk(const Entry &e, int64_t k, int64_t per
     s.flush();
 }
 
-__global__ void __launch_bounds__(kListBlock) k_list_sumsq(const __grid_constant__ Table t, double *part)
+template <int N>
+__global__ void __launch_bounds__(kListBlock) k_list_sumsq(const __grid_constant__ Table<N> t, double *part)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ double red[2][32];
     int flip = 0;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x, flip ^= 1) {
@@ -186,14 +192,16 @@ __global__ void __launch_bounds__(kListBlock) k_list_sumsq(const __grid_constant
 
 // Adds the chunks' sums: a warp to a tensor, lanes in strides and then joined in
 // order; tensors in order of their warps.
-__global__ void __launch_bounds__(1024) k_list_finish(const __grid_constant__ Table t, const double *part, double *sumsq, float *norms,
+template <int N>
+__global__ void __launch_bounds__(1024) k_list_finish(const __grid_constant__ Table<N> t, const double *part, double *sumsq, float *norms,
                                                       int add)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ double red[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     double total = 0.0;
-    for (int k = warp; k < t.count; k += 32) {
+    for (int k = warp; k < t.count; k += warps) {
         const int b = t.e[k].first, e = k + 1 < t.count ? t.e[k + 1].first : t.chunks;
         double x = 0.0;
 #pragma unroll 8
@@ -245,10 +253,12 @@ __device__ __forceinline__ void clip_chunk(const Entry &e, int64_t k, int64_t pe
         [&](int64_t j) { st1(o + j, __fmul_rn(ld1(p + j), c)); });
 }
 
+template <int N>
 __global__ void __launch_bounds__(kListBlock)
-k_list_clip(const __grid_constant__ Table t, const double *sumsq, double max_norm, float *norm, int in_place)
+k_list_clip(const __grid_constant__ Table<N> t, const double *sumsq, double max_norm, float *norm, int in_place)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ float coef;
     if (threadIdx.x == 0) {
         const Clip c(*sumsq, max_norm);
@@ -258,7 +268,8 @@ k_list_clip(const __grid_constant__ Table t, const double *sumsq, double max_nor
     __syncthreads();
     const float c = coef;
     if (in_place && c == 1.f) return;
-    for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    // from the end: what the sum of squares read last is still in L2
+    for (int k = t.chunks - 1 - blockIdx.x; k >= 0; k -= gridDim.x) {
         const Entry &e = t.e[entry_of(t, k)];
         if (e.f32) clip_chunk<float>(e, k - e.first, t.chunk, c);
         else clip_chunk<uint16_t>(e, k - e.first, t.chunk, c);
@@ -275,6 +286,7 @@ __global__ void __launch_bounds__(kBlock, MT > 0 ? 4 : 3)
 k_shard_sumsq(const __grid_constant__ GradPtrs g, int M, const Walk w, float inv, float *sums, double *part)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ double red[32];
     const int64_t tid = grid_tid(), nthr = grid_threads();
     SumSq acc;
@@ -310,6 +322,7 @@ k_shard_sumsq(const __grid_constant__ GradPtrs g, int M, const Walk w, float inv
 __global__ void __launch_bounds__(256) k_shard_finish(const double *part, int parts, double *sumsq, int add)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ double red[32];
     double x = 0.0;
 #pragma unroll 4
@@ -349,6 +362,7 @@ k_step_clipped(const __grid_constant__ GradPtrs g, int M, const float *sums, con
                const double *sumsq, double max_norm, float *norm, uint32_t *flag, int wide)
 {
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ float shared_coef;
     __shared__ int bad;
     if (threadIdx.x == 0) {
@@ -366,7 +380,8 @@ k_step_clipped(const __grid_constant__ GradPtrs g, int M, const float *sums, con
     const float coef = shared_coef;
     const int64_t tid = grid_tid(), nthr = grid_threads();
     const bool w32 = w.w32 != 0;
-    for (int64_t i = tid; i < w.nvec; i += nthr) {
+    // from the end: what the first pass read or wrote last is still in L2
+    for (int64_t i = w.nvec - 1 - tid; i >= 0; i -= nthr) {
         const int64_t j = w.head + i * kVec;
         float s[kVec];
         if constexpr (KEPT) {
@@ -441,14 +456,14 @@ int check_list(const zero1_tensor_t *t, int32_t count, const char *call, const c
 
 // Groups of at most kGroup tensors, with their chunks.  outs may be NULL.  `run`
 // launches one group.
-template <class F>
-int each_group(const zero1_tensor_t *t, const zero1_tensor_t *outs, int32_t count, int64_t per, F &&run)
+template <int N, class F>
+int each_group_of(const zero1_tensor_t *t, const zero1_tensor_t *outs, int32_t count, int64_t per, F &&run)
 {
     for (int at = 0; at < count;) {
-        Table tab;
+        Table<N> tab;
         int64_t chunks = 0;
         int n = 0;
-        for (; at + n < count && n < kGroup && chunks <= INT32_MAX / 2; ++n) {
+        for (; at + n < count && n < N && chunks <= INT32_MAX / 2; ++n) {
             const zero1_tensor_t &x = t[at + n];
             const int es = esize(x.dtype);
             Entry &e = tab.e[n];
@@ -472,12 +487,34 @@ int each_group(const zero1_tensor_t *t, const zero1_tensor_t *outs, int32_t coun
     return ZERO1_OK;
 }
 
+template <class F>
+int each_group(const zero1_tensor_t *t, const zero1_tensor_t *outs, int32_t count, int64_t per, F &&run)
+{
+    return count <= kShort ? each_group_of<kShort>(t, outs, count, per, run) : each_group_of<kGroup>(t, outs, count, per, run);
+}
+
 int list_grid(const void *kernel, int chunks, int sms)
 {
     const int64_t wave = (int64_t)sms * blocks_per_sm(kernel, kListBlock);
     const int grid = (int)(chunks < wave ? chunks : wave);
     z1_note_launch(kernel, grid, blocks_per_sm(kernel, kListBlock), kListBlock, 0);
     return grid < 1 ? 1 : grid;
+}
+
+template <int N>
+auto sumsq_of(const Table<N> &)
+{
+    return k_list_sumsq<N>;
+}
+template <int N>
+auto finish_of(const Table<N> &)
+{
+    return k_list_finish<N>;
+}
+template <int N>
+auto clip_of(const Table<N> &)
+{
+    return k_list_clip<N>;
 }
 
 // EINVAL if two of the extents share a byte.
@@ -547,15 +584,12 @@ int list_chunk(int64_t total, const char *call, int64_t *per, int *sms)
     return ZERO1_OK;
 }
 
-// Doubles of the largest group of a list.
+// Doubles for the chunks of any group of a list.
 int64_t most_chunks(const zero1_tensor_t *t, int32_t count, int64_t per)
 {
-    int64_t most = 1;
-    each_group(t, nullptr, count, per, [&](const Table &tab, int) {
-        most = std::max<int64_t>(most, tab.chunks);
-        return ZERO1_OK;
-    });
-    return most;
+    int64_t n = 1;
+    for (int k = 0; k < count; ++k) n += chunks_of(t[k], per);
+    return n;
 }
 
 }  // namespace
@@ -598,21 +632,22 @@ extern "C" int zero1_grad_sumsq(const zero1_tensor_t *tensors, int32_t count, do
     if (in_host_memory(workspace)) return z1_fail(ZERO1_EINVAL, "%s: the workspace must be device memory", call);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     double *part = static_cast<double *>(workspace);
-    auto finish = [&](const Table &tab, int at) -> int {
-        const cudaError_t e = launch_after(k_list_finish, dim3(1), 1024, 0, st, tab, (const double *)part, sumsq,
+    auto finish = [&](const auto &tab, int at) -> int {
+        const cudaError_t e = launch_after(finish_of(tab), dim3(1), tab.chunks <= 256 ? 256 : 1024, 0, st, tab, (const double *)part, sumsq,
                                            norms ? norms + at : nullptr, accumulate || at > 0 ? 1 : 0);
         return e == cudaSuccess ? ZERO1_OK : pdl_fail(e, call);
     };
     if (count == 0) {
-        Table none;
+        Table<kShort> none;
         none.count = none.chunks = 0;
         none.chunk = per;
         return finish(none, 0);
     }
-    return each_group(tensors, nullptr, count, per, [&](const Table &tab, int at) -> int {
+    return each_group(tensors, nullptr, count, per, [&](const auto &tab, int at) -> int {
         if (tab.chunks > 0) {
-            const int grid = list_grid(reinterpret_cast<const void *>(k_list_sumsq), tab.chunks, sms);
-            const cudaError_t e = launch_after(k_list_sumsq, dim3(grid), kListBlock, 0, st, tab, part);
+            const auto kernel = sumsq_of(tab);
+            const int grid = list_grid(reinterpret_cast<const void *>(kernel), tab.chunks, sms);
+            const cudaError_t e = launch_after(kernel, dim3(grid), kListBlock, 0, st, tab, part);
             if (e != cudaSuccess) return pdl_fail(e, call);
         }
         return finish(tab, at);
@@ -639,14 +674,15 @@ extern "C" int zero1_grad_clip(const zero1_tensor_t *tensors, const zero1_tensor
     if ((rc = check_outs(tensors, outs ? outs : tensors, count, sumsq, norm, call)) || (rc = list_chunk(total, call, &per, &sms)))
         return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    auto run = [&](const Table &tab, int at) -> int {
-        const int grid = list_grid(reinterpret_cast<const void *>(k_list_clip), tab.chunks, sms);
-        const cudaError_t e = launch_after(k_list_clip, dim3(grid), kListBlock, 0, st, tab, sumsq, (double)max_norm,
+    auto run = [&](const auto &tab, int at) -> int {
+        const auto kernel = clip_of(tab);
+        const int grid = list_grid(reinterpret_cast<const void *>(kernel), tab.chunks, sms);
+        const cudaError_t e = launch_after(kernel, dim3(grid), kListBlock, 0, st, tab, sumsq, (double)max_norm,
                                            at == 0 ? norm : nullptr, outs ? 0 : 1);
         return e == cudaSuccess ? ZERO1_OK : pdl_fail(e, call);
     };
     if (count == 0) {
-        Table none;
+        Table<kShort> none;
         none.count = none.chunks = 0;
         none.chunk = per;
         return norm ? run(none, 0) : ZERO1_OK;

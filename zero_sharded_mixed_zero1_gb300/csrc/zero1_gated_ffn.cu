@@ -344,11 +344,16 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tc_alloc(&bar.tmem);
+    if (warp == 3 && lane == 0) {  // (every product has these two)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.a0) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.b0) : "memory");
+    }
     tc_before();
     __syncthreads();
     cluster_sync();
     tc_after();
     wait_prior_grid();  // up to here this kernel may run beside the one before it
+    let_next_grid_start();
     const uint32_t tmem = bar.tmem;
     const int items = items_of(a);
     const int first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -538,7 +543,7 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                 }
             }
         }
-        boxes_written();  // before the grid counts as done
+        boxes_read();  // the places belong to this block; what is under way to memory is part of the grid
     }
     __syncwarp();
     __syncthreads();
@@ -584,6 +589,7 @@ __global__ void __launch_bounds__(256) k_gated_ffn_join(const Mm a)
     constexpr bool kDual = dual(KIND);
     constexpr int kCols = TN / 2, W = kDual ? TN / 4 : TN / 2, kGroups = W / 32;  // results' columns of a warp
     wait_prior_grid();
+    let_next_grid_start();
     __shared__ float sum[kDual ? 2 : 1][32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int slot = blockIdx.x / kGroups, c0 = blockIdx.x % kGroups * 32;
@@ -635,6 +641,90 @@ __global__ void __launch_bounds__(256) k_gated_ffn_join(const Mm a)
                     *o = to_bf16(a.accumulate ? bf_one(*o) + x : x);
                 }
             }
+        }
+    }
+}
+
+// ------------------------------------------------------- aligned copies ----
+//
+// Operands whose rows do not start on 16-byte boundaries (or, along the
+// contraction, do not end on one) are copied to rows that do, all of a call's in
+// one launch: a warp takes 1024 columns of a row, by the 16-byte pieces that hold
+// them, shifted into place; columns past the last one become 0.
+
+constexpr int kCopyCols = 1024;
+
+struct AlignCopy {
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t ld, rows, cols, wide, segments, end;  // segments of a row; end: of its items among all
+};
+struct AlignCopies {
+    AlignCopy m[4];
+    int count;
+    int64_t items;
+};
+
+// 16 bytes of a matrix that lies in [begin, end); what is outside is not read.
+__device__ __forceinline__ uint4 piece_of(const unsigned char *p, const unsigned char *begin, const unsigned char *end)
+{
+    if (p >= begin && p + 16 <= end) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        w[k] = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const unsigned char *q = p + 4 * k + 2 * h;
+            if (q >= begin && q < end) w[k] |= (uint32_t) * reinterpret_cast<const uint16_t *>(q) << (16 * h);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(256) k_align_operands(const AlignCopies all)
+{
+    wait_prior_grid();
+    let_next_grid_start();
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; i < all.items; i += (int64_t)gridDim.x * 8) {
+        int k = 0;
+        while (i >= all.m[k].end) ++k;
+        const AlignCopy &m = all.m[k];
+        const int64_t in = i - (k ? all.m[k - 1].end : 0), row = in / m.segments, c0 = in % m.segments * kCopyCols + lane * 8;
+        const unsigned char *begin = reinterpret_cast<const unsigned char *>(m.src), *end = begin + ((m.rows - 1) * m.ld + m.cols) * 2;
+        const unsigned char *p = begin + (row * m.ld + c0) * 2;
+        const int odd = (int)((uintptr_t)p & 15) / 2;  // the same for every lane
+        p -= 2 * odd;
+        uint4 lo[4], hi[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+            if (c0 + 256 * u >= m.cols) continue;
+            lo[u] = piece_of(p + 512 * u, begin, end);
+            if (odd) hi[u] = piece_of(p + 512 * u + 16, begin, end);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t c = c0 + 256 * u;
+            if (c >= m.wide) continue;
+            const uint32_t x[9] = {lo[u].x, lo[u].y, lo[u].z, lo[u].w, hi[u].x, hi[u].y, hi[u].z, hi[u].w, 0};
+            uint32_t w[5], o[4];
+            if (odd & 4) {
+#pragma unroll
+                for (int j = 0; j < 5; ++j) w[j] = odd & 2 ? x[min(j + 3, 8)] : x[j + 2];
+            } else {
+#pragma unroll
+                for (int j = 0; j < 5; ++j) w[j] = odd & 2 ? x[j + 1] : x[j];
+            }
+            const int left = (int)min((int64_t)8, m.cols - c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[j] = odd & 1 ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+                if (2 * j >= left) o[j] = 0;
+                else if (2 * j + 1 >= left) o[j] &= 0xffffu;
+            }
+            *reinterpret_cast<uint4 *>(m.dst + row * m.wide + c) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -713,23 +803,43 @@ int check_device(const char *call, const Mat *mats, int n)
     return ZERO1_OK;
 }
 
-// The map of an operand, of a copy of it in the workspace if need be.
-int operand_map(const Call &c, const Operand &o, int box_rows, char **scratch, CUtensorMap *map, cudaStream_t st)
+// The map of an operand, or of its copy in the workspace.
+int operand_map(const Call &c, const Operand &o, int box_rows, const AlignCopy *copy, CUtensorMap *map)
 {
-    const void *p = o.p;
-    int64_t ld = o.rows > 1 ? o.ld : round_up(o.cols, 8), cols = o.cols;
-    if (!usable(o)) {
-        uint16_t *copy = reinterpret_cast<uint16_t *>(*scratch);
-        *scratch += copy_bytes(o);
-        const int64_t wide = round_up(o.cols, 8);
-        const dim3 grid((unsigned)(o.rows < 32768 ? (o.rows + 7) / 8 : 4096), (unsigned)(wide < 256 * 65535 ? (wide + 255) / 256 : 65535));
-        k_align_rows<<<grid, 256, 0, st>>>(static_cast<const uint16_t *>(o.p), o.rows > 1 ? o.ld : 0, o.rows, o.cols, copy, wide);
-        const int rc = launch_status("gated feed-forward: aligned copy");
-        if (rc != ZERO1_OK) return rc;
-        p = copy;
-        ld = cols = wide;
+    const int64_t cols = copy ? copy->wide : o.cols, ld = copy ? copy->wide : o.rows > 1 ? o.ld : round_up(o.cols, 8);
+    return make_map(c.name, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, copy ? copy->dst : o.p, o.rows, cols, ld, 64, o.what, box_rows);
+}
+
+// The maps of a product's operands, after one launch that copies those that TMA
+// cannot address.
+int operand_maps(const Call &c, int b_rows, char *scratch, Maps *maps, int sms, cudaStream_t st)
+{
+    const Operand *ops[4] = {c.a, c.b, c.na > 1 ? c.a + 1 : nullptr, c.nb > 1 ? c.b + 1 : nullptr};
+    CUtensorMap *to[4] = {&maps->a0, &maps->b0, &maps->a1, &maps->b1};
+    AlignCopies all{};
+    const AlignCopy *copy[4] = {};
+    for (int k = 0; k < 4; ++k) {
+        if (!ops[k] || usable(*ops[k])) continue;
+        const Operand &o = *ops[k];
+        AlignCopy &q = all.m[all.count++];
+        q = AlignCopy{static_cast<const uint16_t *>(o.p), reinterpret_cast<uint16_t *>(scratch), o.rows > 1 ? o.ld : 0, o.rows, o.cols,
+                      round_up(o.cols, 8), (o.cols + kCopyCols - 1) / kCopyCols, 0};
+        scratch += copy_bytes(o);
+        all.items += o.rows * q.segments;
+        q.end = all.items;
+        copy[k] = &q;
     }
-    return make_map(c.name, map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, o.rows, cols, ld, 64, o.what, box_rows);
+    if (all.count) {
+        const int64_t need = (all.items + 7) / 8, wave = (int64_t)sms * 8;
+        const cudaError_t e = launch_after(k_align_operands, dim3((unsigned)(need < wave ? need : wave)), 256, 0, st, all);
+        if (e != cudaSuccess) return pdl_fail(e, "gated feed-forward: aligned copies");
+    }
+    for (int k = 0; k < 4; ++k) {
+        if (!ops[k]) continue;
+        const int rc = operand_map(c, *ops[k], ops[k]->across ? kDeep : k % 2 ? b_rows : 128, copy[k], to[k]);
+        if (rc != ZERO1_OK) return rc;
+    }
+    return ZERO1_OK;
 }
 
 int out_map(const Call &c, const Out &o, int64_t M, int64_t N, bool f32, CUtensorMap *map, const char *what)
@@ -763,11 +873,7 @@ int launch(const Call &c, Mm &a, void *workspace, cudaStream_t st)
     int rc;
     if (p.kblocks > 0) {
         Maps maps{};
-        char *scratch = static_cast<char *>(workspace) + p.bytes;
-        for (int k = 0; k < c.na; ++k)
-            if ((rc = operand_map(c, c.a[k], c.a[k].across ? kDeep : 128, &scratch, k ? &maps.a1 : &maps.a0, st))) return rc;
-        for (int k = 0; k < c.nb; ++k)
-            if ((rc = operand_map(c, c.b[k], c.b[k].across ? kDeep : TN / 2, &scratch, k ? &maps.b1 : &maps.b0, st))) return rc;
+        if ((rc = operand_maps(c, TN / 2, static_cast<char *>(workspace) + p.bytes, &maps, 2 * p.clusters, st))) return rc;
         if ((rc = out_map(c, a.out[0], c.M, c.N, a.out_f32, &maps.out0, "the results")) ||
             (rc = out_map(c, a.out[1], c.M, c.N, false, &maps.out1, "du")) ||
             (rc = out_map(c, a.out[2], c.M, c.N, false, &maps.out2, "a")))

@@ -5,8 +5,12 @@
 
 namespace {
 
-// Adds the blocks' partial column sums in block order: 32 columns per block, 8
-// slices of the partials each summed in order and then joined in order.
+// Adds the blocks' partial column sums in block order: 32 columns per block, 32
+// slices of the partials each summed in order and then joined in order.  The
+// partials were just written and come from L2; all of a slice's loads are under way
+// together (8 slices took three times as long).
+constexpr int kSlices = 32;
+
 struct LnFinish {
     const float *part;
     int64_t nparts;
@@ -14,26 +18,30 @@ struct LnFinish {
     void *out[2];  // dw, db (NULL: not wanted)
 };
 
-__global__ void __launch_bounds__(256) k_layer_norm_finish(const LnFinish f)
+__global__ void __launch_bounds__(32 * kSlices) k_layer_norm_finish(const LnFinish f)
 {
     wait_prior_grid();
-    __shared__ float sum[8][32];
+    let_next_grid_start();
+    __shared__ float sum[kSlices][33];
     const int s = blockIdx.y;
     if (!f.out[s]) return;
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+    int col = blockIdx.x * 32 + lane;
     const float *p = f.part + (int64_t)s * f.nparts * f.D + col;
-    const int64_t per = (f.nparts + 7) / 8, b = slice * per, e = b + per < f.nparts ? b + per : f.nparts;
+    const int per = (int)((f.nparts + kSlices - 1) / kSlices), b = slice * per, e = min(b + per, (int)f.nparts);
     float x = 0.f;
     if (col < f.D) {
-#pragma unroll 8
-        for (int64_t q = b; q < e; ++q) x += p[q * f.D];
+#pragma unroll 20
+        for (int q = b; q < e; ++q) x += __ldcg(p + (int64_t)q * f.D);
     }
     sum[slice][lane] = x;
     __syncthreads();
-    if (slice || col >= f.D) return;
+    // a warp joins 32 slices of a column, in order of a tree
+    x = sum[lane][slice];
 #pragma unroll
-    for (int q = 1; q < 8; ++q) x += sum[q][lane];
+    for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    col = blockIdx.x * 32 + slice;
+    if (lane || col >= f.D) return;
     if (f.f32) {
         float *o = static_cast<float *>(f.out[s]) + col;
         *o = f.accumulate ? *o + x : x;
@@ -207,7 +215,7 @@ extern "C" int zero1_layer_norm_backward(const zero1_layer_norm_t *cfg, const ze
     f.accumulate = cfg->accumulate != 0;
     f.out[0] = io->dw;
     f.out[1] = io->db;
-    const cudaError_t e = launch_after(k_layer_norm_finish, dim3((unsigned)((D + 31) / 32), 2), 256, 0, st, f);
+    const cudaError_t e = launch_after(k_layer_norm_finish, dim3((unsigned)((D + 31) / 32), 2), 32 * kSlices, 0, st, f);
     if (e != cudaSuccess) return pdl_fail(e, "layer norm backward: column sums");
     return ZERO1_OK;
 }

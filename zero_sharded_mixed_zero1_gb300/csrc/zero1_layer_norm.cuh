@@ -74,15 +74,97 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2 *red)
     return s;
 }
 
-// keep_vector, `without` where there is none.
-template <int T, int C>
+// How a row's columns are shared out over a block, in chunks of eight per thread.
+// kAligned: eight consecutive ones, in 128-bit accesses; kAnywhere: the same at any
+// element offset, by the words that hold them; kLanes: fp32 rows at any offset
+// without a checkpoint, a thread's columns 16 apart, so that 16 lanes copy and
+// store 64 consecutive bytes (2003 x 1021, backward: 10 us, where words of eight
+// consecutive columns per thread took 17).
+constexpr int kAnywhere = 0, kAligned = 1, kLanes = 2;
+
+template <int T, int LAY>
+struct Cols {
+    using Ld = Row<T, LAY == kAligned>;
+    static __device__ __forceinline__ int col(int i)
+    {
+        return LAY == kLanes ? chunk_col<false>(i, threadIdx.x, T) : threadIdx.x * 8 + i * T * 8;
+    }
+    template <int E>
+    static __host__ __device__ constexpr int bytes(int n)
+    {
+        return LAY == kLanes ? n * E : Ld::template bytes<E>(n);
+    }
+    template <int E>
+    static __device__ __forceinline__ void copy(unsigned char *region, int i, const void *row, int D, bool first)
+    {
+        if constexpr (LAY == kLanes) {
+            const float *src = static_cast<const float *>(row);
+            const uint32_t d = (uint32_t)__cvta_generic_to_shared(region) + (i * 8 * T + threadIdx.x) * 4;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = col(i) + 16 * k, n = c < D ? 4 : 0;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 4 * T * k), "l"(n ? src + c : src), "r"(n) : "memory");
+            }
+        } else {
+            Ld::template copy<E>(region, i, row, col(i), D, first);
+        }
+    }
+    template <class V>
+    static __device__ __forceinline__ V8 take(const unsigned char *region, int i, const V *row)
+    {
+        if constexpr (LAY == kLanes) {
+            const float *f = reinterpret_cast<const float *>(region) + i * 8 * T + threadIdx.x;
+            return V8{{pair(f[0], f[T]), pair(f[2 * T], f[3 * T]), pair(f[4 * T], f[5 * T]), pair(f[6 * T], f[7 * T])}};
+        } else {
+            return Ld::template take<V>(region, i, row);
+        }
+    }
+    template <class V>
+    static __device__ __forceinline__ void put(V *row, int i, int D, const V8 &v)
+    {
+        if constexpr (LAY == kLanes) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 f = split(v.p[k]);
+                const int c = col(i) + 32 * k;
+                if (c < D) __stcs(row + c, f.x);
+                if (c + 16 < D) __stcs(row + c + 16, f.y);
+            }
+        } else {
+            Ld::put(row, col(i), D, v);
+        }
+    }
+    // The values below column D, zeros beyond.
+    static __device__ __forceinline__ V8 inside(const V8 &v, int i, int D)
+    {
+        if constexpr (LAY == kAligned) return v;
+        if constexpr (LAY == kAnywhere) return below(v, col(i), D);
+        V8 r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = split(v.p[k]);
+            const int c = col(i) + 32 * k;
+            r.p[k] = pair(c < D ? f.x : 0.f, c + 16 < D ? f.y : 0.f);
+        }
+        return r;
+    }
+};
+
+// Keeps a [D] vector in shared memory as fp32 values, as keep_vector does and in
+// the columns' layout; `without` where there is none.
+template <int T, int C, int LAY>
 __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, int f32, int D, float without)
 {
-    if (src) return keep_vector<T, C>(kept, src, f32, D, 0);
+    if (src && LAY != kLanes) return keep_vector<T, C>(kept, src, f32, D, 0);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = without;
+        if (src) param8<false>(src, f32, 0, 0, Cols<T, LAY>::col(i), D, f);
         float4 *q = reinterpret_cast<float4 *>(kept) + i * T + threadIdx.x;
-        q[0] = q[C * T] = make_float4(without, without, without, without);
+        q[0] = make_float4(f[0], f[1], f[2], f[3]);
+        q[C * T] = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -99,37 +181,38 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // MIX: 1 y and a checkpoint, 2 y and no checkpoint, 3 neither, 0 decided at run
 // time.  FULL: the row has exactly 8 C T columns.
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, bool AL>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
 __global__ void __launch_bounds__(T, kOwnRegs / T)
 k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_bytes)
 {
-    using Ld = Row<T, AL>;
+    using Ld = Cols<T, LAY>;
     constexpr int A = sizeof(TA), B = sizeof(TR), N = 8 * C * T, kVector = N * 4;
     constexpr int at_x = 0, at_y = Ld::template bytes<B>(N);
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float red[2][2][16];  // by the row's parity and sum
     const int tid = threadIdx.x;
-    const bool res = MIX ? MIX != 3 : a.y != nullptr, r8 = MIX ? MIX == 1 : a.r8.codes != nullptr;
+    const bool res = MIX ? MIX != 3 : a.y != nullptr, r8 = LAY != kLanes && (MIX ? MIX == 1 : a.r8.codes != nullptr);
     unsigned char *kept = smem;  // w, b
     unsigned char *ring = smem + 2 * kVector;
-    auto in = [&](int i) { return FULL || tid * 8 + i * T * 8 < a.D; };
+    auto in = [&](int i) { return FULL || Ld::col(i) < a.D; };
     auto fetch = [&](int64_t row, unsigned char *to) {
         if (row < a.rows) {
             const TR *x = static_cast<const TR *>(a.x) + row * a.ld_x;
             const TA *y = static_cast<const TA *>(a.y) + row * a.ld_y;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const int col = tid * 8 + i * T * 8;
                 if (!in(i)) continue;
-                Ld::template copy<B>(to + at_x, i, x, col, a.D, row * a.ld_x == 0);
-                if (res) Ld::template copy<A>(to + at_y, i, y, col, a.D, row * a.ld_y == 0);
+                Ld::template copy<B>(to + at_x, i, x, a.D, row * a.ld_x == 0);
+                if (res) Ld::template copy<A>(to + at_y, i, y, a.D, row * a.ld_y == 0);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    wait_prior_grid();
+    let_next_grid_start();
     for (int k = 0; k + 1 < stages; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, ring + k * stage_bytes);
-    keep_or<T, C>(kept, a.w, a.pf32, a.D, 1.f);
-    keep_or<T, C>(kept + kVector, a.b, a.pf32, a.D, 0.f);
+    keep_or<T, C, LAY>(kept, a.w, a.pf32, a.D, 1.f);
+    keep_or<T, C, LAY>(kept + kVector, a.b, a.pf32, a.D, 0.f);
 
     int st = 0, flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -147,7 +230,7 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
             v[i] = Ld::take(p + at_x, i, static_cast<const TR *>(a.x) + row * a.ld_x);
             if (res) {
                 v[i] = fma8(Ld::take(p + at_y, i, static_cast<const TA *>(a.y) + row * a.ld_y), a.alpha, v[i]);
-                Ld::put(r, tid * 8 + i * T * 8, a.D, v[i]);
+                Ld::put(r, i, a.D, v[i]);
             }
             s += sum8(v[i]);
         }
@@ -157,7 +240,7 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
         for (int i = 0; i < C; ++i) {
             if (!in(i)) continue;
             v[i] = plus8(v[i], -mean);
-            if (!AL) v[i] = below(v[i], tid * 8 + i * T * 8, a.D);
+            v[i] = Ld::inside(v[i], i, a.D);
             s += dot8(v[i], v[i]);
         }
         const float rstd = rsqrtf(fmaf(block_sum<T>(s, red[flip][1]), a.inv_d, a.eps));
@@ -168,9 +251,9 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
         TA *h = static_cast<TA *>(a.h) + row * a.ld_h;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int col = tid * 8 + i * T * 8;
             v[i] = mul8(v[i], rstd);
             if (r8) {
+                const int col = Ld::col(i);
                 int E;
                 const uint2 q = encode8(v[i], E);
                 if (FULL || col / kQBlock * kQBlock < a.D) {
@@ -178,7 +261,7 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
                     if ((tid & 15) == 0) a.r8.exps[(int64_t)(col / kQBlock) * a.r8.ld_exps + row] = (uint8_t)E;
                 }
             }
-            if (in(i)) Ld::put(h, col, a.D, fma8(v[i], kept8<T, C>(kept, i), kept8<T, C>(kept + kVector, i)));
+            if (in(i)) Ld::put(h, i, a.D, fma8(v[i], kept8<T, C>(kept, i), kept8<T, C>(kept + kVector, i)));
         }
         flip ^= 1;
         if (++st == stages) st = 0;
@@ -194,6 +277,8 @@ __global__ void __launch_bounds__(1024) k_layer_norm_fwd(const z1ln::Fwd a)
     __shared__ float red[2][2][32];
     const int tid = threadIdx.x, nthr = blockDim.x;
     int flip = 0;
+    wait_prior_grid();
+    let_next_grid_start();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         Chunk<TR, VEC> xq[C];
         Chunk<TA, VEC> yq[C];
@@ -296,9 +381,9 @@ struct LnWords {
     }
 };
 
-template <class TA, class TR, int T, int C, int MIX, bool AL>
+template <class TA, class TR, int T, int C, int MIX, int LAY>
 struct LnStage {
-    using Ld = Row<T, AL>;
+    using Ld = Cols<T, LAY>;
     static constexpr int n = 8 * C * T;
     static constexpr int A = Ld::template bytes<sizeof(TA)>(n), B = Ld::template bytes<sizeof(TR)>(n);
     static constexpr int dh = 0, dr = dh + A, r = dr + (MIX == 3 ? 0 : B), words = r + (MIX == 1 ? n : B);
@@ -306,19 +391,19 @@ struct LnStage {
     static constexpr int bytes = words + T / 32 * words_bytes;
 };
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, bool AL>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
 __global__ void __launch_bounds__(T, kOwnRegs / T)
 k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
 {
-    using S = LnStage<TA, TR, T, C, MIX, AL>;
-    using Ld = Row<T, AL>;
+    using S = LnStage<TA, TR, T, C, MIX, LAY>;
+    using Ld = Cols<T, LAY>;
     constexpr int A = sizeof(TA), B = sizeof(TR), kVector = S::n * 4;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 red[2][16];
     const int tid = threadIdx.x;
-    const bool has_dr = MIX ? MIX != 3 : a.dr != nullptr, r8 = MIX ? MIX == 1 : a.r8.codes != nullptr;
+    const bool has_dr = MIX ? MIX != 3 : a.dr != nullptr, r8 = LAY != kLanes && (MIX ? MIX == 1 : a.r8.codes != nullptr);
     unsigned char *kept = smem, *ring = smem + kVector;
-    auto in = [&](int i) { return FULL || tid * 8 + i * T * 8 < a.D; };
+    auto in = [&](int i) { return FULL || Ld::col(i) < a.D; };
     const LnWords<T, C> row_words(a);
     auto words_of = [&](unsigned char *stage) { return reinterpret_cast<uint32_t *>(stage + S::words + tid / 32 * S::words_bytes); };
 
@@ -331,18 +416,19 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
             const void *r = r8 ? (const void *)(a.r8.codes + row * a.r8.ld_codes) : (const void *)(static_cast<const TR *>(a.r) + row * a.ld_r);
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const int col = tid * 8 + i * T * 8;
                 if (!in(i)) continue;
-                Ld::template copy<A>(to + S::dh, i, dh, col, a.D, row * a.ld_dh == 0);
-                if (r8) copy8_ahead<1>(to + S::r + chunk_at<T, 1>(i), r, col);
-                else Ld::template copy<B>(to + S::r, i, r, col, a.D, row * a.ld_r == 0);
-                if (has_dr) Ld::template copy<B>(to + S::dr, i, dr, col, a.D, row * a.ld_dr == 0);
+                Ld::template copy<A>(to + S::dh, i, dh, a.D, row * a.ld_dh == 0);
+                if (r8) copy8_ahead<1>(to + S::r + chunk_at<T, 1>(i), r, Ld::col(i));
+                else Ld::template copy<B>(to + S::r, i, r, a.D, row * a.ld_r == 0);
+                if (has_dr) Ld::template copy<B>(to + S::dr, i, dr, a.D, row * a.ld_dr == 0);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    wait_prior_grid();
+    let_next_grid_start();
     for (int k = 0; k + 1 < stages; ++k) fetch(blockIdx.x + (int64_t)k * gridDim.x, ring + k * S::bytes);
-    keep_or<T, C>(kept, a.w, a.pf32, a.D, 1.f);
+    keep_or<T, C, LAY>(kept, a.w, a.pf32, a.D, 1.f);
     V8 acc_w[C], acc_b[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) acc_w[i] = acc_b[i] = splat8(0.f);
@@ -365,7 +451,7 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
             d[i] = Ld::take(p + S::dh, i, static_cast<const TA *>(a.dh) + row * a.ld_dh);
             if (r8) h[i] = take_codes(p + S::r + chunk_at<T, 1>(i), row_words.scale(words, row, i));
             else h[i] = mul8(plus8(Ld::take(p + S::r, i, static_cast<const TR *>(a.r) + row * a.ld_r), -mean), rstd);
-            if (!AL) h[i] = below(h[i], tid * 8 + i * T * 8, a.D);
+            h[i] = Ld::inside(h[i], i, a.D);
             acc_w[i] = fma8(d[i], h[i], acc_w[i]);
             acc_b[i] = add8(acc_b[i], d[i]);
             d[i] = mul8(d[i], kept8<T, C>(kept, i));
@@ -379,13 +465,12 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
         TA *dy = static_cast<TA *>(a.dy) + row * a.ld_dy;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int col = tid * 8 + i * T * 8;
             if (!in(i)) continue;
             const V8 x = plus8(fma8(h[i], t, d[i]), s);
             if (has_dr) d[i] = fma8(x, rstd, Ld::take(p + S::dr, i, static_cast<const TR *>(a.dr) + row * a.ld_dr));
             else d[i] = mul8(x, rstd);
-            Ld::put(dx, col, a.D, d[i]);
-            if (a.dy) Ld::put(dy, col, a.D, mul8(d[i], a.alpha));
+            Ld::put(dx, i, a.D, d[i]);
+            if (a.dy) Ld::put(dy, i, a.D, mul8(d[i], a.alpha));
         }
         flip ^= 1;
         if (++st == stages) st = 0;
@@ -395,9 +480,13 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         if (!in(i)) continue;
-        const int col = tid * 8 + i * T * 8;
-        if (a.need_w) put8_any(part, col, a.D, acc_w[i]);
-        if (a.need_b) put8_any(part + plane, col, a.D, acc_b[i]);
+        if constexpr (LAY == kLanes) {
+            if (a.need_w) Ld::put(part, i, a.D, acc_w[i]);
+            if (a.need_b) Ld::put(part + plane, i, a.D, acc_b[i]);
+        } else {
+            if (a.need_w) put8_any(part, Ld::col(i), a.D, acc_w[i]);
+            if (a.need_b) put8_any(part + plane, Ld::col(i), a.D, acc_b[i]);
+        }
     }
 }
 
@@ -426,6 +515,8 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
         else acc[s][i][k] += x;
     };
     int flip = 0;
+    wait_prior_grid();
+    let_next_grid_start();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         Chunk<TA, VEC> hq[C];
         Chunk<TR, VEC> rq[C], dq[C];
@@ -501,11 +592,11 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
 
 // -------------------------------------------------------------- launch -----
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, bool AL>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
 bool ln_fwd_staged(const z1ln::Fwd &a, int sms, cudaStream_t st, int *rc)
 {
-    auto kernel = k_layer_norm_fwd_staged<TA, TR, T, C, MIX, FULL, AL>;
-    using Ld = Row<T, AL>;
+    auto kernel = k_layer_norm_fwd_staged<TA, TR, T, C, MIX, FULL, LAY>;
+    using Ld = Cols<T, LAY>;
     constexpr int N = 8 * C * T, kept = 2 * N * 4;
     const int stage = Ld::template bytes<sizeof(TR)>(N) + (a.y ? Ld::template bytes<sizeof(TA)>(N) : 0);
     const int stages = stages_that_fit(T, kept, stage);
@@ -517,9 +608,9 @@ bool ln_fwd_staged(const z1ln::Fwd &a, int sms, cudaStream_t st, int *rc)
         return true;
     }
     const int64_t wave = (int64_t)sms * (kOwnRegs / T), grid = a.rows < wave ? a.rows : wave;
-    kernel<<<(unsigned)grid, T, kept + stages * stage, st>>>(a, stages, stage);
+    const cudaError_t le = launch_after(kernel, dim3((unsigned)grid), T, kept + stages * stage, st, a, stages, stage);
     z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, kOwnRegs / T, T, 0);
-    *rc = launch_status("layer norm forward launch");
+    *rc = le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm forward launch");
     return true;
 }
 
@@ -530,14 +621,17 @@ bool ln_forward_staged(const z1ln::Fwd &a, bool vec, int sms, cudaStream_t st, i
     const int mix = a.y ? (a.r8.codes ? 1 : 2) : (a.r8.codes ? 0 : 3);
     return pick_threads(a.D, [&](auto t, auto n) {
         constexpr int T = decltype(t)::value, C = decltype(n)::value;
-        if (!vec) return ln_fwd_staged<TA, TR, T, C, 0, false, false>(a, sms, st, rc);
+        if constexpr (sizeof(TA) == 4) {
+            if (!vec && !a.r8.codes) return ln_fwd_staged<TA, TR, T, C, 0, false, kLanes>(a, sms, st, rc);
+        }
+        if (!vec) return ln_fwd_staged<TA, TR, T, C, 0, false, kAnywhere>(a, sms, st, rc);
         if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
             const int m = a.D == 8 * C * T ? mix : 0;
-            if (m == 1) return ln_fwd_staged<TA, TR, T, C, 1, true, true>(a, sms, st, rc);
-            if (m == 2) return ln_fwd_staged<TA, TR, T, C, 2, true, true>(a, sms, st, rc);
-            if (m == 3) return ln_fwd_staged<TA, TR, T, C, 3, true, true>(a, sms, st, rc);
+            if (m == 1) return ln_fwd_staged<TA, TR, T, C, 1, true, kAligned>(a, sms, st, rc);
+            if (m == 2) return ln_fwd_staged<TA, TR, T, C, 2, true, kAligned>(a, sms, st, rc);
+            if (m == 3) return ln_fwd_staged<TA, TR, T, C, 3, true, kAligned>(a, sms, st, rc);
         }
-        return ln_fwd_staged<TA, TR, T, C, 0, false, true>(a, sms, st, rc);
+        return ln_fwd_staged<TA, TR, T, C, 0, false, kAligned>(a, sms, st, rc);
     });
 }
 
@@ -547,16 +641,16 @@ int ln_fwd_direct(const z1ln::Fwd &a, int sms, cudaStream_t st)
     auto kernel = k_layer_norm_fwd<TA, TR, VEC>;
     const int threads = row_threads(a.D), per_sm = blocks_per_sm(reinterpret_cast<const void *>(kernel), threads);
     const int64_t grid = a.rows < (int64_t)sms * per_sm ? a.rows : (int64_t)sms * per_sm;
-    kernel<<<(unsigned)grid, threads, 0, st>>>(a);
+    const cudaError_t le = launch_after(kernel, dim3((unsigned)grid), threads, 0, st, a);
     z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, per_sm, threads, 0);
-    return launch_status("layer norm forward launch");
+    return le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm forward launch");
 }
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, bool AL>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
 bool ln_bwd_staged(const z1ln::Bwd &a, int64_t grid, cudaStream_t st, int *rc)
 {
-    auto kernel = k_layer_norm_bwd_staged<TA, TR, T, C, MIX, FULL, AL>;
-    using S = LnStage<TA, TR, T, C, MIX, AL>;
+    auto kernel = k_layer_norm_bwd_staged<TA, TR, T, C, MIX, FULL, LAY>;
+    using S = LnStage<TA, TR, T, C, MIX, LAY>;
     const int stages = stages_that_fit(T, S::n * 4, S::bytes);
     if (stages == 0) return false;
     static std::atomic<uint64_t> done{0};
@@ -565,9 +659,9 @@ bool ln_bwd_staged(const z1ln::Bwd &a, int64_t grid, cudaStream_t st, int *rc)
         *rc = z1_fail(ZERO1_ECUDA, "layer norm backward: %s", cudaGetErrorString(e));
         return true;
     }
-    kernel<<<(unsigned)grid, T, S::n * 4 + stages * S::bytes, st>>>(a, stages);
+    const cudaError_t le = launch_after(kernel, dim3((unsigned)grid), T, S::n * 4 + stages * S::bytes, st, a, stages);
     z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, kOwnRegs / T, T, 0);
-    *rc = launch_status("layer norm backward launch");
+    *rc = le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm backward launch");
     return true;
 }
 
@@ -578,14 +672,17 @@ bool ln_backward_staged(const z1ln::Bwd &a, bool vec, int64_t grid, cudaStream_t
     const int mix = a.dr ? (a.r8.codes ? 1 : 2) : (a.r8.codes ? 0 : 3);
     return pick_threads(a.D, [&](auto t, auto n) {
         constexpr int T = decltype(t)::value, C = decltype(n)::value;
-        if (!vec) return ln_bwd_staged<TA, TR, T, C, 0, false, false>(a, grid, st, rc);
+        if constexpr (sizeof(TA) == 4) {
+            if (!vec && !a.r8.codes) return ln_bwd_staged<TA, TR, T, C, 0, false, kLanes>(a, grid, st, rc);
+        }
+        if (!vec) return ln_bwd_staged<TA, TR, T, C, 0, false, kAnywhere>(a, grid, st, rc);
         if constexpr (sizeof(TA) == 2 && !(T == 512 && C == 1)) {
             const int m = a.D == 8 * C * T ? mix : 0;
-            if (m == 1) return ln_bwd_staged<TA, TR, T, C, 1, true, true>(a, grid, st, rc);
-            if (m == 2) return ln_bwd_staged<TA, TR, T, C, 2, true, true>(a, grid, st, rc);
-            if (m == 3) return ln_bwd_staged<TA, TR, T, C, 3, true, true>(a, grid, st, rc);
+            if (m == 1) return ln_bwd_staged<TA, TR, T, C, 1, true, kAligned>(a, grid, st, rc);
+            if (m == 2) return ln_bwd_staged<TA, TR, T, C, 2, true, kAligned>(a, grid, st, rc);
+            if (m == 3) return ln_bwd_staged<TA, TR, T, C, 3, true, kAligned>(a, grid, st, rc);
         }
-        return ln_bwd_staged<TA, TR, T, C, 0, false, true>(a, grid, st, rc);
+        return ln_bwd_staged<TA, TR, T, C, 0, false, kAligned>(a, grid, st, rc);
     });
 }
 
@@ -599,9 +696,9 @@ int ln_bwd_direct(const z1ln::Bwd &a, int64_t grid, cudaStream_t st)
         const cudaError_t e = allow_smem(kernel, 2 * 16 * 1024 * 4, done);
         if (e != cudaSuccess) return z1_fail(ZERO1_ECUDA, "layer norm backward: %s", cudaGetErrorString(e));
     }
-    kernel<<<(unsigned)grid, threads, smem, st>>>(a);
+    const cudaError_t le = launch_after(kernel, dim3((unsigned)grid), threads, smem, st, a);
     z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, 1, threads, 0);
-    return launch_status("layer norm backward launch");
+    return le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm backward launch");
 }
 
 }  // namespace
@@ -620,5 +717,5 @@ int z1ln::run_backward(const Bwd &a, bool vec, int64_t grid, cudaStream_t st)
     int rc;
     if (ln_backward_staged<TA, TR>(a, vec, grid, st, &rc)) return rc;
     if (a.D <= 8192) return vec ? ln_bwd_direct<TA, TR, true, false>(a, grid, st) : ln_bwd_direct<TA, TR, false, false>(a, grid, st);
-    return vec ? ln_bwd_direct<TA, TR, true, true>(a, grid, st) : ln_bwd_direct<TA, TR, false, true>(a, grid, st);
+    return vec ? ln_bwd_direct<TA, TR, true, kAligned>(a, grid, st) : ln_bwd_direct<TA, TR, false, true>(a, grid, st);
 }

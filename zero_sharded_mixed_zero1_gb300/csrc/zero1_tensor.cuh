@@ -151,6 +151,13 @@ __device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bo
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
+// All boxes that this warp has sent have been read from shared memory.
+__device__ __forceinline__ void boxes_read()
+{
+    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
 // All boxes that this warp has sent are written.
 __device__ __forceinline__ void boxes_written()
 {
@@ -159,15 +166,6 @@ __device__ __forceinline__ void boxes_written()
 }
 
 // ------------------------------------------------------------- matrices ----
-
-// Copies a matrix to rows that start on 16-byte boundaries, eight elements per thread.
-__global__ void __launch_bounds__(256)
-k_align_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t T, int64_t N, uint16_t *__restrict__ dst, int64_t ld_dst)
-{
-    for (int64_t c = ((int64_t)blockIdx.y * 32 + threadIdx.x % 32) * 8; c < N; c += (int64_t)gridDim.y * 256)
-        for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; t < T; t += (int64_t)gridDim.x * 8)
-            *reinterpret_cast<uint4 *>(dst + t * ld_dst + c) = load8_any(src + t * ld, c, N, t * ld == 0);
-}
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,

@@ -713,6 +713,15 @@ __global__ void __launch_bounds__(256) k_weight_grad_join(const Wg a)
     }
 }
 
+// Copies dy to rows that start on 16-byte boundaries, eight elements per thread.
+__global__ void __launch_bounds__(256)
+k_align_rows(const uint16_t *__restrict__ src, int64_t ld, int64_t T, int64_t N, uint16_t *__restrict__ dst, int64_t ld_dst)
+{
+    for (int64_t c = ((int64_t)blockIdx.y * 32 + threadIdx.x % 32) * 8; c < N; c += (int64_t)gridDim.y * 256)
+        for (int64_t t = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; t < T; t += (int64_t)gridDim.x * 8)
+            *reinterpret_cast<uint4 *>(dst + t * ld_dst + c) = load8_any(src + t * ld, c, N, t * ld == 0);
+}
+
 // --------------------------------------------------------------- launch ----
 
 int plan_of(int64_t T, int64_t N, int64_t K, const void *dy, int64_t ld, Plan *p)

@@ -15,7 +15,7 @@ import torch
 
 from . import block as _block
 from ._lib import _check_rc
-from .block import _code, _dims, _launch_stream, _matrix, _workspace
+from .block import _call_with, _code, _dims, _matrix
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 _ACTS = {"silu": 0, "gelu": 1}
@@ -57,8 +57,7 @@ def _call(fn, kind: int, act: str, rows: int, d: int, f: int, h, w_gate, w_up, d
         need = _i64()
         _check_rc(lib.zero1_gated_ffn_workspace(c, kind, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
-    _check_rc(fn(c, ws, nbytes, _launch_stream(stream)))
+    _check_rc(_call_with(workspace, nbytes, stream, fn, c))
 
 
 def _shapes(x, w_gate, what: str) -> tuple[int, int, int]:
@@ -147,6 +146,5 @@ def zero1_weight_grad_bf16(dy, x, dw, *, accumulate: bool = False, workspace: to
         need = _i64()
         _check_rc(lib.zero1_weight_grad_bf16_workspace(rows, n, k, pdy, ldy, px, lx, code, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
-    _check_rc(lib.zero1_weight_grad_bf16(pdy, ldy, n, px, lx, k, rows, pw, lw, code, 1 if accumulate else 0, ws, nbytes,
-                                         _launch_stream(stream)))
+    _check_rc(_call_with(workspace, nbytes, stream, lib.zero1_weight_grad_bf16, pdy, ldy, n, px, lx, k, rows, pw, lw, code,
+                         1 if accumulate else 0))

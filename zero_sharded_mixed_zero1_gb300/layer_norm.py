@@ -16,7 +16,7 @@ import torch
 
 from . import block as _block
 from ._lib import ZERO1_DTYPE_BF16, _check_rc
-from .block import Checkpoint8, _ckpt, _code, _dims, _launch_stream, _matrix, _optional, _vector, _workspace
+from .block import Checkpoint8, _call_with, _ckpt, _code, _dims, _launch_stream, _matrix, _optional, _vector
 
 _vp, _i64 = ctypes.c_void_p, ctypes.c_int64
 _CFG = struct.Struct("=qqff5i4x")  # zero1_layer_norm_t
@@ -116,5 +116,4 @@ def zero1_layer_norm_backward(cfg: LayerNorm, dh, dr, r, mean, rstd, dx, *, dy=N
         need = _i64()
         _check_rc(lib.zero1_layer_norm_workspace(c, ctypes.addressof(need)))
         nbytes = need.value
-    ws, nbytes, keep = _workspace(workspace, nbytes, stream)
-    _check_rc(lib.zero1_layer_norm_backward(c, io, ws, nbytes, _launch_stream(stream)))
+    _check_rc(_call_with(workspace, nbytes, stream, lib.zero1_layer_norm_backward, c, io))
