@@ -8,10 +8,27 @@ A, B = math.sqrt(2.0 / math.pi), 0.044715
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 # The largest slopes of act and of act' (silu: 1.0999 and 0.5; gelu: 1.1290 and 0.8142).
 SLOPE, CURVE = 1.13, 0.82
-# The activation's own arithmetic in fp32: k(g) by three roundings, its logistic
-# function and slope within 16 half steps, three more products.
-OWN = 32 * 2.0 ** -24
 TINY = 2.0 ** -126
+
+
+HALF_STEP = 2.0 ** -24
+
+
+def own(g: torch.Tensor, act: str):
+    """What the activation's own arithmetic in fp32 adds: the relative error of f = g
+    s(k) and the absolute one of f' = s + g k' (s - s^2).  k by up to four roundings
+    and t = k log2 e by one more, of a constant that is rounded too: 6 half steps of k,
+    which 2^t turns into 6 |k| half steps of e; 2^t itself 4.  In s = e / (1 + e) an error
+    of e counts 1 - s times; 1 + e, 1 / x and the product are good for 6 half steps, none
+    where t is cut at 64 and all three are exact.  s - s^2 moves with s by at most 1 times
+    and is rounded once, as are its product and the sum."""
+    k = g if act == "silu" else 2 * A * (g + B * g.pow(3))
+    gdk = g if act == "silu" else 2 * A * (g + 3 * B * g.pow(3))
+    s, rest = torch.sigmoid(k), torch.sigmoid(-k)
+    es = ((6 * k.abs().clamp(max=110) + 4) * rest + torch.where(k > 44.5, 0.0, 6.0)) * HALF_STEP
+    slope = s * rest
+    edf = s * es + gdk.abs() * (s * es + HALF_STEP * slope) + 8 * HALF_STEP * (s + gdk.abs() * slope)
+    return es + 2 * HALF_STEP, 1.01 * edf
 
 
 def sum_bound(terms: int, size: torch.Tensor) -> torch.Tensor:
@@ -41,7 +58,7 @@ def forward(h, w_gate, w_up, act):
     """a and the bound of its error."""
     (g, eg), (u, eu) = projections(h, w_gate), projections(h, w_up)
     f, _ = activation(g, act)
-    ef = SLOPE * eg + OWN * (f.abs() + TINY)
+    ef = SLOPE * eg + own(g, act)[0] * (f.abs() + TINY)
     a = f * u
     return a, ef * u.abs() + (f.abs() + ef) * eu + HALF[torch.bfloat16] * a.abs() * 1.01 + 2.0 ** -133
 
@@ -51,9 +68,9 @@ def backward(da, h, w_gate, w_up, act):
     (g, eg), (u, eu) = projections(h, w_gate), projections(h, w_up)
     f, df = activation(g, act)
     d = da.double()
-    ef = SLOPE * eg + OWN * (f.abs() + TINY)
-    # act' is a sum of s and g s (1 - s) k', each within OWN of itself; |g| s (1 - s) k' is at most 1.2
-    edf = CURVE * eg + OWN * 2.2
+    rel, edf = own(g, act)
+    ef = SLOPE * eg + rel * (f.abs() + TINY)
+    edf = CURVE * eg + edf
     dg, du = d * u * df, d * f
     r = 1.01 * HALF[torch.bfloat16]
     return ((dg, d.abs() * (edf * u.abs() + (df.abs() + edf) * eu) + r * dg.abs() + 2.0 ** -133),

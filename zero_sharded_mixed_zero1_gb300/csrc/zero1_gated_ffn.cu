@@ -33,14 +33,17 @@ constexpr int kForward = 0, kBackward = 1, kInputGrad = 2, kWeightGrad = 3;
 
 constexpr int kThreads = 32 * 12, kStoring = 8;  // storing warps
 constexpr int kABytes = 128 * kDeep * 2;
-constexpr int kRingBytes = 6 * (kABytes + 128 * kDeep * 2);
 template <int TN>
 constexpr int kStageBytes = kABytes + TN / 2 * kDeep * 2;
+
+constexpr int kRingBytes = 6 * kStageBytes<256>;
 template <int TN>
 constexpr int kStages = kRingBytes / kStageBytes<TN>;
 
-constexpr int kPlaceBytes = 32 * 64;  // 32 rows of 64 bytes, swizzled, on their way out
-constexpr int kPlaces = 2;            // of each storing warp
+// Results on their way out: 32 rows of 64 bytes, swizzled, in two places of each
+// storing warp.  (Four, for a stage less, were no faster where kBackward stores three
+// results for each pair of sums, and cost 5% at 8192 x 4096 x 14336.)
+constexpr int kPlaceBytes = 32 * 64, kPlaces = 2;
 
 struct Bars {
     uint64_t full[8], empty[8], dfull[2], dempty[2];
@@ -63,6 +66,7 @@ struct Mm {
     int64_t M, N;                     // results: rows, columns (of a, or of the gradient)
     int tiles_m, tiles_n, kblocks;    // kblocks: stages of the whole contraction
     int second;                       // the stage from which kInputGrad reads du and Wu
+    int a_bytes[2];                   // of A, per stage, that each CTA of a pair loads
     int whole, splits, per_split, run;
     int gelu;
     const uint16_t *da;
@@ -145,20 +149,30 @@ __device__ __forceinline__ int items_of(const Mm &a) { return a.whole + (a.tiles
 
 // f = act(g) = g s(k(g)) and df = act'(g) = s + g s (1 - s) k'(g), s the logistic
 // function: silu has k(g) = g, the tanh form of gelu 2 sqrt(2 / pi) (g + 0.044715 g^3).
+// With e = 2^t, t = k log2(e) cut at 64: s = e / (1 + e), right from the subnormal e of
+// very negative k on, and 1 itself from t = 64 on (2^64 and its inverse are exact), in six
+// instructions; its error is that of the product t, |k| half steps, which is nothing to
+// a bf16 result (the logistic function of the gates, good to 2.5 ulps, takes eleven; a
+// storing warp's instructions bound the backward call at small widths).  s (1 - s) is s
+// - s^2 from the rounded s: where s is near but not 1, g k' is at most 140 and a half
+// step of s counts for nothing beside the s that it is added to.
 struct Activated {
     float f, df;
     __device__ __forceinline__ Activated(float g, int gelu)
     {
         constexpr float kA = 1.5957691216f, kB = 0.0713548163f;  // 2 sqrt(2 / pi), 0.044715 of it
-        float k = g, dk = 1.f;
+        float k = g, dk = g;                                     // dk: g k'(g)
         if (gelu) {
             const float q = __fmul_rn(g, g);
             k = __fmul_rn(g, __fmaf_rn(kB, q, kA));
-            dk = __fmaf_rn(3.f * kB, q, kA);
+            dk = __fmul_rn(g, __fmaf_rn(3.f * kB, q, kA));
         }
-        const Logistic<> l(k);
-        f = __fmul_rn(g, l.s);
-        df = __fmaf_rn(__fmul_rn(g, dk), l.slope, l.s);
+        float e, r;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(__fmul_rn(k, 1.44269504f), 64.f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.f, e)));
+        const float s = __fmul_rn(e, r);
+        f = __fmul_rn(g, s);
+        df = __fmaf_rn(dk, __fmaf_rn(-s, s, s), s);
     }
 };
 
@@ -187,6 +201,8 @@ struct Leaving {
         at = at + 1 == kPlaces ? 0 : at + 1;
         return p;
     }
+    // The place that next() gave is given again.
+    __device__ __forceinline__ void again() { at = at == 0 ? kPlaces - 1 : at - 1; }
     // Every use of a place is a group, an empty one where nothing of it lies inside
     // the matrix: next() counts them.
     __device__ __forceinline__ void empty_group()
@@ -298,19 +314,58 @@ __device__ __forceinline__ void hold(float *p, bool begin, int columns, uint32_t
     }
 }
 
-// Eight bf16 values of da at a row and column, zeros outside.
-__device__ __forceinline__ uint4 load_da(const Mm &a, int64_t row, int64_t col)
+// 16 accumulator columns of g and of u, under way together.
+__device__ __forceinline__ void load_pair(uint32_t at_g, uint32_t at_u, uint32_t g[16], uint32_t u[16])
 {
-    if (row >= a.M || col >= a.N) return make_uint4(0, 0, 0, 0);
-    const uint16_t *p = a.da + row * a.ld_da + col;
-    if (a.da_vec && col + 8 <= a.N) return *reinterpret_cast<const uint4 *>(p);
-    uint32_t w[4];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+        "%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3]), "=r"(g[4]), "=r"(g[5]), "=r"(g[6]), "=r"(g[7]), "=r"(g[8]),
+          "=r"(g[9]), "=r"(g[10]), "=r"(g[11]), "=r"(g[12]), "=r"(g[13]), "=r"(g[14]), "=r"(g[15]), "=r"(u[0]), "=r"(u[1]),
+          "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]),
+          "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(at_g), "r"(at_u)
+        : "memory");
+}
+
+// da of a warp's 32 rows x 32 columns from row0, col on: four lanes to a row of 64
+// bytes, eight rows at a time (a row to each thread asked for 32 lines at once), zeros
+// outside.  take_da turns that into the thread's own row, by way of a place.
+__device__ __forceinline__ void load_da(const Mm &a, int64_t row0, int64_t col, uint4 (&d)[4])
+{
+    const int lane = threadIdx.x & 31;
+    col += lane % 4 * 8;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = col + 2 * k < a.N ? p[2 * k] : 0, hi = col + 2 * k + 1 < a.N ? p[2 * k + 1] : 0;
-        w[k] = lo | hi << 16;
+        const int64_t row = row0 + lane / 4 + 8 * k;
+        d[k] = make_uint4(0, 0, 0, 0);
+        if (row >= a.M || col >= a.N) continue;
+        const uint16_t *p = a.da + row * a.ld_da + col;
+        if (a.da_vec && col + 8 <= a.N) {
+            d[k] = *reinterpret_cast<const uint4 *>(p);
+            continue;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = col + 2 * j < a.N ? p[2 * j] : 0, hi = col + 2 * j + 1 < a.N ? p[2 * j + 1] : 0;
+            w[j] = lo | hi << 16;
+        }
+        d[k] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void take_da(const uint4 (&from)[4], uint4 (&d)[4], unsigned char *place)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4 *>(piece(place, lane / 4 + 8 * k, lane % 4)) = from[k];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[k] = *reinterpret_cast<const uint4 *>(piece(place, lane, k));
+    __syncwarp();
 }
 
 // ----------------------------------------------------------------- kernel --
@@ -324,7 +379,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
 {
     constexpr bool kDual = dual(KIND), kAAcross = KIND == kWeightGrad, kBAcross = KIND >= kInputGrad;
-    constexpr int S = kStages<TN>, kBytes = kStageBytes<TN>;
+    constexpr int S = kStages<TN>, kBytes = kStageBytes<TN>, kBBytes = kBytes - kABytes;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     unsigned char *s_places = smem + kRingBytes;
@@ -376,8 +431,9 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                 if (elect_one()) {
                     // both CTAs' loads count on the leading CTA's barrier
                     const uint32_t full = leader_addr(&bar.full[s]);
-                    if (rank == 0) mbar_expect_tx(&bar.full[s], 2 * kBytes);
-                    if (kAAcross) {
+                    if (rank == 0) mbar_expect_tx(&bar.full[s], 2 * kBBytes + a.a_bytes[0] + a.a_bytes[1]);
+                    if (a.a_bytes[rank] == 0) {
+                    } else if (kAAcross) {
                         tma_2d_pair(pa, ma, m, k, full);
                         tma_2d_pair(pa + kABytes / 2, ma, m + 64, k, full);
                     } else {
@@ -442,6 +498,13 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
         float *const held = a.held + ((int64_t)(blockIdx.x / 2) * 16 + slot) * kCols * 32 + lane;
         uint32_t fill = 0;
         bool ok = true;
+        uint4 ahead[4];  // kBackward: da of the next 32 columns, on its way while these are computed
+        auto load_ahead = [&](int i, int c) {  // of an item's columns from c on
+            if (i >= items) return;
+            const Item w = item_of(a, i);
+            load_da(a, (int64_t)w.m * kTileM + (int)rank * 128 + 32 * q, (int64_t)w.n * (TN / 2) + half * W + c, ahead);
+        };
+        if (KIND == kBackward) load_ahead(first, 0);
         for (int i = first; i < items && ok; i += step) {
             const Item w = item_of(a, i);
             const int64_t row0 = (int64_t)w.m * kTileM + (int)rank * 128 + 32 * q;
@@ -449,11 +512,6 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
             float *const part = a.part + ((int64_t)w.part * 16 + slot) * kCols * 32 + lane;
             if (kDual) {
                 const int64_t col0 = (int64_t)w.n * (TN / 2) + half * W;
-                uint4 da[KIND == kBackward ? W / 8 : 1];
-                if (KIND == kBackward && w.part < 0) {  // on their way while the products are summed
-#pragma unroll
-                    for (int k = 0; k < W / 8; ++k) da[KIND == kBackward ? k : 0] = load_da(a, row0 + lane, col0 + 8 * k);
-                }
                 if (!(ok = warp_wait(bar, &bar.dfull[fill & 1], (fill >> 1) & 1))) break;
                 tc_after();
                 uint64_t *dempty = &bar.dempty[fill & 1];
@@ -469,16 +527,22 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) __stcg(part + (c + j) * 32, __uint_as_float(v[j]));
                     }
-                    continue;
+                    continue;  // (all items behind it are parts as well: da is not needed again)
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < W; c += 32) {
                     uint32_t x[3][16];
+                    uint4 da[4];
+                    if (KIND == kBackward) {
+                        take_da(ahead, da, leaving.next());
+                        leaving.again();
+                        // of the 32 columns after these, of the next tile's after the last ones
+                        load_ahead(c + 32 < W ? i : i + step, c + 32 < W ? c + 32 : 0);
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 16) {
                         uint32_t g[16], u[16];
-                        tc_load16(acc + c + e, g);
-                        tc_load16(acc + TN / 2 + c + e, u);
+                        load_pair(acc + c + e, acc + TN / 2 + c + e, g, u);
                         if (c + e + 16 == W) release(dempty);
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
@@ -488,7 +552,7 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                             if (KIND == kForward) {
                                 x[0][at] = pack_bf16x2(__fmul_rn(f0.f, u0), __fmul_rn(f1.f, u1));
                             } else {
-                                const uint4 d4 = da[KIND == kBackward ? (c + e + j) / 8 : 0];
+                                const uint4 d4 = da[(e + j) / 8];
                                 const uint32_t d = (j / 2) % 4 == 0 ? d4.x : (j / 2) % 4 == 1 ? d4.y : (j / 2) % 4 == 2 ? d4.z : d4.w;
                                 const float d0 = bf_lo(d), d1 = bf_hi(d);
                                 x[0][at] = pack_bf16x2(__fmul_rn(__fmul_rn(d0, u0), f0.df), __fmul_rn(__fmul_rn(d1, u1), f1.df));
@@ -560,8 +624,8 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                 // a use is complete after the leading CTA's arrival and both CTAs' bytes
                 const bool announced = q < mine, there = q < other;
                 if (lane == 0)
-                    mbar_make_up(&bar.full[q % S], announced ? 0u : 1u, !announced && there ? kBytes : 0u,
-                                 announced && !there ? kBytes : 0u);
+                    mbar_make_up(&bar.full[q % S], announced ? 0u : 1u, !announced && there ? kBBytes + a.a_bytes[1] : 0u,
+                                 announced && !there ? kBBytes + a.a_bytes[1] : 0u);
                 __syncwarp();
                 warp_wait(bar, &bar.full[q % S], (q / S) & 1);
             }
@@ -803,6 +867,12 @@ int check_device(const char *call, const Mat *mats, int n)
     return ZERO1_OK;
 }
 
+// Rows of A's boxes along the contraction.  Where one tile holds all rows, no more of
+// them are loaded than there are (what lies in shared memory beyond is summed into
+// rows that are not stored): with one row of 4096 and 14336 columns of results the
+// boxes of 128 rows took 81 us, ONEROW_FIGURES.
+int a_rows(const Call &c) { return c.M < 128 ? (int)round_up(c.M, 8) : 128; }
+
 // The map of an operand, or of its copy in the workspace.
 int operand_map(const Call &c, const Operand &o, int box_rows, const AlignCopy *copy, CUtensorMap *map)
 {
@@ -836,7 +906,7 @@ int operand_maps(const Call &c, int b_rows, char *scratch, Maps *maps, int sms, 
     }
     for (int k = 0; k < 4; ++k) {
         if (!ops[k]) continue;
-        const int rc = operand_map(c, *ops[k], ops[k]->across ? kDeep : k % 2 ? b_rows : 128, copy[k], to[k]);
+        const int rc = operand_map(c, *ops[k], ops[k]->across ? kDeep : k % 2 ? b_rows : a_rows(c), copy[k], to[k]);
         if (rc != ZERO1_OK) return rc;
     }
     return ZERO1_OK;
@@ -868,6 +938,8 @@ int launch(const Call &c, Mm &a, void *workspace, cudaStream_t st)
     a.second = p.kblocks / 2;
     a.whole = p.whole; a.splits = p.splits; a.per_split = p.per_split;
     a.run = c.run;
+    a.a_bytes[0] = KIND == kWeightGrad ? kABytes : a_rows(c) * kDeep * 2;
+    a.a_bytes[1] = KIND == kWeightGrad || c.M > 128 ? kABytes : 0;
     a.part = static_cast<float *>(workspace);
     a.held = workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + p.held_at) : nullptr;
     int rc;
