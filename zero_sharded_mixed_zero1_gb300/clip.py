@@ -69,9 +69,11 @@ def _unusual(t, what: str):
 
 
 def _ptr(t, dtype, numel: int, what: str) -> int:
-    """_dev, by the short way for a usual tensor."""
-    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.numel() >= numel:
+    """_dev, by the short way for a usual tensor; on the current device, or pinned."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == _get_device() and t.is_contiguous()
+            and t.numel() >= numel):
         return t.data_ptr()
+    _usable(t, what)
     return _dev(t, dtype, numel, what)
 
 

@@ -30,7 +30,8 @@ struct Bwd {
     void *dx, *dy;           // dy may be NULL
     int64_t ld_dh, ld_dr, ld_r, ld_dx, ld_dy;
     int need_w, need_b;
-    float *part;             // [2][blocks][D]: partial column sums (dw, db)
+    float *part;             // [2][blocks][ld_part]: partial column sums (dw, db)
+    int ld_part;             // D rounded up to 8, so that eight columns are two 16-byte stores
 };
 
 // Launch for one pair of types; vec: every row can be read and written in
@@ -475,18 +476,23 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
         flip ^= 1;
         if (++st == stages) st = 0;
     }
-    float *part = a.part + (int64_t)blockIdx.x * a.D;
-    const int64_t plane = (int64_t)gridDim.x * a.D;
+    float *part = a.part + (int64_t)blockIdx.x * a.ld_part;
+    const int64_t plane = (int64_t)gridDim.x * a.ld_part;
+    auto put = [&](float *p, int i, const V8 &v) {
+        if constexpr (LAY == kLanes) {
+            Ld::put(p, i, a.D, v);
+        } else {
+            const float2 x = split(v.p[0]), y = split(v.p[1]), z = split(v.p[2]), w = split(v.p[3]);
+            float4 *q = reinterpret_cast<float4 *>(p + Ld::col(i));
+            q[0] = make_float4(x.x, x.y, y.x, y.y);
+            q[1] = make_float4(z.x, z.y, w.x, w.y);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         if (!in(i)) continue;
-        if constexpr (LAY == kLanes) {
-            if (a.need_w) Ld::put(part, i, a.D, acc_w[i]);
-            if (a.need_b) Ld::put(part + plane, i, a.D, acc_b[i]);
-        } else {
-            if (a.need_w) put8_any(part, Ld::col(i), a.D, acc_w[i]);
-            if (a.need_b) put8_any(part + plane, Ld::col(i), a.D, acc_b[i]);
-        }
+        if (a.need_w) put(part, i, acc_w[i]);
+        if (a.need_b) put(part + plane, i, acc_b[i]);
     }
 }
 
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         if (!(s == 0 ? a.need_w : a.need_b)) continue;
-        float *part = a.part + ((int64_t)s * gridDim.x + blockIdx.x) * a.D;
+        float *part = a.part + ((int64_t)s * gridDim.x + blockIdx.x) * a.ld_part;
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
