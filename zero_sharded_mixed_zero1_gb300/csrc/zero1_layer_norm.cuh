@@ -177,13 +177,26 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // One pass over memory: x and y are read once, through the block norms' ring of
 // shared-memory stages (a thread copies and reads its own columns, so the ring
 // needs no barrier); the row stays in registers for both sums, the second one of
-// squares of differences, so that a large mean costs no bits.  HBM is the bound.
+// squares of differences, so that a large mean costs no bits.  (Summing the differences
+// as well and correcting the mean by them made it worse: sums of bf16 values are nearly
+// exact, those of differences are not.)  HBM is the bound: 8192 x 4096 bf16 with residual
+// and checkpoint 54 us (5.6 TB/s of 9 bytes per element, 0.84 of the measured copy
+// rate), without a checkpoint 47 us (0.87).
 //
+// The forward kernel keeps no column sums and so fits more threads on an SM than the
+// block norms' 512: 1024 where a warp or two hold a row, else 768 (us at 512, 768 and 1024
+// threads, bf16: 131072 x 128 53, 42, 34; 32768 x 768 with an fp32 residual stream 62, 51,
+// 52; 32768 x 1024 63, 56, 56; 8192 x 4096 without residual 35, 26, 25, with it 48, 47,
+// 53), but 512 for rows of 2049 to 4096 columns with residual and checkpoint (53, 54, 62)
+// or off 16-byte boundaries (8191 x 4095 fp32 57, 76, 70).
+template <int T, int MIX, int LAY>
+constexpr int kFwdBlocks = T >= 512 ? 1 : T == 256 ? (MIX == 1 || LAY != kAligned ? 2 : 3) : T >= 128 ? 768 / T : 1024 / T;
+
 // MIX: 1 y and a checkpoint, 2 y and no checkpoint, 3 neither, 0 decided at run
 // time.  FULL: the row has exactly 8 C T columns.
 
 template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
-__global__ void __launch_bounds__(T, kOwnRegs / T)
+__global__ void __launch_bounds__(T, kFwdBlocks<T, MIX, LAY>)
 k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_bytes)
 {
     using Ld = Cols<T, LAY>;
@@ -343,7 +356,10 @@ __global__ void __launch_bounds__(1024) k_layer_norm_fwd(const z1ln::Fwd a)
 //
 // One pass: both means of a row come from one barrier, and a thread keeps the
 // column sums of its own columns over all rows that its block visits; a second
-// kernel adds the blocks' sums in block order.
+// kernel adds the blocks' sums in block order.  8192 x 4096 bf16 from the checkpoint 53
+// us (5.7 TB/s of 9 bytes per element, 0.85 of the measured copy rate), of which the
+// column sums and their joining take 5; with the partial sums stored a word at a time
+// 60.
 //
 // MIX: 1 dr and a checkpoint, 2 dr and the tensor r, 3 no dr and the tensor, 0
 // decided at run time.
@@ -605,17 +621,22 @@ bool ln_fwd_staged(const z1ln::Fwd &a, int sms, cudaStream_t st, int *rc)
     using Ld = Cols<T, LAY>;
     constexpr int N = 8 * C * T, kept = 2 * N * 4;
     const int stage = Ld::template bytes<sizeof(TR)>(N) + (a.y ? Ld::template bytes<sizeof(TA)>(N) : 0);
-    const int stages = stages_that_fit(T, kept, stage);
-    if (stages == 0) return false;
+    int blocks = kFwdBlocks<T, MIX, LAY>, stages = 0;
+    for (;; --blocks) {  // fewer where so many rings do not fit
+        stages = (kSmemPerSm / blocks - 1280 - kept) / stage;
+        if (stages >= 2 || blocks <= kOwnRegs / T) break;
+    }
+    if (stages < 2) return false;
+    stages = stages < 4 ? stages : 4;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(kernel, kSmemPerSm - 1024, done);
     if (e != cudaSuccess) {
         *rc = z1_fail(ZERO1_ECUDA, "layer norm forward: %s", cudaGetErrorString(e));
         return true;
     }
-    const int64_t wave = (int64_t)sms * (kOwnRegs / T), grid = a.rows < wave ? a.rows : wave;
+    const int64_t wave = (int64_t)sms * blocks, grid = a.rows < wave ? a.rows : wave;
     const cudaError_t le = launch_after(kernel, dim3((unsigned)grid), T, kept + stages * stage, st, a, stages, stage);
-    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, kOwnRegs / T, T, 0);
+    z1_note_launch(reinterpret_cast<const void *>(kernel), (int)grid, blocks, T, 0);
     *rc = le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm forward launch");
     return true;
 }
