@@ -25,6 +25,17 @@ using namespace z1mm;
 // memory, along the contraction (h, Wg, Wu, dg) or across it (the weights of
 // kInputGrad, both operands of kWeightGrad); the MMA reads either.
 //
+// What bounds them at large sizes is the rate of the MMAs, under the power limit over
+// seconds: a stage of 64 takes 512 cycles, and as many to bring its 32 KB to each SM
+// from L2.  8192 rows, D 4096, F 14336, in a burst (fraction of the measured cuBLAS bf16
+// rate) and among others in a long loop: forward 930 to 980 us (1.02 to 1.07) and 1093;
+// backward 990 to 1100 (0.91 to 1.01) and 1155; input gradient 970 to 1050 (0.95 to
+// 1.03); a bf16 weight gradient 485 to 517 (0.97 to 1.03), fp32 570 to 625, whose sums
+// are emptied every 2048 rows.  With few rows it is HBM: 64 rows 46 us (5.1 TB/s of the
+// weights), and below that launch, set-up and one round trip of each: 16 rows of 768 x
+// 2048 5.7 us.  At small widths the storing warps bound the backward call: 12981 x 320 x
+// 4096 115 to 122 us where forward takes 60.
+//
 // Roles (12 warps): warp 0 loads, warp 1 of the leading CTA issues the MMAs,
 // warp 2 keeps the tensor memory, warps 4-11 store, each 32 rows and half of the
 // tile's columns.
@@ -332,8 +343,8 @@ __device__ __forceinline__ void load_pair(uint32_t at_g, uint32_t at_u, uint32_t
 }
 
 // da of a warp's 32 rows x 32 columns from row0, col on: four lanes to a row of 64
-// bytes, eight rows at a time (a row to each thread asked for 32 lines at once), zeros
-// outside.  take_da turns that into the thread's own row, by way of a place.
+// bytes, eight rows at a time, zeros outside.  (A row to each thread asked for 32 lines
+// at once: 132 us at 12981 x 320 x 4096 where this takes 113.)  take_da turns that into the thread's own row, by way of a place.
 __device__ __forceinline__ void load_da(const Mm &a, int64_t row0, int64_t col, uint4 (&d)[4])
 {
     const int lane = threadIdx.x & 31;
@@ -665,15 +676,24 @@ __global__ void __launch_bounds__(256) k_gated_ffn_join(const Mm a)
         const int64_t col0 = (int64_t)n * (kDual ? TN / 2 : TN) + slot / 4 % 2 * W + c0;
         __syncthreads();  // what the tile before left has been read
         if (row0 >= a.M || col0 >= a.N) continue;
+        constexpr int kEach = kDual ? 8 : 4;  // columns of a thread, all under way together
+        const float *p = a.part + (((int64_t)t * a.splits * 16 + slot) * kCols + c0 + warp * 4) * 32 + lane;
+        constexpr int kAtOnce = 16 / kEach;   // of as many parts
+        constexpr int64_t kPart = 16 * kCols * 32;
+        float x[kEach] = {};
+        for (int s = 0; s < a.splits; s += kAtOnce, p += kAtOnce * kPart) {
+            float v[kAtOnce][kEach];
 #pragma unroll
-        for (int k = 0; k < (kDual ? 8 : 4); ++k) {
-            const int set = k / 4, c = warp * 4 + k % 4;
-            const float *p = a.part + (((int64_t)t * a.splits * 16 + slot) * kCols + set * W + c0 + c) * 32 + lane;
-            float x = 0.f;
-#pragma unroll 4
-            for (int s = 0; s < a.splits; ++s) x += __ldcg(p + (int64_t)s * 16 * kCols * 32);
-            sum[set][c][lane] = x;
+            for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) v[j][k] = s + j < a.splits ? __ldcg(p + j * kPart + (k / 4 * W + k % 4) * 32) : 0.f;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) x[k] += v[j][k];
         }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) sum[k / 4][warp * 4 + k % 4][lane] = x[k];
         __syncthreads();
         const int64_t col = col0 + lane;
         if (col >= a.N) continue;
@@ -869,8 +889,8 @@ int check_device(const char *call, const Mat *mats, int n)
 
 // Rows of A's boxes along the contraction.  Where one tile holds all rows, no more of
 // them are loaded than there are (what lies in shared memory beyond is summed into
-// rows that are not stored): with one row of 4096 and 14336 columns of results the
-// boxes of 128 rows took 81 us, ONEROW_FIGURES.
+// rows that are not stored): one row of 4096 x 14336 forward takes 45 us, with boxes of
+// 128 rows 81.
 int a_rows(const Call &c) { return c.M < 128 ? (int)round_up(c.M, 8) : 128; }
 
 // The map of an operand, or of its copy in the workspace.

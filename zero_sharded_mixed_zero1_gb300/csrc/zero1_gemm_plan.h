@@ -20,10 +20,16 @@ struct Plan {
 };
 
 // Time of a stage of a 128-column tile against that of a 256-column one: its MMAs
-// take half, but they wait for A's loads.
+// take half, but they wait for A's loads (8192 x 4096 x 14336 in narrow and wide tiles:
+// forward 1253 and 978 us, a weight gradient 643 and 521).  Narrow tiles pay where
+// wide ones leave pairs idle: 64 rows forward 46 and 53 us, 12981 x 320 x 4096 62 and 65,
+// a weight gradient of 1376 x 1000 over 776 rows 6.8 and 8.7.
 constexpr double kNarrow = 0.62;
 constexpr int kEnds = 8;     // an item's start and end, in stages
 constexpr int kLaunch = 10;  // the joining launch, in stages
+// (Split and not: 64 rows x 4096 x 14336, input gradient 48 and 90 us; 12981 x 320 x 4096 71
+// and 80.  With the ends, the parts and the launch taken for nothing: 2048 x 1024 x 4096
+// weight gradient 58 us for 14.)
 
 // The estimated time, in stages of a 256-column tile (0.28 us), of the best way
 // to cut tiles of tn columns; fills the plan.  The pairs of CTAs take the tiles in

@@ -79,8 +79,8 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2 *red)
 // kAligned: eight consecutive ones, in 128-bit accesses; kAnywhere: the same at any
 // element offset, by the words that hold them; kLanes: fp32 rows at any offset
 // without a checkpoint, a thread's columns 16 apart, so that 16 lanes copy and
-// store 64 consecutive bytes (2003 x 1021, backward: 10 us, where words of eight
-// consecutive columns per thread took 17).
+// store 64 consecutive bytes (2003 x 1021, backward: 12 us, where words of eight
+// consecutive columns per thread took 20).
 constexpr int kAnywhere = 0, kAligned = 1, kLanes = 2;
 
 template <int T, int LAY>
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
     let_next_grid_start();
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
         Chunk<TA, VEC> hq[C];
-        Chunk<TR, VEC> rq[C], dq[C];
+        Chunk<TR, VEC> rq[C], dq[SACC ? 1 : C];
         uint2 q8[C];
         int e8[C];
 #pragma unroll
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
             hq[i].load(static_cast<const TA *>(a.dh) + row * a.ld_dh, col, a.D);
             if (a.r8.codes) load_codes<VEC>(a.r8, row, col, a.D, q8[i], e8[i]);
             else rq[i].load(static_cast<const TR *>(a.r) + row * a.ld_r, col, a.D);
-            if (a.dr) dq[i].load(static_cast<const TR *>(a.dr) + row * a.ld_dr, col, a.D);
+            if (!SACC && a.dr) dq[i].load(static_cast<const TR *>(a.dr) + row * a.ld_dr, col, a.D);
         }
         const float mean = a.mean[row], rstd = a.rstd[row];
         float d[C][8], h[C][8], s = 0.f, t = 0.f;
@@ -587,7 +587,8 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
             float r0[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) r0[k] = 0.f;
-            if (a.dr) dq[i].get(r0);
+            if (SACC && a.dr) dq[0].load(static_cast<const TR *>(a.dr) + row * a.ld_dr, col, a.D);  // (registers are short)
+            if (a.dr) dq[SACC ? 0 : i].get(r0);
 #pragma unroll
             for (int k = 0; k < 8; ++k) d[i][k] = fmaf(rstd, fmaf(-h[i][k], t, d[i][k]) - s, r0[k]);
             store_chunk<TR, VEC>(static_cast<TR *>(a.dx) + row * a.ld_dx, col, a.D, d[i]);
