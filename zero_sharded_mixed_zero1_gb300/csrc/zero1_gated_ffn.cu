@@ -888,9 +888,9 @@ int check_device(const char *call, const Mat *mats, int n)
 }
 
 // Rows of A's boxes along the contraction.  Where one tile holds all rows, no more of
-// them are loaded than there are (what lies in shared memory beyond is summed into
-// rows that are not stored): one row of 4096 x 14336 forward takes 45 us, with boxes of
-// 128 rows 81.
+// them are loaded than there are; what lies in shared memory beyond is summed into
+// rows that are not stored.  (One row of 4096 x 14336 forward takes 45 us, with boxes of
+// 128 rows 81.)
 int a_rows(const Call &c) { return c.M < 128 ? (int)round_up(c.M, 8) : 128; }
 
 // The map of an operand, or of its copy in the workspace.
