@@ -863,7 +863,7 @@ int zero1_gated_ffn_input_grad(const zero1_gated_ffn_t *ffn, void *workspace, in
  * dy: device bf16 [rows, n]; x: device bf16 [rows, k]; dw: device [n, k] of
  * out_dtype, for instance a view into a replica's flat gradient buffer at any
  * element offset; accumulate != 0 adds the fp32 sum to it, with one rounding.  The
- * sums are fp32 on the tensor cores, in runs of 2048 rows that are added in fp32
+ * sums are fp32 on the tensor cores, in runs of 512 rows that are added in fp32
  * for an fp32 dw, of 131072 rows for a bf16 one.  Without rows dw gets +0 (or stays,
  * when accumulated into).  Device memory only; dw must not overlap dy or x.  workspace and
  * waits as above (zero1_weight_grad_bf16_workspace bytes). */

@@ -85,12 +85,12 @@ def input_grad(dg, du, w_gate, w_up):
 
 
 def weight_grad(dy, x, dtype, start=None):
-    """dy^T x (+ start) and the bound; fp32 results in runs of 2048 rows, whose
-    sums are added with one rounding each."""
+    """dy^T x (+ start) and the bound; fp32 results in runs of 512 rows, bf16 ones of
+    131072, whose sums are added with one rounding each."""
     y, x = dy.double(), x.double()
     dw, size = y.t() @ x, y.abs().t() @ x.abs()
-    runs = max(1, -(-dy.shape[0] // 2048)) if dtype is torch.float32 else 1
-    e = sum_bound(min(dy.shape[0], 2048) if dtype is torch.float32 else dy.shape[0], size) + runs * 2.0 ** -24 * size
+    run = 512 if dtype is torch.float32 else 131072
+    e = sum_bound(min(dy.shape[0], run), size) + -(-dy.shape[0] // run) * 2.0 ** -24 * size
     if start is not None:
         dw = dw + start.double()
     return dw, e + 1.01 * HALF[dtype] * (dw.abs() + e) + 2.0 ** -133

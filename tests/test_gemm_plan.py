@@ -16,10 +16,9 @@ DRIVER = r"""
 using namespace z1mm;
 int main(int, char **argv)
 {
-    const Plan p = plan_of(atoll(argv[1]), atoll(argv[2]), atoi(argv[3]), 76, atoi(argv[4]));
+    const Plan p = plan_of(atoll(argv[1]), atoll(argv[2]), atoi(argv[3]), 76);
     printf("{\"tn\": %d, \"tiles_m\": %d, \"tiles_n\": %d, \"kblocks\": %d, \"whole\": %d, \"splits\": %d, \"per_split\": %d, "
-           "\"bytes\": %lld, \"held_at\": %lld}", p.tn, p.tiles_m, p.tiles_n, p.kblocks, p.whole, p.splits, p.per_split,
-           (long long)p.bytes, (long long)p.held_at);
+           "\"bytes\": %lld}", p.tn, p.tiles_m, p.tiles_n, p.kblocks, p.whole, p.splits, p.per_split, (long long)p.bytes);
 }
 """
 
@@ -39,9 +38,8 @@ SIZES = [(1, 1, 1), (256, 256, 4), (257, 129, 7), (8192, 28672, 64), (8192, 4096
 
 
 @pytest.mark.parametrize("M,N,kblocks", SIZES)
-@pytest.mark.parametrize("run", [32, 2048])
-def test_tiles_and_parts_cover_everything_once(plan, M, N, kblocks, run):
-    p = plan(M, N, kblocks, run)
+def test_tiles_and_parts_cover_everything_once(plan, M, N, kblocks):
+    p = plan(M, N, kblocks)
     assert p["tn"] in (128, 256)
     assert (p["tiles_m"] - 1) * 256 < M <= p["tiles_m"] * 256
     assert (p["tiles_n"] - 1) * p["tn"] < N <= p["tiles_n"] * p["tn"]
@@ -56,15 +54,12 @@ def test_tiles_and_parts_cover_everything_once(plan, M, N, kblocks, run):
 
 
 @pytest.mark.parametrize("M,N,kblocks", SIZES)
-@pytest.mark.parametrize("run", [32, 2048])
-def test_the_workspace_holds_the_parts_and_the_runs(plan, M, N, kblocks, run):
-    p = plan(M, N, kblocks, run)
-    tile = 256 * p["tn"] * 4
-    parts = (p["tiles_m"] * p["tiles_n"] - p["whole"]) * p["splits"] * tile if p["splits"] > 1 else 0
-    assert p["held_at"] == parts
-    assert p["bytes"] == parts + (76 * tile if p["whole"] and kblocks > run else 0)
+def test_the_workspace_holds_the_parts(plan, M, N, kblocks):
+    p = plan(M, N, kblocks)
+    rest = p["tiles_m"] * p["tiles_n"] - p["whole"]
+    assert p["bytes"] == (rest * p["splits"] * 256 * p["tn"] * 4 if p["splits"] > 1 else 0)
 
 
 def test_nothing_to_contract(plan):
-    p = plan(300, 500, 0, 32)
+    p = plan(300, 500, 0)
     assert p["splits"] == 1 and p["bytes"] == 0

@@ -191,3 +191,63 @@ def test_offsets_beyond_32_bits():
     assert sumsq.item() == 169.0
     z.zero1_grad_clip([big], sumsq, 6.5)
     assert (big[-1].item(), big[1 << 31].item(), big[0].item()) == (1.5, 2.0, 6.0)
+
+
+def test_pinned_host_memory():
+    """Gradients and a residual stream in pinned host memory are read and written
+    where they are; the feed-forward block, which is fed by copies of boxes, refuses
+    them."""
+    t = [normal(5001, seed=1).cpu().pin_memory(), normal(333, seed=2, dtype=F32).cpu().pin_memory(), normal(4096, seed=3)]
+    near = [x.cuda() for x in t]
+    a, b = (torch.empty(1, dtype=F64, device="cuda") for _ in range(2))
+    z.zero1_grad_sumsq(t, a)
+    z.zero1_grad_sumsq(near, b)
+    assert torch.equal(a, b)
+    z.zero1_grad_clip(t, a, 1.0)
+    z.zero1_grad_clip(near, b, 1.0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x.cuda(), y) for x, y in zip(t, near))
+
+    x = normal(40, 200, seed=4)
+    far, out = x.cpu().pin_memory(), torch.empty(40, 200, dtype=BF16).pin_memory()
+    h, stats = torch.empty_like(x), [torch.empty(40, device="cuda") for _ in range(2)]
+    z.zero1_layer_norm_forward(z.LayerNorm(), x, h, *stats)
+    z.zero1_layer_norm_forward(z.LayerNorm(), far, out, *stats)
+    torch.cuda.synchronize()
+    assert torch.equal(out.cuda(), h)
+
+    wg, wu, act = normal(64, 200, seed=5), normal(64, 200, seed=6), torch.empty(40, 64, dtype=BF16, device="cuda")
+    with pytest.raises(z.Zero1Error, match="device memory"):
+        z.zero1_gated_ffn_forward(far, wg, wu, act)
+    with pytest.raises(z.Zero1Error, match="device memory"):
+        z.zero1_weight_grad_bf16(x, far, torch.empty(200, 200, dtype=BF16, device="cuda"))
+
+
+def test_two_host_threads():
+    """Calls from two threads at once, each on its own stream, give what they give alone."""
+    import threading
+    chains = [Chain(*SIZES[k], seed=10 * k) for k in (1, 2)]
+    for c in chains:
+        c.run()
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in c.results()] for c in chains]
+    wrong = []
+
+    def work(k):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    chains[k].run()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong
+    for c, w in zip(chains, want):
+        assert all(torch.equal(a, b) for a, b in zip(c.results(), w))

@@ -30,8 +30,7 @@ using namespace z1mm;
 // from L2.  8192 rows, D 4096, F 14336, in a burst (fraction of the measured cuBLAS bf16
 // rate) and among others in a long loop: forward 930 to 980 us (1.02 to 1.07) and 1093;
 // backward 990 to 1100 (0.91 to 1.01) and 1155; input gradient 970 to 1050 (0.95 to
-// 1.03); a bf16 weight gradient 485 to 517 (0.97 to 1.03), fp32 570 to 625, whose sums
-// are emptied every 2048 rows.  With few rows it is HBM: 64 rows 46 us (5.1 TB/s of the
+// 1.03); a bf16 weight gradient 475 to 520 (0.96 to 1.05), fp32 533 to 582.  With few rows it is HBM: 64 rows 46 us (5.1 TB/s of the
 // weights), and below that launch, set-up and one round trip of each: 16 rows of 768 x
 // 2048 5.7 us.  At small widths the storing warps bound the backward call: 12981 x 320 x
 // 4096 115 to 122 us where forward takes 60.
@@ -86,7 +85,6 @@ struct Mm {
     Out out[3];                       // kForward: a; kBackward: dg, du, a; the others: their gradient
     int out_f32, accumulate;
     float *part;                      // [split tile][part][slot][column][32 lanes]
-    float *held;                      // [CTA][storing warp][column][32 lanes]
 };
 
 __host__ __device__ constexpr bool dual(int kind) { return kind <= kBackward; }
@@ -308,20 +306,26 @@ __device__ __forceinline__ void release(uint64_t *dempty)
     if ((threadIdx.x & 31) == 0) arrive_leader(dempty);
 }
 
-// Sums that wait in the workspace, 32 lanes side by side: stored, or added to.
-// No other thread touches them.
-__device__ __forceinline__ void hold(float *p, bool begin, int columns, uint32_t acc, uint64_t *dempty)
+// Eight accumulator columns of this thread's lane.
+__device__ __forceinline__ void load8_acc(uint32_t addr, uint32_t r[8])
 {
-#pragma unroll 1
-    for (int c = 0; c < columns; c += 16) {
-        uint32_t v[16];
-        tc_load16(acc + c, v);
-        if (c + 16 == columns) release(dempty);
-        float old[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// The sum of a run, put in place of or added to those before it, in registers.
+template <int N>
+__device__ __forceinline__ void take_run(float (&sum)[N], bool begin, uint32_t acc, uint64_t *dempty)
+{
 #pragma unroll
-        for (int j = 0; j < 16; ++j) old[j] = begin ? 0.f : __ldcg(p + (c + j) * 32);
+    for (int c = 0; c < N; c += 8) {
+        uint32_t v[8];
+        load8_acc(acc + c, v);
+        if (c + 8 == N) release(dempty);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) __stcg(p + (c + j) * 32, old[j] + __uint_as_float(v[j]));
+        for (int j = 0; j < 8; ++j) sum[c + j] = (begin ? 0.f : sum[c + j]) + __uint_as_float(v[j]);
     }
 }
 
@@ -344,7 +348,8 @@ __device__ __forceinline__ void load_pair(uint32_t at_g, uint32_t at_u, uint32_t
 
 // da of a warp's 32 rows x 32 columns from row0, col on: four lanes to a row of 64
 // bytes, eight rows at a time, zeros outside.  (A row to each thread asked for 32 lines
-// at once: 132 us at 12981 x 320 x 4096 where this takes 113.)  take_da turns that into the thread's own row, by way of a place.
+// at once: 132 us at 12981 x 320 x 4096 where this takes 113.)  take_da turns that into
+// the thread's own row, by way of a place.
 __device__ __forceinline__ void load_da(const Mm &a, int64_t row0, int64_t col, uint4 (&d)[4])
 {
     const int lane = threadIdx.x & 31;
@@ -385,7 +390,15 @@ struct Maps {
     CUtensorMap a0, a1, b0, b1, out0, out1, out2;
 };
 
-template <int KIND, int TN>
+// RUNS: a contraction of more stages than the accumulator sums at one time; the
+// storing threads add the runs up in registers (128 of them each; tensor memory is read
+// eight columns at a time, so that nothing is spilled).  The tensor cores' truncation is
+// one-sided and grows with the terms of a run: an fp32 weight gradient of normal draws is
+// off by 2.1e-6 of its norm with runs of 2048 rows, 1.0e-6 with 1024, 4.8e-7 with 512,
+// 2.4e-7 with 256 (an fp32 library product 3.9e-7 over 2048 rows, 9.6e-7 over 8192).  512
+// rows it is: 8192 x 4096 x 14336 550 to 570 us, where sums of 2048 rows held in the
+// workspace took 605; 8192 x 1024 x 4096 46 for 53.
+template <int KIND, int TN, bool RUNS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
 {
@@ -506,7 +519,6 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
         const int q = warp % 4, half = (warp - 4) / 4, slot = (int)rank * 8 + half * 4 + q;
         constexpr int kCols = TN / 2, W = TN / 4;  // accumulator columns of a warp; results' columns where it has g and u
         Leaving leaving{s_places + (warp - 4) * kPlaces * kPlaceBytes, 0};
-        float *const held = a.held + ((int64_t)(blockIdx.x / 2) * 16 + slot) * kCols * 32 + lane;
         uint32_t fill = 0;
         bool ok = true;
         uint4 ahead[4];  // kBackward: da of the next 32 columns, on its way while these are computed
@@ -581,29 +593,38 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                 continue;
             }
             const int64_t col0 = (int64_t)w.n * TN + half * kCols;
-            for (int kb = w.kb0; kb < w.kb1; kb += a.run) {
+            float sum[RUNS ? kCols : 1];
+            uint32_t acc = 0;
+            uint64_t *dempty = nullptr;
+            for (int kb = w.kb0; kb < w.kb1; kb += a.run) {  // (without RUNS once)
                 if (!(ok = warp_wait(bar, &bar.dfull[fill & 1], (fill >> 1) & 1))) break;
                 tc_after();
-                uint64_t *dempty = &bar.dempty[fill & 1];
-                const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (fill & 1) * TN + half * kCols;
+                dempty = &bar.dempty[fill & 1];
+                acc = tmem + ((uint32_t)(32 * q) << 16) + (fill & 1) * TN + half * kCols;
                 ++fill;
-                const bool begin = kb == w.kb0, end = kb + a.run >= w.kb1;
-                if (w.part >= 0 || !end) {
-                    hold(w.part >= 0 ? part : held, begin, kCols, acc, dempty);
-                    continue;
-                }
-                if (!a.out_f32 && !a.accumulate && begin) {
-#pragma unroll 1
-                    for (int c = 0; c < kCols; c += 32) {
-                        uint32_t v[32], x[16];
-                        tc_load32(acc + c, v);
-                        if (c + 32 == kCols) release(dempty);
+                if constexpr (RUNS) take_run(sum, kb == w.kb0, acc, dempty);
+            }
+            if (!ok) break;
+            if constexpr (RUNS) {
+                // (registers are not indexed at run time)
+                if (w.part >= 0) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) x[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                        leave_bf16(leaving, a.out[0], &maps.out0, row0, col0 + c, rows, a.N, x);
-                    }
-                    continue;
+                    for (int j = 0; j < kCols; ++j) __stcg(part + j * 32, sum[j]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 16) leave_f32(leaving, a, &maps.out0, row0, col0 + c, rows, sum + c);
                 }
+            } else if (w.part < 0 && !a.out_f32 && !a.accumulate) {
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    uint32_t v[32], x[16];
+                    tc_load32(acc + c, v);
+                    if (c + 32 == kCols) release(dempty);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+                    leave_bf16(leaving, a.out[0], &maps.out0, row0, col0 + c, rows, a.N, x);
+                }
+            } else {
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 16) {
                     uint32_t v[16];
@@ -611,14 +632,17 @@ k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)
                     tc_load16(acc + c, v);
                     if (c + 16 == kCols) release(dempty);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = begin ? 0.f : __ldcg(held + (c + j) * 32);
+                    for (int j = 0; j < 16; ++j) x[j] = __uint_as_float(v[j]);
+                    if (w.part >= 0) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] += __uint_as_float(v[j]);
-                    leave_f32(leaving, a, &maps.out0, row0, col0 + c, rows, x);
+                        for (int j = 0; j < 16; ++j) __stcg(part + (c + j) * 32, x[j]);
+                    } else {
+                        leave_f32(leaving, a, &maps.out0, row0, col0 + c, rows, x);
+                    }
                 }
             }
         }
-        boxes_read();  // the places belong to this block; what is under way to memory is part of the grid
+        boxes_written();  // before the grid counts as done
     }
     __syncwarp();
     __syncthreads();
@@ -858,7 +882,7 @@ int plan_call(Call *c)
     const int64_t N = dual(c->kind) ? 2 * c->N : c->N;
     if ((c->M + 255) / 256 * ((N + 127) / 128) > (1 << 24))
         return z1_fail(ZERO1_ERANGE, "%s: %lld x %lld results: size not supported", c->name, (long long)c->M, (long long)c->N);
-    c->plan = plan_of(c->M, N, (int)stages, sms / 2, c->run);
+    c->plan = plan_of(c->M, N, (int)stages, sms / 2);
     c->bytes = c->plan.bytes;
     for (int k = 0; k < c->na; ++k) c->bytes += copy_bytes(c->a[k]);
     for (int k = 0; k < c->nb; ++k) c->bytes += copy_bytes(c->b[k]);
@@ -948,10 +972,10 @@ Out out_of(const Mat &m, int es)
     return o;
 }
 
-template <int KIND, int TN>
+template <int KIND, int TN, bool RUNS>
 int launch(const Call &c, Mm &a, void *workspace, cudaStream_t st)
 {
-    auto kernel = k_gated_ffn<KIND, TN>;
+    auto kernel = k_gated_ffn<KIND, TN, RUNS>;
     const Plan &p = c.plan;
     a.M = c.M; a.N = c.N;
     a.tiles_m = p.tiles_m; a.tiles_n = p.tiles_n; a.kblocks = p.kblocks;
@@ -961,7 +985,6 @@ int launch(const Call &c, Mm &a, void *workspace, cudaStream_t st)
     a.a_bytes[0] = KIND == kWeightGrad ? kABytes : a_rows(c) * kDeep * 2;
     a.a_bytes[1] = KIND == kWeightGrad || c.M > 128 ? kABytes : 0;
     a.part = static_cast<float *>(workspace);
-    a.held = workspace ? reinterpret_cast<float *>(static_cast<char *>(workspace) + p.held_at) : nullptr;
     int rc;
     if (p.kblocks > 0) {
         Maps maps{};
@@ -994,7 +1017,11 @@ template <int KIND>
 int launch_tile(const Call &c, Mm &a, void *workspace, zero1_stream_t stream)
 {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    return c.plan.tn == 256 ? launch<KIND, 256>(c, a, workspace, st) : launch<KIND, 128>(c, a, workspace, st);
+    if constexpr (!dual(KIND)) {  // (the widths of the others fit one run)
+        if (c.plan.kblocks > c.run)
+            return c.plan.tn == 256 ? launch<KIND, 256, true>(c, a, workspace, st) : launch<KIND, 128, true>(c, a, workspace, st);
+    }
+    return c.plan.tn == 256 ? launch<KIND, 256, false>(c, a, workspace, st) : launch<KIND, 128, false>(c, a, workspace, st);
 }
 
 // ------------------------------------------------- gated feed-forward ------

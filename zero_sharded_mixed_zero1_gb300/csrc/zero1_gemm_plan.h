@@ -8,15 +8,14 @@ namespace z1mm {
 
 constexpr int kTileM = 256;   // rows of a pair of CTAs' tile, 128 each
 constexpr int kDeep = 64;     // of the contraction, per stage
-constexpr int kRunF32 = 32, kRunBf16 = 2048;  // stages that the accumulator sums at one time, for fp32 and bf16 results
+constexpr int kRunF32 = 8, kRunBf16 = 2048;  // stages that the accumulator sums at one time, for fp32 and bf16 results
 
 // M x N results in tiles of kTileM x tn, over `kblocks` stages.  Tiles from
 // `whole` on are split into `splits` parts of per_split stages, whose fp32 sums
 // go through the workspace.
 struct Plan {
     int tn, tiles_m, tiles_n, kblocks, clusters, whole, splits, per_split;
-    int64_t bytes;  // of the parts, then of what whole tiles hold between runs
-    int64_t held_at;
+    int64_t bytes;  // of the parts
 };
 
 // Time of a stage of a 128-column tile against that of a 256-column one: its MMAs
@@ -68,16 +67,14 @@ inline double plan_tiles(Plan *p, int64_t M, int64_t N, int tn, int kblocks, int
     return rounds + best;
 }
 
-// The plan of M x N results over `kblocks` stages.  run: stages that the
-// accumulator sums at one time.
-inline Plan plan_of(int64_t M, int64_t N, int kblocks, int clusters, int run)
+// The plan of M x N results over `kblocks` stages.
+inline Plan plan_of(int64_t M, int64_t N, int kblocks, int clusters)
 {
     Plan wide, narrow;
     const double a = plan_tiles(&wide, M, N, 256, kblocks, clusters), b = plan_tiles(&narrow, M, N, 128, kblocks, clusters);
     Plan p = b < a ? narrow : wide;
-    const int64_t tile = (int64_t)kTileM * p.tn * 4, tiles = (int64_t)p.tiles_m * p.tiles_n;
-    p.held_at = p.splits > 1 ? (tiles - p.whole) * p.splits * tile : 0;
-    p.bytes = p.held_at + (p.whole > 0 && kblocks > run ? clusters * tile : 0);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    p.bytes = p.splits > 1 ? (tiles - p.whole) * p.splits * kTileM * p.tn * 4 : 0;
     return p;
 }
 

@@ -151,13 +151,6 @@ __device__ __forceinline__ void box_out(const CUtensorMap *map, int x, int y, bo
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// All boxes that this warp has sent have been read from shared memory.
-__device__ __forceinline__ void boxes_read()
-{
-    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
-}
-
 // All boxes that this warp has sent are written.
 __device__ __forceinline__ void boxes_written()
 {
