@@ -23,6 +23,10 @@ constexpr int kMinE = 8;      // biased exponents of the scales: 127 - 119 .. 12
 constexpr int kMaxE = 246;
 constexpr int kNanE = 255;
 
+// Lets the next kernel's blocks start as soon as there is room for them; they wait
+// for this grid's end in their own wait_prior_grid().
+__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ------------------------------------------------------- typed elements ----
 
 __device__ __forceinline__ float ld1(const uint16_t *p) { return bf_one(*p); }

@@ -61,10 +61,6 @@ struct Walk {
 // attribute, the wait returns at once.
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Lets the next kernel's blocks start as soon as there is room for them; they wait
-// for this grid's end in their own wait_prior_grid().
-__device__ __forceinline__ void let_next_grid_start() { asm volatile("griddepcontrol.launch_dependents;"); }
-
 template <class K, class... Args>
 cudaError_t launch_pdl(K kernel, int grid, int block, cudaStream_t st, Args... args)
 {
