@@ -165,6 +165,10 @@ __device__ __forceinline__ int items_of(const Mm &a) { return a.whole + (a.tiles
 // storing warp's instructions bound the backward call at small widths).  s (1 - s) is s
 // - s^2 from the rounded s: where s is near but not 1, g k' is at most 140 and a half
 // step of s counts for nothing beside the s that it is added to.
+// From |g| = 1.17e13 on gelu's g k' leaves fp32, where s is 0 or 1 and s - s^2 is 0 to the
+// last bit (both are so from |g| = 16 on): it is cut to a finite value, which 0 makes 0, in
+// one instruction that lets NaN through (12981 x 320 x 4096 120.5 us, without it 119.2; a
+// comparison and a selection took 3% more).
 struct Activated {
     float f, df;
     __device__ __forceinline__ Activated(float g, int gelu)
@@ -174,7 +178,7 @@ struct Activated {
         if (gelu) {
             const float q = __fmul_rn(g, g);
             k = __fmul_rn(g, __fmaf_rn(kB, q, kA));
-            dk = __fmul_rn(g, __fmaf_rn(3.f * kB, q, kA));
+            asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(dk) : "f"(__fmul_rn(g, __fmaf_rn(3.f * kB, q, kA))), "f"(3e38f));
         }
         float e, r;
         asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fminf(__fmul_rn(k, 1.44269504f), 64.f)));
