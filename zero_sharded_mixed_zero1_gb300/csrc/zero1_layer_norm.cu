@@ -124,6 +124,7 @@ extern "C" int zero1_layer_norm_forward(const zero1_layer_norm_t *cfg, const zer
     a.eps = cfg->eps;
     a.alpha = cfg->residual_scale;
     a.inv_d = (float)(1.0 / (double)D);
+    a.inv_d_low = (float)(1.0 / (double)D - (double)a.inv_d);
     a.pf32 = cfg->param_dtype == ZERO1_DTYPE_F32;
     a.x = io->x; a.y = io->y; a.w = io->w; a.b = io->b;
     a.r = io->r; a.h = io->h;

@@ -10,7 +10,7 @@ namespace z1ln {
 struct Fwd {
     int64_t rows;
     int D;
-    float eps, alpha, inv_d;
+    float eps, alpha, inv_d, inv_d_low;  // 1 / D, and what its rounding leaves
     int pf32;                // fp32 weight and bias
     const void *x, *y, *w, *b;  // y, w, b may be NULL
     void *r, *h;             // r NULL without y
@@ -73,6 +73,16 @@ __device__ __forceinline__ float2 block_sum2(float x, float y, float2 *red)
         s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
     }
     return s;
+}
+
+// The mean of a row from its sum: by 1 / D in two parts, as the rounded inverse alone
+// moves the mean of equal values off their value, which 1 / sqrt(eps) then multiplies
+// (100, 1000 times: 2e-3 in h).  (An infinite sum stays one.  A division instead took
+// 7.9 us for 6.9 at 2003 x 1021 fp32.)
+__device__ __forceinline__ float mean_of(float sum, const z1ln::Fwd &a)
+{
+    constexpr float kMost = 3e38f;
+    return __fmaf_rn(sum, a.inv_d, fminf(fmaxf(__fmul_rn(sum, a.inv_d_low), -kMost), kMost));
 }
 
 // How a row's columns are shared out over a block, in chunks of eight per thread.
@@ -177,9 +187,11 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // One pass over memory: x and y are read once, through the block norms' ring of
 // shared-memory stages (a thread copies and reads its own columns, so the ring
 // needs no barrier); the row stays in registers for both sums, the second one of
-// squares of differences, so that a large mean costs no bits.  (Summing the differences
-// as well and correcting the mean by them made it worse: sums of bf16 values are nearly
-// exact, those of differences are not.)  HBM is the bound: 8192 x 4096 bf16 with residual
+// squares of differences, so that the variance does not cancel.  A large mean still costs
+// what its own fp32 sum is rounded by, a few 2^-24 of it in every r - mean, as it does in
+// fp32 rows themselves.  (Summing the differences as well and correcting the mean by them
+// made bf16 rows worse: sums of bf16 values are nearly exact, those of differences are
+// not.)  HBM is the bound: 8192 x 4096 bf16 with residual
 // and checkpoint 54 us (5.6 TB/s of 9 bytes per element, 0.84 of the measured copy
 // rate), without a checkpoint 47 us (0.87).
 //
@@ -248,7 +260,7 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
             }
             s += sum8(v[i]);
         }
-        const float mean = block_sum<T>(s, red[flip][0]) * a.inv_d;
+        const float mean = mean_of(block_sum<T>(s, red[flip][0]), a);
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(1024) k_layer_norm_fwd(const z1ln::Fwd a)
 #pragma unroll
             for (int k = 0; k < 8; ++k) s += f[i][k];
         }
-        const float mean = row_sum(s, red[flip][0]) * a.inv_d;
+        const float mean = mean_of(row_sum(s, red[flip][0]), a);
         s = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i)
