@@ -1251,6 +1251,7 @@ extern "C" int zero1_weight_grad_bf16(const void *dy, int64_t ld_dy, int64_t n, 
     if ((rc = plan_call(&c)) || (rc = check_workspace(c, workspace, workspace_bytes, all, 3)) ||
         (rc = check_device(call, all, 3)))
         return rc;
+    if (rows == 0 && accumulate) return ZERO1_OK;  // (adding 0 would make -0 of dw +0 and change a NaN's bits)
     Mm a{};
     a.out[0] = out_of(all[0], eo);
     a.out_f32 = out_dtype == ZERO1_DTYPE_F32;
