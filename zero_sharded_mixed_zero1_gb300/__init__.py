@@ -81,5 +81,6 @@ from .clip import (  # noqa: E402,F401
     zero1_grad_sumsq,
     zero1_grad_sumsq_workspace,
     zero1_shard_grad_sumsq,
+    zero1_shard_grad_sumsq_workspace,
     zero1_step_clipped,
 )

@@ -7,6 +7,7 @@ as its square, a float64 tensor of one element.
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -16,7 +17,6 @@ from ._lib import AdamW, Plan, _AdamWStruct, _check_rc, _dev, _range, _replicas
 from .block import _CODES, _call_with, _get_device, _launch_stream, _usable
 
 _vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
-SHARD_WORKSPACE = 8 * 2048
 
 _ready = None
 
@@ -133,9 +133,18 @@ def zero1_shard_grad_sumsq(plan: Plan, shard_begin: int, shard_end: int, grads, 
     shard_end), written to sumsq (float64, one element) or added to it.  sums:
     fp32, L elements, keeps the replicas' sums for zero1_step_clipped."""
     _, L, nv = _range(plan, shard_begin, shard_end)
-    _check_rc(_call_with(workspace, SHARD_WORKSPACE, stream, _lib().zero1_shard_grad_sumsq, ctypes.byref(plan), shard_begin,
+    nbytes = zero1_shard_grad_sumsq_workspace() if workspace is None else 0
+    _check_rc(_call_with(workspace, nbytes, stream, _lib().zero1_shard_grad_sumsq, ctypes.byref(plan), shard_begin,
                          shard_end, _grads(plan, grads, nv), ctypes.byref(hp.c_struct()), _ptr(sumsq, _F64, 1, "sumsq"),
                          _scalar(sums, _F32, L, "sums"), 1 if accumulate else 0))
+
+
+@functools.cache
+def zero1_shard_grad_sumsq_workspace() -> int:
+    """Bytes of scratch memory that zero1_shard_grad_sumsq needs, the same for every plan."""
+    out = _i64()
+    _check_rc(_lib().zero1_shard_grad_sumsq_workspace(ctypes.addressof(out)))
+    return out.value
 
 
 def zero1_step_clipped(plan: Plan, shard_begin: int, shard_end: int, grads, master, m, v, params, hp: AdamW,
