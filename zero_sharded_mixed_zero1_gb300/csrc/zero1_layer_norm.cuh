@@ -91,9 +91,10 @@ __device__ __forceinline__ float mean_of(float sum, const z1ln::Fwd &a)
 // without a checkpoint, a thread's columns 16 apart, so that 16 lanes copy and
 // store 64 consecutive bytes (2003 x 1021, backward: 12 us, where words of eight
 // consecutive columns per thread took 20).
-constexpr int kAnywhere = 0, kAligned = 1, kLanes = 2;
+enum class Lay { kAnywhere, kAligned, kLanes };  // (no number: it must not pass for a count or a flag)
+constexpr Lay kAnywhere = Lay::kAnywhere, kAligned = Lay::kAligned, kLanes = Lay::kLanes;
 
-template <int T, int LAY>
+template <int T, Lay LAY>
 struct Cols {
     using Ld = Row<T, LAY == kAligned>;
     static __device__ __forceinline__ int col(int i)
@@ -163,7 +164,7 @@ struct Cols {
 
 // Keeps a [D] vector in shared memory as fp32 values, as keep_vector does and in
 // the columns' layout; `without` where there is none.
-template <int T, int C, int LAY>
+template <int T, int C, Lay LAY>
 __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, int f32, int D, float without)
 {
     if (src && LAY != kLanes) return keep_vector<T, C>(kept, src, f32, D, 0);
@@ -201,13 +202,13 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // 52; 32768 x 1024 63, 56, 56; 8192 x 4096 without residual 35, 26, 25, with it 48, 47,
 // 53), but 512 for rows of 2049 to 4096 columns with residual and checkpoint (53, 54, 62)
 // or off 16-byte boundaries (8191 x 4095 fp32 57, 76, 70).
-template <int T, int MIX, int LAY>
+template <int T, int MIX, Lay LAY>
 constexpr int kFwdBlocks = T >= 512 ? 1 : T == 256 ? (MIX == 1 || LAY != kAligned ? 2 : 3) : T >= 128 ? 768 / T : 1024 / T;
 
 // MIX: 1 y and a checkpoint, 2 y and no checkpoint, 3 neither, 0 decided at run
 // time.  FULL: the row has exactly 8 C T columns.
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, Lay LAY>
 __global__ void __launch_bounds__(T, kFwdBlocks<T, MIX, LAY>)
 k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_bytes)
 {
@@ -410,7 +411,7 @@ struct LnWords {
     }
 };
 
-template <class TA, class TR, int T, int C, int MIX, int LAY>
+template <class TA, class TR, int T, int C, int MIX, Lay LAY>
 struct LnStage {
     using Ld = Cols<T, LAY>;
     static constexpr int n = 8 * C * T;
@@ -420,7 +421,7 @@ struct LnStage {
     static constexpr int bytes = words + T / 32 * words_bytes;
 };
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, Lay LAY>
 __global__ void __launch_bounds__(T, kOwnRegs / T)
 k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
 {
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln
 
 // -------------------------------------------------------------- launch -----
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, Lay LAY>
 bool ln_fwd_staged(const z1ln::Fwd &a, int sms, cudaStream_t st, int *rc)
 {
     auto kernel = k_layer_norm_fwd_staged<TA, TR, T, C, MIX, FULL, LAY>;
@@ -686,7 +687,7 @@ int ln_fwd_direct(const z1ln::Fwd &a, int sms, cudaStream_t st)
     return le == cudaSuccess ? ZERO1_OK : pdl_fail(le, "layer norm forward launch");
 }
 
-template <class TA, class TR, int T, int C, int MIX, bool FULL, int LAY>
+template <class TA, class TR, int T, int C, int MIX, bool FULL, Lay LAY>
 bool ln_bwd_staged(const z1ln::Bwd &a, int64_t grid, cudaStream_t st, int *rc)
 {
     auto kernel = k_layer_norm_bwd_staged<TA, TR, T, C, MIX, FULL, LAY>;
@@ -757,5 +758,5 @@ int z1ln::run_backward(const Bwd &a, bool vec, int64_t grid, cudaStream_t st)
     int rc;
     if (ln_backward_staged<TA, TR>(a, vec, grid, st, &rc)) return rc;
     if (a.D <= 8192) return vec ? ln_bwd_direct<TA, TR, true, false>(a, grid, st) : ln_bwd_direct<TA, TR, false, false>(a, grid, st);
-    return vec ? ln_bwd_direct<TA, TR, true, kAligned>(a, grid, st) : ln_bwd_direct<TA, TR, false, true>(a, grid, st);
+    return vec ? ln_bwd_direct<TA, TR, true, true>(a, grid, st) : ln_bwd_direct<TA, TR, false, true>(a, grid, st);
 }
