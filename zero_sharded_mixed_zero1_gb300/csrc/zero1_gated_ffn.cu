@@ -28,12 +28,16 @@ using namespace z1mm;
 // What bounds them at large sizes is the rate of the MMAs, under the power limit over
 // seconds: a stage of 64 takes 512 cycles, and as many to bring its 32 KB to each SM
 // from L2.  8192 rows, D 4096, F 14336, in a burst (fraction of the measured cuBLAS bf16
-// rate) and among others in a long loop: forward 930 to 980 us (1.02 to 1.07) and 1093;
-// backward 990 to 1100 (0.91 to 1.01) and 1155; input gradient 970 to 1050 (0.95 to
-// 1.03); a bf16 weight gradient 475 to 520 (0.96 to 1.05), fp32 533 to 582.  With few rows it is HBM: 64 rows 46 us (5.1 TB/s of the
-// weights), and below that launch, set-up and one round trip of each: 16 rows of 768 x
-// 2048 5.7 us.  At small widths the storing warps bound the backward call: 12981 x 320 x
-// 4096 115 to 122 us where forward takes 60.
+// rate) and in a long loop, over four GPUs: forward 930 to 1050 us (0.95 to 1.07) and 1090
+// to 1140; backward 1010 to 1220 (0.82 to 0.99) and 1155 to 1200; input gradient 970 to
+// 1160 (0.86 to 1.03) and 1160; a bf16 weight gradient 475 to 600 (0.84 to 1.05) and 570,
+// fp32 533 to 600 and 600.  With few rows it is HBM: 64 rows 46 us (5.1 TB/s of the
+// weights), and below that launch, set-up and one round trip of each: 16 rows of 768 x 2048
+// 5.8 us.  At small widths the storing warps hold the backward call up: 12981 x 320 x 4096
+// 112 to 122 us (gelu 121 to 128) where forward takes 56 to 60 and the bytes 66.  They issue
+// in 46 % of the cycles (gelu 50 %), the tensor pipe works in 24 %: two of them per
+// scheduler, each waiting for the last instruction, for da, for tensor memory and for a
+// place in turn, do not hide one another's waits.
 //
 // Roles (12 warps): warp 0 loads, warp 1 of the leading CTA issues the MMAs,
 // warp 2 keeps the tensor memory, warps 4-11 store, each 32 rows and half of the
@@ -161,8 +165,8 @@ __device__ __forceinline__ int items_of(const Mm &a) { return a.whole + (a.tiles
 // With e = 2^t, t = k log2(e) cut at 64: s = e / (1 + e), right from the subnormal e of
 // very negative k on, and 1 itself from t = 64 on (2^64 and its inverse are exact), in six
 // instructions; its error is that of the product t, |k| half steps, which is nothing to
-// a bf16 result (the logistic function of the gates, good to 2.5 ulps, takes eleven; a
-// storing warp's instructions bound the backward call at small widths).  s (1 - s) is s
+// a bf16 result (the logistic function of the gates, good to 2.5 ulps, takes eleven, and
+// the storing warps hold the backward call up at small widths).  s (1 - s) is s
 // - s^2 from the rounded s: where s is near but not 1, g k' is at most 140 and a half
 // step of s counts for nothing beside the s that it is added to.
 // From |g| = 1.17e13 on gelu's g k' leaves fp32, where s is 0 or 1 and s - s^2 is 0 to the
@@ -395,13 +399,13 @@ struct Maps {
 };
 
 // RUNS: a contraction of more stages than the accumulator sums at one time; the
-// storing threads add the runs up in registers (128 of them each; tensor memory is read
-// eight columns at a time, so that nothing is spilled).  The tensor cores' truncation is
+// storing threads add the runs up in registers (128 of them each, tensor memory read eight
+// columns at a time; of 168 registers two words are spilled).  The tensor cores' truncation is
 // one-sided and grows with the terms of a run: an fp32 weight gradient of normal draws is
 // off by 2.1e-6 of its norm with runs of 2048 rows, 1.0e-6 with 1024, 4.8e-7 with 512,
 // 2.4e-7 with 256 (an fp32 library product 3.9e-7 over 2048 rows, 9.6e-7 over 8192).  512
-// rows it is: 8192 x 4096 x 14336 550 to 570 us, where sums of 2048 rows held in the
-// workspace took 605; 8192 x 1024 x 4096 46 for 53.
+// rows it is: on one GPU 8192 x 4096 x 14336 took 560 us where sums of 2048 rows held in
+// the workspace took 605; 8192 x 1024 x 4096 46 for 53.
 template <int KIND, int TN, bool RUNS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 k_gated_ffn(const __grid_constant__ Maps maps, const Mm a)

@@ -188,9 +188,10 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // One pass over memory: x and y are read once, through the block norms' ring of
 // shared-memory stages (a thread copies and reads its own columns, so the ring
 // needs no barrier); the row stays in registers for both sums, the second one of
-// squares of differences, so that the variance does not cancel.  A large mean still costs
-// what its own fp32 sum is rounded by, a few 2^-24 of it in every r - mean, as it does in
-// fp32 rows themselves.  (Summing the differences as well and correcting the mean by them
+// squares of differences, so that the variance does not cancel.  A large mean costs what
+// its fp32 sum is rounded by, a few 2^-24 of it in every r - mean: h of fp32 rows of mean
+// 1000 and spread 1 is off by 3e-5 of its norm (4096 columns; a plain fp32 form by 3e-5 as
+// well), by 6e-8 with mean 0.  (Summing the differences as well and correcting the mean by them
 // made bf16 rows worse: sums of bf16 values are nearly exact, those of differences are
 // not.)  HBM is the bound: 8192 x 4096 bf16 with residual
 // and checkpoint 54 us (5.6 TB/s of 9 bytes per element, 0.84 of the measured copy
@@ -201,7 +202,10 @@ __device__ __forceinline__ void keep_or(unsigned char *kept, const void *src, in
 // threads, bf16: 131072 x 128 53, 42, 34; 32768 x 768 with an fp32 residual stream 62, 51,
 // 52; 32768 x 1024 63, 56, 56; 8192 x 4096 without residual 35, 26, 25, with it 48, 47,
 // 53), but 512 for rows of 2049 to 4096 columns with residual and checkpoint (53, 54, 62)
-// or off 16-byte boundaries (8191 x 4095 fp32 57, 76, 70).
+// or off 16-byte boundaries (8191 x 4095 fp32 57, 76, 70).  fp32 rows off 16-byte
+// boundaries of up to 1024 columns take 768 (16001 x 1021 33 us at 512, 28); those of 1025
+// to 2048 take them too, although two chunks per thread spill 61 words there (8191 x 2045
+// 30 us at 512, 43): open.
 template <int T, int MIX, Lay LAY>
 constexpr int kFwdBlocks = T >= 512 ? 1 : T == 256 ? (MIX == 1 || LAY != kAligned ? 2 : 3) : T >= 128 ? 768 / T : 1024 / T;
 
@@ -296,7 +300,9 @@ k_layer_norm_fwd_staged(const z1ln::Fwd a, const int stages, const int stage_byt
 }
 
 // The direct kernel, for rows that do not fit the ring (above 8192 columns): a
-// block's threads hold 16 elements of a row each.
+// block's threads hold 16 elements of a row each, and nothing of the next row is under way
+// while its two sums are taken (bf16 with residual and checkpoint, 2048 x 16384 78 us, its
+// bytes 45; 2048 x 12288 65 of 34; fp32 with residual, 2048 x 16384 92 of 80).
 template <class TA, class TR, bool VEC>
 __global__ void __launch_bounds__(1024) k_layer_norm_fwd(const z1ln::Fwd a)
 {
@@ -525,8 +531,12 @@ k_layer_norm_bwd_staged(const z1ln::Bwd a, const int stages)
     }
 }
 
-// The direct kernel, for rows that do not fit the ring; a row of more than 8192
-// columns takes 1024 threads, whose column sums are in shared memory (SACC).
+// The direct kernel, for rows that do not fit the ring: above 8192 columns, and fp32 rows
+// of 1025 to 2048 and of 4097 to 8192, whose two stages, with room for dr, miss a block's
+// share of shared memory by 1024 and by 256 bytes.  A row of more than 8192 columns takes
+// 1024 threads, whose column sums are in shared memory (SACC) and whose 64 registers spill
+// (bf16 30 words, fp32 72).  bf16 from the checkpoint, 2048 x 16384 139 us, its bytes 45;
+// 2048 x 12288 123 of 34; fp32 from r, 8192 x 2048 70 of 50, 4096 x 8192 160 of 100.
 template <class TA, class TR, bool VEC, bool SACC>
 __global__ void __launch_bounds__(SACC ? 1024 : 512) k_layer_norm_bwd(const z1ln::Bwd a)
 {
