@@ -726,8 +726,8 @@ int zero1_grad_sumsq_workspace(const zero1_tensor_t *tensors, int32_t count, int
 int zero1_grad_sumsq(const zero1_tensor_t *tensors, int32_t count, double *sumsq, float *norms, int32_t accumulate,
                      void *workspace, int64_t workspace_bytes, zero1_stream_t stream);
 
-/* Every element times c, rounded once, into `outs` (tensors of the same sizes and
- * types), or in place with outs NULL, where nothing is read or written if c is 1.  Where
+/* Every element times c in fp32, rounded to its type, into `outs` (tensors of the same
+ * sizes and types), or in place with outs NULL, where nothing is read or written if c is 1.  Where
  * *sumsq is not finite, c is 1: the Inf or NaN stays and reaches the step's
  * overflow flag.  norm: device, the norm, or NULL.  max_norm: finite, > 0.  An output
  * may be its own input (same data), and shares no byte with any other tensor of the call. */
@@ -862,7 +862,7 @@ int zero1_gated_ffn_input_grad(const zero1_gated_ffn_t *ffn, void *workspace, in
  *   dw[n, k] (+)= sum_t dy[t, n] * x[t, k]
  * dy: device bf16 [rows, n]; x: device bf16 [rows, k]; dw: device [n, k] of
  * out_dtype, for instance a view into a replica's flat gradient buffer at any
- * element offset; accumulate != 0 adds the fp32 sum to it, with one rounding.  The
+ * element offset; accumulate != 0 adds the fp32 sum to it in fp32 and rounds to its type.  The
  * sums are fp32 on the tensor cores, in runs of 512 rows that are added in fp32
  * for an fp32 dw, of 131072 rows for a bf16 one.  Without rows dw gets +0 (or stays,
  * when accumulated into).  Device memory only; dw must not overlap dy or x.  workspace and
